@@ -309,6 +309,95 @@ int selective_logprob_bwd(const void* hidden, const void* weight, const void* bi
                           void* grad_hidden, float* grad_weight, float* grad_bias, int accumulate,
                           void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Layer norm of rows, forward:
+ *
+ *   mean_i = avg_j x_ij,  rstd_i = 1 / sqrt(avg_j (x_ij - mean_i)^2 + eps)
+ *   y_ij   = (x_ij - mean_i) rstd_i weight_j + bias_j
+ *
+ * and backward, for grad_y = d L / d y, with xhat_ij = (x_ij - mean_i) rstd_i
+ * and g_ij = grad_y_ij weight_j:
+ *
+ *   grad_x_ij     = rstd_i (g_ij - avg_j g_ij - xhat_ij avg_j (g_ij xhat_ij))
+ *   grad_weight_j = sum_i grad_y_ij xhat_ij,   grad_bias_j = sum_i grad_y_ij
+ *
+ * Statistics and sums are float32 (the squared deviations are taken from the
+ * rounded mean, in a second pass over the row in registers); every output is
+ * rounded once.  The reduction over the rows has a fixed order (no atomics),
+ * so repeated calls give equal bits.
+ *
+ * x, y, grad_y, grad_x : (rows, cols) `dtype` (RLPL_F32, RLPL_F16 or RLPL_BF16), dense row-major
+ * weight, bias         : (cols,) `weight_dtype`, which is `dtype` or RLPL_F32; NULL for ones / zeros
+ * mean, rstd           : (rows,) float32; the forward's may be NULL (not wanted)
+ * grad_x               : NULL if not wanted
+ * grad_weight, grad_bias : (cols,) `weight_dtype`, written, or NULL
+ * workspace            : layer_norm_workspace_bytes(rows, cols) bytes, 256-byte
+ *                        aligned, no initial contents needed; one call in flight per workspace
+ *
+ * 1 <= rows < 2^31, 1 <= cols <= 65536.  Pointers aligned to their elements;
+ * 16-byte aligned pointers with a row pitch of a multiple of 16 bytes are read
+ * faster.  y may be x; the backward's outputs must not overlap its inputs.
+ */
+int layer_norm_fwd(const void* x, const void* weight, const void* bias, int64_t rows, int64_t cols, int dtype,
+                   int weight_dtype, float eps, void* y, float* mean_out, float* rstd_out, hipStream_t stream);
+
+size_t layer_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+int layer_norm_bwd(const void* grad_y, const void* x, const void* weight, const float* mean, const float* rstd,
+                   int64_t rows, int64_t cols, int dtype, int weight_dtype, void* grad_x, void* grad_weight,
+                   void* grad_bias, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * AdamW over a list of tensors.  For each element with gradient g (times
+ * *grad_scale where that is given), step t >= 1 and the tensor's weight decay wd:
+ *
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * in float32, each operation rounded once.  The parameters are float32 or 16
+ * bits (rounded to nearest even after the step); float32 ones may have 16-bit
+ * copies, written with the new values.
+ *
+ * Moments are held in float32 (state_bits 32), or (state_bits 8) as e4m3
+ * values with one float32 scale per 256 consecutive elements of a tensor:
+ * exp_avg = m / scale and exp_avg_sq = sqrt(v) / scale, scale = the block's
+ * largest finite magnitude / 448 (0 for a block below 2^-118).  Values are
+ * rounded up with the probability of the part that rounding down would drop,
+ * by 16 random bits hashed from (seed, t, the tensor's place in the list, the
+ * element), so that the same call on the same state gives the same bits; a
+ * root above zero is never rounded to zero.  An element that is not finite
+ * becomes NaN and leaves its block's others as they would be.
+ *
+ * A plan holds what does not change between steps.  rlpl_adamw_plan_build
+ * writes it to host memory (8-byte aligned, rlpl_adamw_plan_bytes bytes); the
+ * caller copies those bytes to device memory (8-byte aligned) and passes both.
+ *
+ * sizes            : elements per tensor, 0 <= size <= 2^40 (host array, as all lists here)
+ * params, copies   : device pointers, one per tensor (copies may be NULL: none; copy_dtype
+ *                    RLPL_F16 or RLPL_BF16, with float32 parameters only)
+ * exp_avg, exp_avg_sq : device pointers: float32, or bytes that hold e4m3 values
+ * exp_avg_scale, exp_avg_sq_scale : (size + 255) / 256 floats per tensor (8 bits), else ignored
+ * weight_decay     : one per tensor, >= 0
+ * grads            : device pointers, read during the call only; NULL leaves its tensor as it is
+ * lr_device, step_device, grad_scale : device scalars (float, int64, float) or NULL; the first two
+ *                    take the place of lr and step, so that a captured call can be replayed with others
+ *
+ * The buffers of a plan must not overlap.  Pointers are aligned to their
+ * elements; tensors whose buffers are all 16-byte aligned go faster.  0 <= beta < 1,
+ * lr, eps >= 0.  A call enqueues one launch per 440 tensors (more for more
+ * than 2^35 elements); calls on one plan must be ordered by the caller's streams.
+ */
+size_t rlpl_adamw_plan_bytes(const int64_t* sizes, int64_t count);
+
+int rlpl_adamw_plan_build(void* plan, size_t plan_bytes, const int64_t* sizes, int64_t count, void* const* params,
+                          int param_dtype, void* const* copies, int copy_dtype, void* const* exp_avg,
+                          void* const* exp_avg_sq, float* const* exp_avg_scale, float* const* exp_avg_sq_scale,
+                          int state_bits, const double* weight_decay);
+
+int rlpl_adamw_step(const void* plan, const void* plan_device, const void* const* grads, int grad_dtype, double lr,
+                    const float* lr_device, double beta1, double beta2, double eps, int64_t step,
+                    const int64_t* step_device, const float* grad_scale, uint32_t seed, hipStream_t stream);
+
 /* bnpo_loss for callers that cannot allocate (code under HIP graph capture,
  * tight serving loops, harnesses that forbid hipMalloc): the same kernels,
  * results bit-identical to bnpo_loss, with no workspace argument.  The

@@ -24,6 +24,11 @@ Entry points (model card "Geometric-AI Kernels": sections "BNPO Loss",
   hidden states and the output projection, on the matrix cores (page "Add SM100
   CuTe DSL GRPO fast path", section "Summary")
 
+* ``layer_norm_fwd(x, weight, bias)`` -> (y, mean, rstd) and ``layer_norm_bwd(grad_y, x, weight, mean, rstd)`` ->
+  (grad_x, grad_weight, grad_bias): the norm in front of the output projection
+* ``adamw_plan(params, ...)`` and ``adamw_step(plan, grads, step=, lr=)``: the update of many tensors at once, with
+  moments in float32 or in 8 bits
+
 Autograd-aware forms (``rl_post_loss_amd.autograd``): ``bnpo_loss_autograd``,
 ``grpo_loss_autograd``, ``reverse_kl_autograd`` and ``reverse_kl_logits_autograd``
 return the loss as a differentiable tensor (torch custom ops over the same
@@ -56,7 +61,8 @@ __all__ = ["bnpo_loss", "bnpo_loss_fwd", "grpo_loss", "grpo_loss_fwd", "reverse_
            "set_wait_limits", "workspace_flags", "check_workspace",
            "launch_shape", "reverse_kl_logits", "reverse_kl_logits_fwd", "bnpo_loss_autograd",
            "grpo_loss_autograd", "reverse_kl_autograd", "reverse_kl_logits_autograd",
-           "selective_logprob_fwd", "selective_logprob_bwd", "selective_logprob_autograd"]
+           "selective_logprob_fwd", "selective_logprob_bwd", "selective_logprob_autograd",
+           "layer_norm_fwd", "layer_norm_bwd", "layer_norm_autograd", "adamw_plan", "adamw_step", "AdamWPlan"]
 
 STATUS = {0: "RLPL_OK", 1: "RLPL_ERR_NULL", 2: "RLPL_ERR_SHAPE", 3: "RLPL_ERR_ALIGN",
           4: "RLPL_ERR_DTYPE", 5: "RLPL_ERR_PARAM", 6: "RLPL_ERR_WORKSPACE", 7: "RLPL_ERR_DEVICE",
@@ -124,6 +130,15 @@ def _declare(lib):
     lib.selective_logprob_fwd.restype = ctypes.c_int
     lib.selective_logprob_bwd.argtypes = lp_common + [vp, vp, i64, i64, i64, i32, vp, vp, vp, i32, vp, sz, vp]
     lib.selective_logprob_bwd.restype = ctypes.c_int
+    lib.layer_norm_fwd.argtypes = [vp, vp, vp, i64, i64, i32, i32, f32, vp, vp, vp, vp]
+    lib.layer_norm_workspace_bytes.argtypes, lib.layer_norm_workspace_bytes.restype = [i64, i64], sz
+    lib.layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, i32, vp, vp, vp, vp, sz, vp]
+    f64 = ctypes.c_double
+    lib.rlpl_adamw_plan_bytes.argtypes, lib.rlpl_adamw_plan_bytes.restype = [vp, i64], sz
+    lib.rlpl_adamw_plan_build.argtypes = [vp, sz, vp, i64, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp]
+    lib.rlpl_adamw_step.argtypes = [vp, vp, vp, i32, f64, vp, f64, f64, f64, i64, vp, vp, ctypes.c_uint32, vp]
+    for name in ("layer_norm_fwd", "layer_norm_bwd", "rlpl_adamw_plan_build", "rlpl_adamw_step"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.rlpl_policy_loss.argtypes = [i32, ctypes.c_uint32] + policy
     lib.rlpl_policy_loss.restype = ctypes.c_int
     lib.rlpl_workspace_bytes.argtypes, lib.rlpl_workspace_bytes.restype = [i64, i64, i32], sz
@@ -498,5 +513,6 @@ def selective_logprob_bwd(hidden, weight, bias, targets, lse, grad_logp, *, need
     return dh, dw, db
 
 
-from .autograd import (bnpo_loss_autograd, grpo_loss_autograd, reverse_kl_autograd,  # noqa: E402
-                       reverse_kl_logits_autograd, selective_logprob_autograd)
+from .training import (AdamWPlan, adamw_plan, adamw_step, layer_norm_bwd, layer_norm_fwd)  # noqa: E402
+from .autograd import (bnpo_loss_autograd, grpo_loss_autograd, layer_norm_autograd,  # noqa: E402
+                       reverse_kl_autograd, reverse_kl_logits_autograd, selective_logprob_autograd)

@@ -20,9 +20,10 @@ from typing import Optional, Tuple
 import torch
 
 from . import _policy, _rkl, _rkl_logits, selective_logprob_bwd, selective_logprob_fwd
+from .training import layer_norm_bwd, layer_norm_fwd
 
 __all__ = ["bnpo_loss_autograd", "grpo_loss_autograd", "reverse_kl_autograd",
-           "reverse_kl_logits_autograd", "selective_logprob_autograd"]
+           "reverse_kl_logits_autograd", "selective_logprob_autograd", "layer_norm_autograd"]
 
 _LIB = "rlpl"
 
@@ -178,3 +179,56 @@ def selective_logprob_autograd(hidden, weight, bias, targets):
     """Per-token target log-probabilities (float32, (n,)) as a differentiable tensor: gradients flow to
     hidden, weight and bias (the weight and bias gradients are formed in float32, then cast to their dtype)."""
     return _selective(hidden, weight, bias, targets)[0]
+
+
+@torch.library.custom_op(f"{_LIB}::layer_norm", mutates_args=())
+def _norm(x: torch.Tensor, weight: Optional[torch.Tensor], bias: Optional[torch.Tensor],
+          eps: float) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    return layer_norm_fwd(x, weight, bias, eps=eps)
+
+
+@_norm.register_fake
+def _(x, weight, bias, eps):
+    stat = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    return x.new_empty(x.shape), stat, torch.empty_like(stat)
+
+
+@torch.library.custom_op(f"{_LIB}::layer_norm_backward", mutates_args=())
+def _norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
+              rstd: torch.Tensor, need_x: bool, need_weight: bool,
+              need_bias: bool) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    out = layer_norm_bwd(grad_y, x, weight, mean, rstd, need_x=need_x, need_weight=need_weight, need_bias=need_bias)
+    return tuple(x.new_empty((0,)) if t is None else t for t in out)
+
+
+@_norm_bwd.register_fake
+def _(grad_y, x, weight, mean, rstd, need_x, need_weight, need_bias):
+    vec = x.new_empty(x.shape[-1:], dtype=x.dtype if weight is None else weight.dtype)
+    none = x.new_empty((0,))
+    return (x.new_empty(x.shape) if need_x else none, vec if need_weight and weight is not None else none.clone(),
+            torch.empty_like(vec) if need_bias else none.clone())
+
+
+def _norm_setup(ctx, inputs, output):
+    x, weight, bias, _ = inputs
+    ctx.bias_dtype = None if bias is None else bias.dtype
+    ctx.save_for_backward(x, weight, output[1], output[2])
+
+
+def _norm_backward(ctx, grad_y, _grad_mean, _grad_rstd):
+    x, weight, mean, rstd = ctx.saved_tensors
+    need_x, need_w = ctx.needs_input_grad[0], weight is not None and ctx.needs_input_grad[1]
+    need_b = ctx.bias_dtype is not None and ctx.needs_input_grad[2]
+    if not (need_x or need_w or need_b):
+        return None, None, None, None
+    dx, dw, db = _norm_bwd(grad_y, x, weight, mean, rstd, need_x, need_w, need_b)
+    return dx if need_x else None, dw if need_w else None, db.to(ctx.bias_dtype) if need_b else None, None
+
+
+_norm.register_autograd(_norm_backward, setup_context=_norm_setup)
+
+
+def layer_norm_autograd(x, weight=None, bias=None, *, eps=1e-5):
+    """Layer norm over the last dimension as a differentiable tensor of x's shape and dtype (gradients flow to x,
+    weight and bias; the saved statistics are float32)."""
+    return _norm(x, weight, bias, float(eps))[0]

@@ -1,0 +1,326 @@
+// C ABI of the operators around the losses (declared in
+// include/rl_post_loss.h): layer norm and the AdamW step.
+//
+// As in abi.cpp, arguments are validated on the host before any HIP call,
+// nothing is allocated and nothing synchronises; kernels go to the caller's
+// stream.
+#include "train_abi.h"
+
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "adamw_kernels.h"
+#include "norm_kernels.h"
+
+namespace {
+
+using namespace rlpl;
+
+constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+
+struct Device {
+    std::once_flag once;
+    int status = RLPL_ERR_DEVICE;
+    int cus = 0;
+};
+Device g_devices[kMaxDevices];
+
+// The current device, checked once: a gfx950 with a known number of compute units.
+int device(const Device** out) {
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
+        (void)hipGetLastError();
+        return RLPL_ERR_DEVICE;
+    }
+    Device& d = g_devices[dev];
+    std::call_once(d.once, [&d, dev] {
+        hipDeviceProp_t prop;
+        if (hipGetDeviceProperties(&prop, dev) != hipSuccess || std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return;
+        if (hipDeviceGetAttribute(&d.cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || d.cus < 1) return;
+        d.status = RLPL_OK;
+    });
+    *out = &d;
+    return d.status;
+}
+
+// ----------------------------------------------------------------------------- layer norm
+
+bool norm_types_ok(int dtype, int wdtype) {
+    return known_dtype(dtype) && known_dtype(wdtype) && (wdtype == dtype || wdtype == RLPL_F32);
+}
+
+bool norm_shape_ok(int64_t rows, int64_t cols) {
+    return rows >= 1 && rows < kMaxRows && cols >= 1 && cols <= kNormMaxCols;
+}
+
+// Rows start on 16 bytes where every pointer does and the pitch is a multiple of 16 bytes.
+bool norm_vector(int64_t cols, int dtype, const void* p0, const void* p1, const void* p2, const void* p3,
+                 const void* p4) {
+    return (size_t(cols) * dtype_bytes(dtype)) % 16 == 0 && is_aligned(p0, 16) && is_aligned(p1, 16) &&
+           is_aligned(p2, 16) && is_aligned(p3, 16) && is_aligned(p4, 16);
+}
+
+// Slabs of rows of the backward pass: about 2048 workgroups, at least 16 rows
+// each (four a wavefront).  The narrow tile of unaligned rows bounds the workspace's size.
+int64_t norm_slabs(int64_t rows, int64_t col_tiles) {
+    int64_t slabs = 2048 / col_tiles;
+    const int64_t most = div_up(rows, 16);
+    if (slabs > most) slabs = most;
+    if (slabs < 1) slabs = 1;
+    const int64_t slab_rows = div_up(rows, slabs);
+    return div_up(rows, slab_rows);
+}
+
+unsigned row_grid(int64_t rows, int per_group) {
+    const int64_t g = div_up(rows, per_group);
+    return unsigned(g < kNormMaxGrid ? g : kNormMaxGrid);
+}
+
+struct NormLayout {
+    size_t sums, part, total;
+};
+NormLayout norm_layout(int64_t rows, int64_t cols) {
+    NormLayout L{};
+    L.sums = up256(size_t(rows) * sizeof(float2));
+    // the widest column tile (512) gives the most slabs
+    L.part = up256(size_t(norm_slabs(rows, div_up(cols, 512))) * 2 * size_t(cols) * sizeof(float));
+    L.total = L.sums + L.part;
+    return L;
+}
+
+// ----------------------------------------------------------------------------- AdamW
+
+constexpr int64_t kAdamMaxTensors = int64_t(1) << 24;
+constexpr int64_t kAdamMaxElements = int64_t(1) << 40;      // of one tensor
+constexpr int64_t kAdamMaxChunks = int64_t(1) << 31;
+constexpr int64_t kAdamLaunchChunks = int64_t(1) << 23;     // workgroups of one launch (x 256 lanes < 2^32)
+
+// Chunks of a list of tensors, or -1 where its sizes cannot be taken.
+int64_t adam_chunks(const int64_t* sizes, int64_t count) {
+    if (!sizes || count < 1 || count > kAdamMaxTensors) return -1;
+    int64_t chunks = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] < 0 || sizes[i] > kAdamMaxElements) return -1;
+        chunks += div_up(sizes[i], kAdamChunk);
+        if (chunks >= kAdamMaxChunks) return -1;
+    }
+    return chunks;
+}
+
+size_t adam_bytes(int64_t count, int64_t chunks) {
+    return sizeof(AdamPlan) + size_t(count) * sizeof(AdamTensor) + size_t(chunks) * sizeof(AdamChunk);
+}
+
+// The murmur3 finalizer, as the kernels' mix32.
+uint32_t mix(uint32_t h) {
+    h ^= h >> 16;
+    h *= 0x85ebca6bu;
+    h ^= h >> 13;
+    h *= 0xc2b2ae35u;
+    return h ^ (h >> 16);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t rlpl_adamw_plan_bytes(const int64_t* sizes, int64_t count) {
+    const int64_t chunks = adam_chunks(sizes, count);
+    return chunks < 0 ? 0 : adam_bytes(count, chunks);
+}
+
+int rlpl_adamw_plan_build(void* plan, size_t plan_bytes, const int64_t* sizes, int64_t count, void* const* params,
+                          int param_dtype, void* const* copies, int copy_dtype, void* const* exp_avg,
+                          void* const* exp_avg_sq, float* const* exp_avg_scale, float* const* exp_avg_sq_scale,
+                          int state_bits, const double* weight_decay) {
+    if (!plan || !sizes || !params || !exp_avg || !exp_avg_sq || !weight_decay) return RLPL_ERR_NULL;
+    if (state_bits != 32 && state_bits != 8) return RLPL_ERR_DTYPE;
+    const bool eight = state_bits == 8;
+    if (eight && (!exp_avg_scale || !exp_avg_sq_scale)) return RLPL_ERR_NULL;
+    const int64_t chunks = adam_chunks(sizes, count);
+    if (chunks < 0) return RLPL_ERR_SHAPE;
+    if (!known_dtype(param_dtype)) return RLPL_ERR_DTYPE;
+    if (copies && (param_dtype != RLPL_F32 || (copy_dtype != RLPL_F16 && copy_dtype != RLPL_BF16))) return RLPL_ERR_DTYPE;
+    if (!is_aligned(plan, 8)) return RLPL_ERR_ALIGN;
+    if (plan_bytes < adam_bytes(count, chunks)) return RLPL_ERR_WORKSPACE;
+    for (int64_t i = 0; i < count; ++i) {
+        if (!std::isfinite(weight_decay[i]) || weight_decay[i] < 0.0) return RLPL_ERR_PARAM;
+        if (sizes[i] == 0) continue;
+        if (!params[i] || !exp_avg[i] || !exp_avg_sq[i] || (copies && !copies[i]) ||
+            (eight && (!exp_avg_scale[i] || !exp_avg_sq_scale[i])))
+            return RLPL_ERR_NULL;
+        const uintptr_t state = eight ? 1 : 4;
+        if (!is_aligned(params[i], dtype_bytes(param_dtype)) || (copies && !is_aligned(copies[i], 2)) ||
+            !is_aligned(exp_avg[i], state) || !is_aligned(exp_avg_sq[i], state) ||
+            (eight && (!is_aligned(exp_avg_scale[i], 4) || !is_aligned(exp_avg_sq_scale[i], 4))))
+            return RLPL_ERR_ALIGN;
+    }
+    AdamPlan h{};
+    h.magic = kAdamMagic;
+    h.count = count;
+    h.chunks = chunks;
+    h.param_dtype = param_dtype;
+    h.copy_dtype = copies ? copy_dtype : -1;
+    h.state_bits = state_bits;
+    h.tensors_at = sizeof(AdamPlan);
+    h.chunks_at = h.tensors_at + uint64_t(count) * sizeof(AdamTensor);
+    h.bytes = adam_bytes(count, chunks);
+    char* out = static_cast<char*>(plan);
+    std::memcpy(out, &h, sizeof(h));
+    auto* tensors = reinterpret_cast<AdamTensor*>(out + h.tensors_at);
+    auto* chunk = reinterpret_cast<AdamChunk*>(out + h.chunks_at);
+    for (int64_t i = 0; i < count; ++i) {
+        AdamTensor t{};
+        t.param = params[i];
+        t.copy = copies ? copies[i] : nullptr;
+        t.m = exp_avg[i];
+        t.v = exp_avg_sq[i];
+        t.m_scale = eight ? exp_avg_scale[i] : nullptr;
+        t.v_scale = eight ? exp_avg_sq_scale[i] : nullptr;
+        t.n = sizes[i];
+        t.weight_decay = weight_decay[i];
+        t.aligned = is_aligned(t.param, 16) && is_aligned(t.copy, 16) && is_aligned(t.m, 16) && is_aligned(t.v, 16);
+        tensors[i] = t;
+        for (int64_t c = 0; c < div_up(sizes[i], kAdamChunk); ++c) *chunk++ = AdamChunk{uint32_t(i), uint32_t(c)};
+    }
+    return RLPL_OK;
+}
+
+int rlpl_adamw_step(const void* plan, const void* plan_device, const void* const* grads, int grad_dtype, double lr,
+                    const float* lr_device, double beta1, double beta2, double eps, int64_t step,
+                    const int64_t* step_device, const float* grad_scale, uint32_t seed, hipStream_t stream) {
+    if (!plan || !plan_device || !grads) return RLPL_ERR_NULL;
+    if (!known_dtype(grad_dtype)) return RLPL_ERR_DTYPE;
+    if (!is_aligned(plan, 8) || !is_aligned(plan_device, 8) || !is_aligned(lr_device, 4) || !is_aligned(step_device, 8) ||
+        !is_aligned(grad_scale, 4))
+        return RLPL_ERR_ALIGN;
+    if (!std::isfinite(lr) || lr < 0.0 || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) ||
+        !std::isfinite(eps) || eps < 0.0 || (!step_device && step < 1))
+        return RLPL_ERR_PARAM;
+    AdamPlan h;
+    std::memcpy(&h, plan, sizeof(h));
+    if (h.magic != kAdamMagic) return RLPL_ERR_PARAM;
+    const auto* tensors = reinterpret_cast<const AdamTensor*>(static_cast<const char*>(plan) + h.tensors_at);
+    for (int64_t i = 0; i < h.count; ++i)
+        if (!is_aligned(grads[i], dtype_bytes(grad_dtype))) return RLPL_ERR_ALIGN;
+    const Device* d = nullptr;
+    const int st = device(&d);
+    if (st != RLPL_OK) return st;
+    const char* dev = static_cast<const char*>(plan_device);
+    AdamArgs a{};
+    a.tensors = reinterpret_cast<const AdamTensor*>(dev + h.tensors_at);
+    a.grad_scale = grad_scale;
+    a.lr_at = lr_device;
+    a.step_at = step_device;
+    a.lr = lr;
+    const double t = step_device ? 1.0 : double(step);
+    a.correction1 = 1.0 - std::pow(beta1, t);
+    a.log_beta1 = std::log(beta1);
+    a.log_beta2 = std::log(beta2);
+    a.root = float(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
+    a.beta1 = float(beta1);
+    a.beta2 = float(beta2);
+    a.one_minus_beta1 = float(1.0 - beta1);
+    a.one_minus_beta2 = float(1.0 - beta2);
+    a.eps = float(eps);
+    a.seed = mix(seed);
+    a.step = uint32_t(step);
+    a.copy_dtype = h.copy_dtype;
+    const void* kernel = pick_adamw(h.param_dtype, grad_dtype, h.state_bits);
+    // Windows of tensors whose gradients' pointers fit the kernel arguments, and within one at
+    // most kAdamLaunchChunks workgroups a launch.
+    const auto* chunk0 = reinterpret_cast<const AdamChunk*>(dev + h.chunks_at);
+    int64_t done = 0;
+    for (int64_t first = 0; first < h.count; first += kAdamWindow) {
+        const int64_t last = first + kAdamWindow < h.count ? first + kAdamWindow : h.count;
+        int64_t chunks = 0;
+        for (int64_t i = first; i < last; ++i) {
+            a.grads[i - first] = grads[i];
+            chunks += div_up(tensors[i].n, kAdamChunk);
+        }
+        a.first = uint32_t(first);
+        while (chunks > 0) {
+            const int64_t now = chunks < kAdamLaunchChunks ? chunks : kAdamLaunchChunks;
+            a.chunks = chunk0 + done;
+            const int s = enqueue(kernel, a, dim3(unsigned(now)), kAdamThreads, stream);
+            if (s != RLPL_OK) return s;
+            done += now;
+            chunks -= now;
+        }
+    }
+    return RLPL_OK;
+}
+
+int layer_norm_fwd(const void* x, const void* weight, const void* bias, int64_t rows, int64_t cols, int dtype,
+                   int weight_dtype, float eps, void* y, float* mean_out, float* rstd_out, hipStream_t stream) {
+    if (!x || !y) return RLPL_ERR_NULL;
+    if (!norm_shape_ok(rows, cols)) return RLPL_ERR_SHAPE;
+    if (!norm_types_ok(dtype, weight_dtype)) return RLPL_ERR_DTYPE;
+    if (!std::isfinite(eps) || eps < 0.0f) return RLPL_ERR_PARAM;
+    const size_t e = dtype_bytes(dtype), we = dtype_bytes(weight_dtype);
+    if (!is_aligned(x, e) || !is_aligned(y, e) || !is_aligned(weight, we) || !is_aligned(bias, we) ||
+        !is_aligned(mean_out, 4) || !is_aligned(rstd_out, 4))
+        return RLPL_ERR_ALIGN;
+    const Device* d = nullptr;
+    const int st = device(&d);
+    if (st != RLPL_OK) return st;
+    const NormFwdKernel k =
+        pick_norm_fwd(dtype, weight_dtype, norm_vector(cols, dtype, x, y, weight, bias, nullptr), cols);
+    if (!k.kernel) return RLPL_ERR_DTYPE;
+    const NormFwdArgs a{x, weight, bias, y, mean_out, rstd_out, rows, int32_t(cols), eps};
+    return enqueue(k.kernel, a, dim3(row_grid(rows, k.rows_per_group)), k.threads, stream);
+}
+
+size_t layer_norm_workspace_bytes(int64_t rows, int64_t cols) {
+    return norm_shape_ok(rows, cols) ? norm_layout(rows, cols).total : 0;
+}
+
+int layer_norm_bwd(const void* grad_y, const void* x, const void* weight, const float* mean, const float* rstd,
+                   int64_t rows, int64_t cols, int dtype, int weight_dtype, void* grad_x, void* grad_weight,
+                   void* grad_bias, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!grad_y || !x || !mean || !rstd) return RLPL_ERR_NULL;
+    if (!norm_shape_ok(rows, cols)) return RLPL_ERR_SHAPE;
+    if (!norm_types_ok(dtype, weight_dtype)) return RLPL_ERR_DTYPE;
+    const size_t e = dtype_bytes(dtype), we = dtype_bytes(weight_dtype);
+    if (!is_aligned(grad_y, e) || !is_aligned(x, e) || !is_aligned(grad_x, e) || !is_aligned(weight, we) ||
+        !is_aligned(grad_weight, we) || !is_aligned(grad_bias, we) || !is_aligned(mean, 4) || !is_aligned(rstd, 4))
+        return RLPL_ERR_ALIGN;
+    const NormLayout L = norm_layout(rows, cols);
+    if (!workspace || workspace_bytes < L.total) return RLPL_ERR_WORKSPACE;
+    if (!is_aligned(workspace, 256)) return RLPL_ERR_ALIGN;
+    const Device* d = nullptr;
+    int st = device(&d);
+    if (st != RLPL_OK) return st;
+    const bool vector = norm_vector(cols, dtype, grad_y, x, grad_x, weight, nullptr);
+    const int64_t col_tiles = div_up(cols, norm_col_tile(dtype, vector));
+    const int64_t slabs = norm_slabs(rows, col_tiles);
+    const bool sums = grad_weight || grad_bias;
+    NormBwdArgs a{};
+    a.dy = grad_y;
+    a.x = x;
+    a.w = weight;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.dx = grad_x;
+    a.row_sums = static_cast<float2*>(workspace);
+    a.part = sums ? reinterpret_cast<float*>(static_cast<char*>(workspace) + L.sums) : nullptr;
+    a.rows = rows;
+    a.slab_rows = div_up(rows, slabs);
+    a.cols = int32_t(cols);
+    if (grad_x) {
+        st = enqueue(pick_norm_row_sums(dtype, weight_dtype, vector), a, dim3(row_grid(rows, kNormThreads / 64)),
+                     kNormThreads, stream);
+        if (st != RLPL_OK) return st;
+    }
+    if (!grad_x && !sums) return RLPL_OK;
+    st = enqueue(pick_norm_bwd(dtype, weight_dtype, vector), a, dim3(unsigned(col_tiles), unsigned(slabs)), kNormThreads,
+                 stream);
+    if (st != RLPL_OK || !sums) return st;
+    const NormReduceArgs r{a.part, grad_weight, grad_bias, int32_t(slabs), int32_t(cols)};
+    return enqueue(pick_norm_reduce(weight_dtype), r, dim3(unsigned(div_up(cols, kNormReduceCols)), 2), kNormThreads,
+                   stream);
+}
+
+}  // extern "C"

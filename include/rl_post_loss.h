@@ -309,6 +309,65 @@ int selective_logprob_bwd(const void* hidden, const void* weight, const void* bi
                           void* grad_hidden, float* grad_weight, float* grad_bias, int accumulate,
                           void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* How linear_cross_entropy joins its rows. */
+enum rlpl_reduction { RLPL_REDUCE_MEAN = 0, RLPL_REDUCE_SUM = 1 };
+
+/*
+ * Softmax cross entropy of an output projection over a large vocabulary, with
+ * its gradients, in pieces of the vocabulary (the supervised sibling of the
+ * selective log-probabilities: the logits are never kept).  Over the rows i
+ * whose target y_i is not ignore_index, N of them,
+ *
+ *   z_i  = hidden[i] . weight^T + bias,   lse_i = log sum_v exp(z_i[v])
+ *   loss = s sum_i (lse_i - z_i[y_i] + z_loss lse_i^2)
+ *
+ * with s = 1 / max(N, 1) (RLPL_REDUCE_MEAN; with N = 0 the loss is 0) or 1
+ * (RLPL_REDUCE_SUM), and
+ *
+ *   dz_i[v]     = s ((1 + 2 z_loss lse_i) exp(z_i[v] - lse_i) - (v == y_i))
+ *   grad_hidden = dz . weight,  grad_weight = dz^T . hidden,  grad_bias = sum_i dz_i
+ *
+ * Ignored rows get a +0 gradient and their hidden states enter no product (so they
+ * may hold anything).  A target that is neither ignore_index nor in [0, vocab)
+ * makes the loss NaN and adds no one-hot term.  A bias of -inf takes its entry out.
+ *
+ * The products run on the matrix cores with `dtype` operands (RLPL_F16 or
+ * RLPL_BF16) and float32 accumulation.  dz is rounded to `dtype` (without s,
+ * in fp16 at 256 times its value, so that |1 + 2 z_loss lse_i| must stay below
+ * 255 there), the operand of the gradients' products; every output is rounded
+ * once.  Each call enqueues several kernels on `stream`; sums have a fixed
+ * order (no atomics), so repeated calls give equal bits.
+ *
+ * hidden      : (n, hidden_size) `dtype`, dense row-major, 16-byte aligned
+ * weight      : (vocab, hidden_size) `dtype`, dense row-major, 16-byte aligned
+ * bias        : (vocab,) `dtype`, or NULL (no bias)
+ * targets     : (n,) int64, 8-byte aligned
+ * loss_out    : 1 float32 (written)
+ * grad_hidden : (n, hidden_size) `dtype`, 16-byte aligned, written; or NULL (not wanted)
+ * grad_weight : (vocab, hidden_size) `weight_grad_dtype`, which is `dtype` (16-byte
+ *               aligned) or RLPL_F32; or NULL
+ * grad_bias   : (vocab,) `weight_grad_dtype`, or NULL (also without a bias)
+ * accumulate  : nonzero adds to grad_weight and grad_bias (RLPL_F32 only), else they are overwritten
+ * workspace   : linear_cross_entropy_workspace_bytes(n, hidden_size, vocab, gradients wanted) bytes,
+ *               256-byte aligned, no initial contents needed; one call in flight
+ *               per workspace.  With gradients it holds one piece of dz: 256 MiB, or 16 KiB a row
+ *               where that is more
+ *
+ * Shapes: 1 <= n <= 2^24, hidden_size a multiple of 8 in [8, 65536], 1 <= vocab < 2^22 and fewer than 2^22
+ * tiles of 256 rows by 256 vocabulary entries; 0 <= z_loss <= 1.
+ */
+size_t linear_cross_entropy_workspace_bytes(int64_t n, int64_t hidden_size, int64_t vocab, int gradients);
+
+int linear_cross_entropy_fwd(const void* hidden, const void* weight, const void* bias, const int64_t* targets, int64_t n,
+                             int64_t hidden_size, int64_t vocab, int dtype, int64_t ignore_index, float z_loss,
+                             int reduction, float* loss_out, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+int linear_cross_entropy(const void* hidden, const void* weight, const void* bias, const int64_t* targets, int64_t n,
+                         int64_t hidden_size, int64_t vocab, int dtype, int64_t ignore_index, float z_loss, int reduction,
+                         float* loss_out, void* grad_hidden, void* grad_weight, void* grad_bias, int weight_grad_dtype,
+                         int accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /*
  * Layer norm of rows, forward:
  *

@@ -23,7 +23,8 @@ Entry points (model card "Geometric-AI Kernels": sections "BNPO Loss",
   (grad_hidden, grad_weight, grad_bias): the policy log-probs from the last
   hidden states and the output projection, on the matrix cores (page "Add SM100
   CuTe DSL GRPO fast path", section "Summary")
-
+* ``linear_cross_entropy(hidden, weight, bias, targets)`` -> (loss, grad_hidden, grad_weight, grad_bias);
+  ``linear_cross_entropy_fwd(...)`` -> loss: the supervised loss of the same projection, in pieces of the vocabulary
 * ``layer_norm_fwd(x, weight, bias)`` -> (y, mean, rstd) and ``layer_norm_bwd(grad_y, x, weight, mean, rstd)`` ->
   (grad_x, grad_weight, grad_bias): the norm in front of the output projection
 * ``adamw_plan(params, ...)`` and ``adamw_step(plan, grads, step=, lr=)``: the update of many tensors at once, with
@@ -62,6 +63,7 @@ __all__ = ["bnpo_loss", "bnpo_loss_fwd", "grpo_loss", "grpo_loss_fwd", "reverse_
            "launch_shape", "reverse_kl_logits", "reverse_kl_logits_fwd", "bnpo_loss_autograd",
            "grpo_loss_autograd", "reverse_kl_autograd", "reverse_kl_logits_autograd",
            "selective_logprob_fwd", "selective_logprob_bwd", "selective_logprob_autograd",
+           "linear_cross_entropy", "linear_cross_entropy_fwd", "linear_cross_entropy_autograd",
            "layer_norm_fwd", "layer_norm_bwd", "layer_norm_autograd", "adamw_plan", "adamw_step", "AdamWPlan"]
 
 STATUS = {0: "RLPL_OK", 1: "RLPL_ERR_NULL", 2: "RLPL_ERR_SHAPE", 3: "RLPL_ERR_ALIGN",
@@ -130,6 +132,10 @@ def _declare(lib):
     lib.selective_logprob_fwd.restype = ctypes.c_int
     lib.selective_logprob_bwd.argtypes = lp_common + [vp, vp, i64, i64, i64, i32, vp, vp, vp, i32, vp, sz, vp]
     lib.selective_logprob_bwd.restype = ctypes.c_int
+    lib.linear_cross_entropy_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.linear_cross_entropy_workspace_bytes.restype = sz
+    lib.linear_cross_entropy_fwd.argtypes = lp_common + [i64, i64, i64, i32, i64, f32, i32, vp, vp, sz, vp]
+    lib.linear_cross_entropy.argtypes = lp_common + [i64, i64, i64, i32, i64, f32, i32, vp, vp, vp, vp, i32, i32, vp, sz, vp]
     lib.layer_norm_fwd.argtypes = [vp, vp, vp, i64, i64, i32, i32, f32, vp, vp, vp, vp]
     lib.layer_norm_workspace_bytes.argtypes, lib.layer_norm_workspace_bytes.restype = [i64, i64], sz
     lib.layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, i32, vp, vp, vp, vp, sz, vp]
@@ -137,7 +143,7 @@ def _declare(lib):
     lib.rlpl_adamw_plan_bytes.argtypes, lib.rlpl_adamw_plan_bytes.restype = [vp, i64], sz
     lib.rlpl_adamw_plan_build.argtypes = [vp, sz, vp, i64, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp]
     lib.rlpl_adamw_step.argtypes = [vp, vp, vp, i32, f64, vp, f64, f64, f64, i64, vp, vp, ctypes.c_uint32, vp]
-    for name in ("layer_norm_fwd", "layer_norm_bwd", "rlpl_adamw_plan_build", "rlpl_adamw_step"):
+    for name in ("linear_cross_entropy_fwd", "linear_cross_entropy", "layer_norm_fwd", "layer_norm_bwd", "rlpl_adamw_plan_build", "rlpl_adamw_step"):
         getattr(lib, name).restype = ctypes.c_int
     lib.rlpl_policy_loss.argtypes = [i32, ctypes.c_uint32] + policy
     lib.rlpl_policy_loss.restype = ctypes.c_int
@@ -513,6 +519,7 @@ def selective_logprob_bwd(hidden, weight, bias, targets, lse, grad_logp, *, need
     return dh, dw, db
 
 
-from .training import (AdamWPlan, adamw_plan, adamw_step, layer_norm_bwd, layer_norm_fwd)  # noqa: E402
+from .training import (AdamWPlan, adamw_plan, adamw_step, layer_norm_bwd, layer_norm_fwd,  # noqa: E402
+                       linear_cross_entropy, linear_cross_entropy_fwd)
 from .autograd import (bnpo_loss_autograd, grpo_loss_autograd, layer_norm_autograd,  # noqa: E402
-                       reverse_kl_autograd, reverse_kl_logits_autograd, selective_logprob_autograd)
+                       linear_cross_entropy_autograd, reverse_kl_autograd, reverse_kl_logits_autograd, selective_logprob_autograd)

@@ -20,10 +20,11 @@ from typing import Optional, Tuple
 import torch
 
 from . import _policy, _rkl, _rkl_logits, selective_logprob_bwd, selective_logprob_fwd
-from .training import layer_norm_bwd, layer_norm_fwd
+from .training import layer_norm_bwd, layer_norm_fwd, linear_cross_entropy, linear_cross_entropy_fwd
 
 __all__ = ["bnpo_loss_autograd", "grpo_loss_autograd", "reverse_kl_autograd",
-           "reverse_kl_logits_autograd", "selective_logprob_autograd", "layer_norm_autograd"]
+           "reverse_kl_logits_autograd", "selective_logprob_autograd", "layer_norm_autograd",
+           "linear_cross_entropy_autograd"]
 
 _LIB = "rlpl"
 
@@ -232,3 +233,44 @@ def layer_norm_autograd(x, weight=None, bias=None, *, eps=1e-5):
     """Layer norm over the last dimension as a differentiable tensor of x's shape and dtype (gradients flow to x,
     weight and bias; the saved statistics are float32)."""
     return _norm(x, weight, bias, float(eps))[0]
+
+
+@torch.library.custom_op(f"{_LIB}::linear_cross_entropy", mutates_args=())
+def _ce(hidden: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], targets: torch.Tensor,
+        ignore_index: int, z_loss: float, reduction: str, need_hidden: bool, need_weight: bool,
+        need_bias: bool) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    loss, *grads = linear_cross_entropy(hidden, weight, bias, targets, ignore_index=ignore_index, z_loss=z_loss,
+                                        reduction=reduction, need_hidden=need_hidden, need_weight=need_weight,
+                                        need_bias=need_bias)
+    return (loss, *(hidden.new_empty((0,)) if g is None else g for g in grads))
+
+
+@_ce.register_fake
+def _(hidden, weight, bias, targets, ignore_index, z_loss, reduction, need_hidden, need_weight, need_bias):
+    none = lambda: hidden.new_empty((0,))  # noqa: E731
+    return (hidden.new_empty((), dtype=torch.float32), hidden.new_empty(hidden.shape) if need_hidden else none(),
+            weight.new_empty(weight.shape) if need_weight else none(),
+            bias.new_empty(bias.shape) if need_bias and bias is not None else none())
+
+
+def _ce_setup(ctx, inputs, output):
+    ctx.save_for_backward(*output[1:])
+    ctx.need = inputs[7:9] + (inputs[9] and inputs[2] is not None,)
+
+
+def _ce_backward(ctx, grad_loss, *_grads_of_grads):
+    grads = [_scaled(g, grad_loss) if need else None for g, need in zip(ctx.saved_tensors, ctx.need)]
+    return (*grads, None, None, None, None, None, None, None)
+
+
+_ce.register_autograd(_ce_backward, setup_context=_ce_setup)
+
+
+def linear_cross_entropy_autograd(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean"):
+    """The loss of ``linear_cross_entropy`` as a differentiable 0-d float32 tensor: gradients flow to hidden, weight and
+    bias.  They are formed with the loss, for the inputs that need one; where none does, the loss alone is."""
+    needs = [t is not None and t.requires_grad and torch.is_grad_enabled() for t in (hidden, weight, bias)]
+    if not any(needs):
+        return linear_cross_entropy_fwd(hidden, weight, bias, targets, ignore_index=ignore_index, z_loss=z_loss,
+                                        reduction=reduction)
+    return _ce(hidden, weight, bias, targets, int(ignore_index), float(z_loss), reduction, *needs)[0]

@@ -1,0 +1,125 @@
+// Internal interface between the C ABI layer (train_abi.cpp) and the
+// vocabulary cross-entropy kernels (ce_kernels.hip).  Not part of the public ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "logprob_kernels.h"
+
+namespace rlpl {
+
+constexpr int kCeThreads = 256;            // workgroups of the row and column kernels
+constexpr int kCeCompactThreads = 1024;
+constexpr int64_t kCeMaxRows = int64_t(1) << 24;
+constexpr int kCeMaxSplits = 16;
+
+// What the compaction leaves on the device: the number of rows that count, and (after
+// the loss) the factor of the gradients: 1 / max(count, 1) or 1, over the scale dz is held at.
+struct CeState {
+    int32_t count;
+    float scale;
+};
+
+// Rows whose target is not ignore_index, in order.
+struct CeCompactArgs {
+    const int64_t* targets;    // (n)
+    int64_t ignore_index, vocab;
+    int32_t n;
+    int32_t* row;              // (n): row of the k-th kept one
+    int32_t* place;            // (n): place of a row among the kept ones, or -1
+    int32_t* target;           // (n): target of the k-th kept row, -1 where it is outside [0, vocab)
+    CeState* state;
+};
+const void* ce_compact_kernel();
+
+// The kept rows of hidden, side by side.
+struct CeGatherArgs {
+    const void* hidden;        // (n, cols) 2-byte elements, cols a multiple of 8
+    void* out;
+    const int32_t* row;
+    const CeState* state;
+    int32_t cols;
+};
+const void* ce_gather_kernel();
+
+// One of the step's four products (the kernel's template argument):
+//   kCeLogits   per row and tile of 256 columns (max, sum exp(z - max)), and the target's logit
+//   kCeDlogits  dz of a piece of the vocabulary, in the operand dtype, scaled by kDzScale
+//   kCeHidden   dz . weight of a piece, into (or added to) float32 planes, one a split of K
+//   kCeWeight   dz^T . hidden of a piece, scaled, in the gradient's dtype
+// with z = hidden . weight^T + bias.  A (M x K) and B (K x N) as in GemmArgs.
+enum { kCeLogits = 0, kCeDlogits = 1, kCeHidden = 2, kCeWeight = 3 };
+
+struct CeGemmArgs {
+    const void* a;
+    const void* b;
+    int64_t lda, ldb;
+    int32_t M, N, K;           // kCeWeight: K, else M, is at most state->count
+    int32_t k_split;           // K range of a split (kCeHidden)
+    uint32_t tiles_m, tiles_n; // of the launch (tiles past the kept rows end at once)
+    const CeState* state;
+    void* c;
+    int64_t ldc;
+    int64_t plane;             // elements between the splits' planes (kCeHidden)
+    int32_t accumulate;        // add to c (kCeHidden, and kCeWeight with a float32 c)
+    int32_t out_f32;           // kCeWeight: c is float32, else the operand dtype
+    const void* bias;          // (N) or NULL
+    const int32_t* target;     // (kept rows)
+    int32_t first;             // vocabulary index of column 0
+    const float* lse;          // (kept rows) (kCeDlogits)
+    float z_loss2;             // 2 z_loss (kCeDlogits)
+    float* part;               // (kept rows, tiles_n, 2) (kCeLogits)
+    float* target_logit;       // (kept rows) (kCeLogits)
+    float* col_part;           // (tiles_m, N) column sums of dz over a tile's rows, or NULL (kCeDlogits)
+};
+const void* pick_ce_gemm(int dtype, int product);
+
+// dz is held at this scale (the onehot's 1), so that small probabilities stay
+// above fp16's subnormals; bf16 has float32's range.
+inline float ce_dz_scale(int dtype) { return dtype == 1 ? 256.0f : 1.0f; }
+
+// A kept row's log-sum-exp and loss.
+struct CeRowArgs {
+    const float* part;
+    const float* target_logit;
+    const int32_t* target;
+    const CeState* state;
+    float* lse;                // (kept rows)
+    float* row_loss;           // (kept rows)
+    float z_loss;
+    int32_t tiles;
+};
+const void* ce_row_kernel();
+
+// The loss from the rows', and the gradients' factor.
+struct CeLossArgs {
+    const float* row_loss;
+    CeState* state;
+    float* loss;
+    float inv_dz_scale;
+    int32_t mean;
+};
+const void* ce_loss_kernel();
+
+// The hidden gradient: the splits' planes of a kept row summed in order and scaled, zeros in an ignored row.
+struct CeHiddenArgs {
+    const float* part;
+    const int32_t* place;
+    const CeState* state;
+    void* out;                 // (n, cols)
+    int64_t plane;
+    int32_t n, cols, splits;
+};
+const void* pick_ce_hidden(int dtype);
+
+// The bias's gradient of a piece: the row tiles' column sums added in order and scaled.
+struct CeBiasArgs {
+    const float* part;         // (tiles, cols)
+    const CeState* state;
+    void* out;                 // (cols) operand dtype or float32
+    int32_t cols, out_f32, accumulate;
+};
+const void* pick_ce_bias(int dtype);
+
+}  // namespace rlpl

@@ -1,5 +1,6 @@
 // C ABI of the operators around the losses (declared in
-// include/rl_post_loss.h): layer norm and the AdamW step.
+// include/rl_post_loss.h): the vocabulary cross
+// entropy, layer norm and the AdamW step.
 //
 // As in abi.cpp, arguments are validated on the host before any HIP call,
 // nothing is allocated and nothing synchronises; kernels go to the caller's
@@ -11,6 +12,7 @@
 #include <mutex>
 
 #include "adamw_kernels.h"
+#include "ce_kernels.h"
 #include "norm_kernels.h"
 
 namespace {
@@ -39,10 +41,218 @@ int device(const Device** out) {
         hipDeviceProp_t prop;
         if (hipGetDeviceProperties(&prop, dev) != hipSuccess || std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return;
         if (hipDeviceGetAttribute(&d.cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || d.cus < 1) return;
+        // the contractions take their LDS ring beyond the default limit
+        for (int dt : {RLPL_F16, RLPL_BF16})
+            for (int product = 0; product < 4; ++product)
+                if (hipFuncSetAttribute(pick_ce_gemm(dt, product), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                        kGemmDynLds) != hipSuccess)
+                    return;
         d.status = RLPL_OK;
     });
     *out = &d;
     return d.status;
+}
+
+// ----------------------------------------------------------------------------- vocabulary cross entropy
+
+constexpr int64_t kCeMaxVocab = int64_t(1) << 22;     // a 256-row panel is addressed with 32-bit offsets
+constexpr int64_t kCeMaxHidden = 65536;
+constexpr int64_t kCeMaxTiles = int64_t(1) << 22;     // workgroups of one launch (x 512 lanes < 2^32)
+// A piece of the vocabulary: kCePieceElements of dz (256 MiB), at least kCePieceCols columns, so that
+// adding a piece's hidden gradient to the float32 planes stays small beside its product.
+constexpr int64_t kCePieceElements = int64_t(1) << 27;
+constexpr int64_t kCePieceCols = 8192;
+
+bool ce_shape_ok(int64_t n, int64_t h, int64_t vocab) {
+    return n >= 1 && n <= kCeMaxRows && h >= 8 && h <= kCeMaxHidden && h % 8 == 0 && vocab >= 1 && vocab < kCeMaxVocab &&
+           div_up(n, kGemmBM) * div_up(vocab, kGemmBN) < kCeMaxTiles &&
+           div_up(n, kGemmBM) * div_up(h, kGemmBN) < kCeMaxTiles;
+}
+
+// Workspace of a call, sized for every row: what the compaction leaves and the kept hidden states, then
+// the loss's tile partials, whose place the gradient's dz, planes and column sums take afterwards.
+struct CeLayout {
+    int64_t piece, pieces, tiles_m, tiles_n, splits, k_split;
+    size_t row, place, target, lse, row_loss, target_logit, hidden, part, dz, planes, cols, total;   // offsets
+};
+CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
+    CeLayout L{};
+    size_t at = 256;   // CeState
+    const auto take = [&at](size_t bytes) {
+        const size_t o = at;
+        at += up256(bytes);
+        return o;
+    };
+    L.tiles_m = div_up(n, kGemmBM);
+    L.tiles_n = div_up(vocab, kGemmBN);
+    for (size_t* p : {&L.row, &L.place, &L.target, &L.lse, &L.row_loss, &L.target_logit}) *p = take(size_t(n) * 4);
+    L.hidden = take(size_t(n) * size_t(h) * 2);
+    L.part = at;
+    const size_t after_loss = at + up256(size_t(n) * size_t(L.tiles_n) * 8);
+    if (grads) {
+        int64_t piece = kCePieceElements / n / kGemmBN * kGemmBN;
+        if (piece < kCePieceCols) piece = kCePieceCols;
+        const int64_t all = L.tiles_n * kGemmBN;
+        L.piece = piece < all ? piece : all;
+        L.pieces = div_up(vocab, L.piece);
+        // enough splits of K that the hidden product has a tile for every compute unit
+        const int64_t tiles = L.tiles_m * div_up(h, kGemmBN);
+        int64_t splits = 256 / tiles;
+        const int64_t most = L.piece / kGemmBN;
+        if (splits > kCeMaxSplits) splits = kCeMaxSplits;
+        if (splits > most) splits = most;
+        if (splits < 1) splits = 1;
+        L.splits = splits;
+        L.k_split = div_up(div_up(L.piece, splits), kGemmBK) * kGemmBK;
+        L.dz = take(size_t(n) * size_t(L.piece) * 2);
+        L.planes = take(size_t(splits) * size_t(n) * size_t(h) * sizeof(float));
+        L.cols = take(size_t(L.tiles_m) * size_t(L.piece) * sizeof(float));
+    }
+    L.total = at > after_loss ? at : after_loss;
+    return L;
+}
+
+unsigned capped(int64_t grid, int64_t cap) { return unsigned(grid < cap ? grid : cap); }
+
+struct CeCall {
+    const void *hidden, *weight, *bias;
+    const int64_t* targets;
+    int64_t n, h, vocab;
+    int dtype;
+    int64_t ignore_index;
+    float z_loss;
+    int reduction;
+    float* loss;
+    void *grad_hidden, *grad_weight, *grad_bias;
+    int weight_grad_dtype, accumulate;
+    void* workspace;
+    size_t workspace_bytes;
+};
+
+int ce_check(const CeCall& c, bool grads) {
+    if (!c.hidden || !c.weight || !c.targets || !c.loss) return RLPL_ERR_NULL;
+    if (!ce_shape_ok(c.n, c.h, c.vocab)) return RLPL_ERR_SHAPE;
+    if (c.dtype != RLPL_F16 && c.dtype != RLPL_BF16) return RLPL_ERR_DTYPE;
+    if (grads && c.weight_grad_dtype != RLPL_F32 && c.weight_grad_dtype != c.dtype) return RLPL_ERR_DTYPE;
+    if (!std::isfinite(c.z_loss) || c.z_loss < 0.0f || c.z_loss > 1.0f) return RLPL_ERR_PARAM;
+    if (c.reduction != RLPL_REDUCE_MEAN && c.reduction != RLPL_REDUCE_SUM) return RLPL_ERR_PARAM;
+    if (grads && c.accumulate && c.weight_grad_dtype != RLPL_F32) return RLPL_ERR_PARAM;
+    const size_t we = grads ? dtype_bytes(c.weight_grad_dtype) : 1;
+    if (!is_aligned(c.hidden, 16) || !is_aligned(c.weight, 16) || !is_aligned(c.bias, 2) || !is_aligned(c.targets, 8) ||
+        !is_aligned(c.loss, 4) || !is_aligned(c.grad_hidden, 16) || !is_aligned(c.grad_weight, we < 4 ? 16 : 4) ||
+        !is_aligned(c.grad_bias, we))
+        return RLPL_ERR_ALIGN;
+    if (!c.workspace || c.workspace_bytes < ce_layout(c.n, c.h, c.vocab, grads).total) return RLPL_ERR_WORKSPACE;
+    return is_aligned(c.workspace, 256) ? RLPL_OK : RLPL_ERR_ALIGN;
+}
+
+int ce_product(int dtype, int product, const CeGemmArgs& g, unsigned splits, hipStream_t stream) {
+    return enqueue(pick_ce_gemm(dtype, product), g, dim3(g.tiles_m * g.tiles_n, 1, splits), kGemmThreads, stream,
+                   kGemmDynLds);
+}
+
+int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
+    int st = ce_check(c, grads);
+    if (st != RLPL_OK) return st;
+    const Device* d = nullptr;
+    if ((st = device(&d)) != RLPL_OK) return st;
+    const CeLayout L = ce_layout(c.n, c.h, c.vocab, grads);
+    char* ws = static_cast<char*>(c.workspace);
+    auto* state = reinterpret_cast<CeState*>(ws);
+    const auto ints = [ws](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
+    const auto floats = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    const float dz_scale = ce_dz_scale(c.dtype);
+
+    const CeCompactArgs compact{c.targets, c.ignore_index, c.vocab, int32_t(c.n), ints(L.row), ints(L.place),
+                                ints(L.target), state};
+    if ((st = enqueue(ce_compact_kernel(), compact, dim3(1), kCeCompactThreads, stream)) != RLPL_OK) return st;
+    const CeGatherArgs gather{c.hidden, ws + L.hidden, ints(L.row), state, int32_t(c.h)};
+    if ((st = enqueue(ce_gather_kernel(), gather, dim3(capped(c.n, 1 << 16)), kCeThreads, stream)) != RLPL_OK) return st;
+
+    CeGemmArgs z{};                    // logits of the whole vocabulary, then of its pieces
+    z.a = ws + L.hidden;
+    z.b = c.weight;
+    z.lda = z.ldb = c.h;
+    z.M = int32_t(c.n);
+    z.N = int32_t(c.vocab);
+    z.K = z.k_split = int32_t(c.h);
+    z.tiles_m = uint32_t(L.tiles_m);
+    z.tiles_n = uint32_t(L.tiles_n);
+    z.state = state;
+    z.bias = c.bias;
+    z.target = ints(L.target);
+    z.part = floats(L.part);
+    z.target_logit = floats(L.target_logit);
+    if ((st = ce_product(c.dtype, kCeLogits, z, 1, stream)) != RLPL_OK) return st;
+    const CeRowArgs rows{floats(L.part), floats(L.target_logit), ints(L.target), state, floats(L.lse),
+                         floats(L.row_loss), c.z_loss, int32_t(L.tiles_n)};
+    if ((st = enqueue(ce_row_kernel(), rows, dim3(capped(c.n, 1 << 16)), kCeThreads, stream)) != RLPL_OK) return st;
+    const CeLossArgs loss{floats(L.row_loss), state, c.loss, 1.0f / dz_scale, c.reduction == RLPL_REDUCE_MEAN ? 1 : 0};
+    if ((st = enqueue(ce_loss_kernel(), loss, dim3(1), kCeCompactThreads, stream)) != RLPL_OK) return st;
+    if (!grads || (!c.grad_hidden && !c.grad_weight && !c.grad_bias)) return RLPL_OK;
+
+    const size_t we = dtype_bytes(c.weight_grad_dtype);
+    const int f32 = c.weight_grad_dtype == RLPL_F32 ? 1 : 0;
+    for (int64_t v0 = 0; v0 < c.vocab; v0 += L.piece) {
+        const int64_t cols = c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece;
+        const char* weight = static_cast<const char*>(c.weight) + size_t(v0) * size_t(c.h) * 2;
+        z.b = weight;
+        z.N = int32_t(cols);
+        z.tiles_n = uint32_t(div_up(cols, kGemmBN));
+        z.bias = c.bias ? static_cast<const char*>(c.bias) + size_t(v0) * 2 : nullptr;
+        z.first = int32_t(v0);
+        z.lse = floats(L.lse);
+        z.z_loss2 = 2.0f * c.z_loss;
+        z.c = ws + L.dz;
+        z.ldc = L.piece;
+        z.col_part = c.grad_bias ? floats(L.cols) : nullptr;
+        if ((st = ce_product(c.dtype, kCeDlogits, z, 1, stream)) != RLPL_OK) return st;
+        if (c.grad_hidden) {
+            CeGemmArgs g{};
+            g.a = ws + L.dz;
+            g.b = weight;
+            g.lda = L.piece;
+            g.ldb = g.ldc = c.h;
+            g.M = int32_t(c.n);
+            g.N = int32_t(c.h);
+            g.K = int32_t(cols);
+            g.k_split = int32_t(L.k_split);
+            g.tiles_m = uint32_t(L.tiles_m);
+            g.tiles_n = uint32_t(div_up(c.h, kGemmBN));
+            g.state = state;
+            g.c = ws + L.planes;
+            g.plane = c.n * c.h;
+            g.accumulate = v0 > 0 ? 1 : 0;
+            if ((st = ce_product(c.dtype, kCeHidden, g, unsigned(L.splits), stream)) != RLPL_OK) return st;
+        }
+        if (c.grad_weight) {
+            CeGemmArgs g{};
+            g.a = ws + L.dz;
+            g.b = ws + L.hidden;
+            g.lda = L.piece;
+            g.ldb = g.ldc = c.h;
+            g.M = int32_t(cols);
+            g.N = int32_t(c.h);
+            g.K = g.k_split = int32_t(c.n);
+            g.tiles_m = uint32_t(div_up(cols, kGemmBM));
+            g.tiles_n = uint32_t(div_up(c.h, kGemmBN));
+            g.state = state;
+            g.c = static_cast<char*>(c.grad_weight) + size_t(v0) * size_t(c.h) * we;
+            g.out_f32 = f32;
+            g.accumulate = c.accumulate ? 1 : 0;
+            if ((st = ce_product(c.dtype, kCeWeight, g, 1, stream)) != RLPL_OK) return st;
+        }
+        if (c.grad_bias) {
+            const CeBiasArgs b{floats(L.cols), state, static_cast<char*>(c.grad_bias) + size_t(v0) * we, int32_t(cols), f32,
+                               c.accumulate ? 1 : 0};
+            st = enqueue(pick_ce_bias(c.dtype), b, dim3(unsigned(div_up(cols, kCeThreads))), kCeThreads, stream);
+            if (st != RLPL_OK) return st;
+        }
+    }
+    if (!c.grad_hidden) return RLPL_OK;
+    const CeHiddenArgs h{floats(L.planes), ints(L.place), state, c.grad_hidden, c.n * c.h, int32_t(c.n), int32_t(c.h),
+                         int32_t(L.splits)};
+    return enqueue(pick_ce_hidden(c.dtype), h, dim3(capped(c.n, 1 << 16)), kCeThreads, stream);
 }
 
 // ----------------------------------------------------------------------------- layer norm
@@ -125,6 +335,28 @@ uint32_t mix(uint32_t h) {
 }  // namespace
 
 extern "C" {
+
+size_t linear_cross_entropy_workspace_bytes(int64_t n, int64_t hidden_size, int64_t vocab, int gradients) {
+    return ce_shape_ok(n, hidden_size, vocab) ? ce_layout(n, hidden_size, vocab, gradients != 0).total : 0;
+}
+
+int linear_cross_entropy_fwd(const void* hidden, const void* weight, const void* bias, const int64_t* targets, int64_t n,
+                             int64_t hidden_size, int64_t vocab, int dtype, int64_t ignore_index, float z_loss,
+                             int reduction, float* loss_out, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+    const CeCall c{hidden, weight, bias, targets, n, hidden_size, vocab, dtype, ignore_index, z_loss, reduction, loss_out,
+                   nullptr, nullptr, nullptr, RLPL_F32, 0, workspace, workspace_bytes};
+    return ce_run(c, false, stream);
+}
+
+int linear_cross_entropy(const void* hidden, const void* weight, const void* bias, const int64_t* targets, int64_t n,
+                         int64_t hidden_size, int64_t vocab, int dtype, int64_t ignore_index, float z_loss, int reduction,
+                         float* loss_out, void* grad_hidden, void* grad_weight, void* grad_bias, int weight_grad_dtype,
+                         int accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const CeCall c{hidden, weight, bias, targets, n, hidden_size, vocab, dtype, ignore_index, z_loss, reduction, loss_out,
+                   grad_hidden, grad_weight, grad_bias, weight_grad_dtype, accumulate, workspace, workspace_bytes};
+    return ce_run(c, true, stream);
+}
 
 size_t rlpl_adamw_plan_bytes(const int64_t* sizes, int64_t count) {
     const int64_t chunks = adam_chunks(sizes, count);

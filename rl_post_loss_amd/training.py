@@ -1,5 +1,7 @@
 """Operators of a training step around the losses, over the same C ABI.
 
+* ``linear_cross_entropy`` / ``linear_cross_entropy_fwd``: the softmax cross entropy of an output projection over a
+  large vocabulary, with the gradients of the hidden states, the projection and its bias;
 * ``layer_norm_fwd`` / ``layer_norm_bwd``: the norm of the hidden states that the output projection reads,
   with the reduction of its weight's and bias's gradients;
 * ``adamw_plan`` / ``adamw_step``: one AdamW step over a list of tensors, moments in float32 or in 8 bits.
@@ -16,9 +18,11 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from . import DTYPE, _check, _ws_ptr, library
+from . import DTYPE, _aligned, _check, _ws_ptr, library
 
-__all__ = ["layer_norm_fwd", "layer_norm_bwd", "adamw_plan", "adamw_step", "AdamWPlan"]
+__all__ = ["linear_cross_entropy", "linear_cross_entropy_fwd", "layer_norm_fwd", "layer_norm_bwd", "adamw_plan", "adamw_step", "AdamWPlan"]
+
+REDUCTION = {"mean": 0, "sum": 1}
 
 BLOCK = 256   # values of an 8-bit moment that share one scale
 
@@ -44,6 +48,92 @@ def _scratch(nbytes: int, workspace: Optional[torch.Tensor], device: torch.devic
     if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
     return workspace
+
+
+# ------------------------------------------------------------------------------------- vocabulary cross entropy
+
+def _ce_operands(hidden, weight, bias, targets, reduction):
+    x, w, b = hidden.detach(), weight.detach(), None
+    for name, t in (("hidden", x), ("weight", w)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if x.dtype not in (torch.float16, torch.bfloat16) or w.dtype != x.dtype:
+        raise TypeError("hidden and weight must share a float16 or bfloat16 dtype")
+    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1] or w.device != x.device:
+        raise ValueError("hidden (*, H) and weight (V, H) must agree in H and device")
+    if bias is not None:
+        b = bias.detach().contiguous()
+        if b.dtype != x.dtype or tuple(b.shape) != (w.shape[0],) or b.device != x.device:
+            raise ValueError(f"bias must be a ({w.shape[0]},) tensor of the operands' dtype and device")
+    y = targets.detach()
+    if y.dtype != torch.int64 or y.shape != x.shape[:-1] or y.device != x.device:
+        raise ValueError(f"targets must be an int64 {tuple(x.shape[:-1])} tensor on the operands' device")
+    if reduction not in REDUCTION:
+        raise ValueError(f"reduction must be one of {sorted(REDUCTION)}")
+    if x.numel() == 0 or w.numel() == 0:
+        _check("linear_cross_entropy", 2)
+    return _aligned(x).view(-1, x.shape[-1]), _aligned(w), b, y.contiguous().view(-1)
+
+
+def linear_cross_entropy_fwd(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean",
+                             workspace=None):
+    """The loss of ``linear_cross_entropy`` (a 0-d float32 tensor, bit-identical), without gradients."""
+    x, w, b, y = _ce_operands(hidden, weight, bias, targets, reduction)
+    (n, H), V, dev, lib = x.shape, w.shape[0], x.device, library()
+    ws = _scratch(lib.linear_cross_entropy_workspace_bytes(n, H, V, 0), workspace, dev,
+                  "linear_cross_entropy_workspace_bytes")
+    wp, wn = _ws_ptr(ws)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    with _on(dev):
+        _check("linear_cross_entropy_fwd", lib.linear_cross_entropy_fwd(
+            x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr(), n, H, V, DTYPE[x.dtype], int(ignore_index), float(z_loss),
+            REDUCTION[reduction], loss.data_ptr(), wp, wn, _stream(dev)))
+    return loss
+
+
+def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean",
+                         need_hidden=True, need_weight=True, need_bias=True, weight_grad_dtype=None, grad_weight=None,
+                         grad_bias=None, workspace=None):
+    """Softmax cross entropy of the logits hidden . weight^T + bias, with its gradients, in pieces of the vocabulary
+    (the logits are never kept): (loss, grad_hidden, grad_weight, grad_bias), None for gradients not wanted and for
+    a bias that is not there.
+
+    hidden (*, H) and weight (V, H) float16 or bfloat16, H a multiple of 8; bias (V,) or None; targets int64, of hidden's
+    leading shape.  Rows whose target is ``ignore_index`` do not count.  loss is the mean (or sum) over the others of
+    lse - z[target] + z_loss * lse^2, a 0-d float32 tensor, and 0 where no row counts.
+
+    weight_grad_dtype: the operands' dtype (the default) or torch.float32, of grad_weight and grad_bias.  Passing
+    ``grad_weight`` / ``grad_bias`` (contiguous float32) adds to them, over groups of tokens or micro-batches."""
+    x, w, b, y = _ce_operands(hidden, weight, bias, targets, reduction)
+    (n, H), V, dev, lib = x.shape, w.shape[0], x.device, library()
+    need_bias = need_bias and b is not None
+    accumulate = grad_weight is not None or grad_bias is not None
+    if accumulate:
+        if weight_grad_dtype not in (None, torch.float32):
+            raise ValueError("gradients are added to in float32")
+        weight_grad_dtype = torch.float32
+        if (need_weight and grad_weight is None) or (need_bias and grad_bias is None):
+            raise ValueError("to accumulate, pass both grad_weight (when wanted) and grad_bias (with a bias)")
+    wdt = x.dtype if weight_grad_dtype is None else weight_grad_dtype
+    if wdt not in (x.dtype, torch.float32):
+        raise TypeError("weight_grad_dtype must be the operands' dtype or float32")
+    for name, t, shape in (("grad_weight", grad_weight, (V, H)), ("grad_bias", grad_bias, (V,))):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()
+                              or t.device != dev):
+            raise ValueError(f"{name} must be a contiguous float32 {shape} tensor on the operands' device")
+    dh = torch.empty_like(x) if need_hidden else None
+    dw = (grad_weight if accumulate else torch.empty((V, H), dtype=wdt, device=dev)) if need_weight else None
+    db = (grad_bias if accumulate else torch.empty(V, dtype=wdt, device=dev)) if need_bias else None
+    ws = _scratch(lib.linear_cross_entropy_workspace_bytes(n, H, V, 1), workspace, dev,
+                  "linear_cross_entropy_workspace_bytes")
+    wp, wn = _ws_ptr(ws)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    with _on(dev):
+        _check("linear_cross_entropy", lib.linear_cross_entropy(
+            x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr(), n, H, V, DTYPE[x.dtype], int(ignore_index), float(z_loss),
+            REDUCTION[reduction], loss.data_ptr(), _ptr(dh), _ptr(dw), _ptr(db), DTYPE[wdt], int(accumulate), wp, wn,
+            _stream(dev)))
+    return loss, None if dh is None else dh.view(hidden.shape), dw, db
 
 
 # ------------------------------------------------------------------------------------------------------- layer norm

@@ -344,8 +344,8 @@ enum rlpl_reduction { RLPL_REDUCE_MEAN = 0, RLPL_REDUCE_SUM = 1 };
  * targets     : (n,) int64, 8-byte aligned
  * loss_out    : 1 float32 (written)
  * grad_hidden : (n, hidden_size) `dtype`, 16-byte aligned, written; or NULL (not wanted)
- * grad_weight : (vocab, hidden_size) `weight_grad_dtype`, which is `dtype` (16-byte
- *               aligned) or RLPL_F32; or NULL
+ * grad_weight : (vocab, hidden_size) `weight_grad_dtype`, which is `dtype` or RLPL_F32, 16-byte
+ *               aligned; or NULL
  * grad_bias   : (vocab,) `weight_grad_dtype`, or NULL (also without a bias)
  * accumulate  : nonzero adds to grad_weight and grad_bias (RLPL_F32 only), else they are overwritten
  * workspace   : linear_cross_entropy_workspace_bytes(n, hidden_size, vocab, gradients wanted) bytes,
@@ -354,7 +354,7 @@ enum rlpl_reduction { RLPL_REDUCE_MEAN = 0, RLPL_REDUCE_SUM = 1 };
  *               where that is more
  *
  * Shapes: 1 <= n <= 2^24, hidden_size a multiple of 8 in [8, 65536], 1 <= vocab < 2^22 and fewer than 2^22
- * tiles of 256 rows by 256 vocabulary entries; 0 <= z_loss <= 1.
+ * tiles of 256 rows by 256 vocabulary entries, 2^18 of 256 rows by 256 hidden values; 0 <= z_loss <= 1.
  */
 size_t linear_cross_entropy_workspace_bytes(int64_t n, int64_t hidden_size, int64_t vocab, int gradients);
 

@@ -11,6 +11,7 @@ namespace rlpl {
 
 constexpr int kCeThreads = 256;            // workgroups of the row and column kernels
 constexpr int kCeCompactThreads = 1024;
+constexpr int kCeDynLds = 160 * 1024;      // the products' LDS ring: all of a compute unit's
 constexpr int64_t kCeMaxRows = int64_t(1) << 24;
 constexpr int kCeMaxSplits = 16;
 
@@ -51,17 +52,42 @@ const void* ce_gather_kernel();
 // with z = hidden . weight^T + bias.  A (M x K) and B (K x N) as in GemmArgs.
 enum { kCeLogits = 0, kCeDlogits = 1, kCeHidden = 2, kCeWeight = 3 };
 
+// Splits of the hidden product's K: the number, at most `most`, that takes the least time where 256 workgroups run
+// at once and each costs its K steps and about 12 more (first copies, and its part of the planes).  A piece's
+// tiles number as few as the rows that count allow, which the device alone knows, so both sides ask here.
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+inline uint32_t ce_splits(uint32_t tiles_m, uint32_t tiles_n, int32_t split_k, int32_t most) {
+    const uint32_t tiles = tiles_m * tiles_n, steps = uint32_t(split_k + kGemmBK - 1) / kGemmBK;
+    uint32_t best = 1, least = 0xFFFFFFFFu;
+    for (uint32_t s = 1; s <= uint32_t(most); ++s) {
+        const uint32_t time = (tiles * s + 255) / 256 * ((steps + s - 1) / s + 12);
+        if (time < least) {
+            least = time;
+            best = s;
+        }
+    }
+    return best;
+}
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+inline int32_t ce_k_split(int32_t split_k, uint32_t splits) {
+    const int32_t steps = (split_k + kGemmBK - 1) / kGemmBK;
+    return (steps + int32_t(splits) - 1) / int32_t(splits) * kGemmBK;
+}
+
 struct CeGemmArgs {
     const void* a;
     const void* b;
     int64_t lda, ldb;
     int32_t M, N, K;           // kCeWeight: K, else M, is at most state->count
-    int32_t k_split;           // K range of a split (kCeHidden)
+    int32_t split_k, max_splits;   // the longest piece's K, and the planes there is room for (kCeHidden; ce_splits)
     uint32_t tiles_m, tiles_n; // of the launch (tiles past the kept rows end at once)
     const CeState* state;
     void* c;
     int64_t ldc;
-    int64_t plane;             // elements between the splits' planes (kCeHidden)
     int32_t accumulate;        // add to c (kCeHidden, and kCeWeight with a float32 c)
     int32_t out_f32;           // kCeWeight: c is float32, else the operand dtype
     const void* bias;          // (N) or NULL
@@ -108,8 +134,7 @@ struct CeHiddenArgs {
     const int32_t* place;
     const CeState* state;
     void* out;                 // (n, cols)
-    int64_t plane;
-    int32_t n, cols, splits;
+    int32_t n, cols, split_k, max_splits;
 };
 const void* pick_ce_hidden(int dtype);
 

@@ -27,6 +27,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ce_kernels.h"
 #include "device_common.h"
 #include "loss_kernels.h"
@@ -39,6 +41,175 @@ namespace {
 
 template <typename T> constexpr float kDzScale = 1.0f;
 template <> constexpr float kDzScale<_Float16> = 256.0f;
+
+// A wavefront's 128 x 64 block as 8 x 4 tiles of v_mfma_f32_16x16x32: at random operands, which hold the
+// chip to its power, it reaches 2.04 PFLOP/s from registers against 1.82 for 32x32x16 (a loop of
+// matrix instructions alone), at 2.05 against 1.80 GHz.
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+constexpr int kRowTiles = kWaveM / 16, kColTiles = kWaveN / 16;
+
+template <typename T>
+__device__ __forceinline__ floatx4 mfma16(uint4 a, uint4 b, floatx4 c) {
+    if constexpr (sizeof(T) == 2 && std::is_same_v<T, __bf16>)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                       0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+// Stages as in mfma_tile.h, but for the MN-contiguous operand's swizzle: a pass of 32 lanes reads 16
+// columns of K rows k .. k + 3 and k + 8 .. k + 11, which bits 1 and 3 of k spread over all banks.
+struct CeStage : Stage<kGemmBK> {
+    static __device__ __forceinline__ int mn_swizzle(int k) { return (((k >> 1) & 1) << 2) | (((k >> 3) & 1) << 1); }
+    static __device__ __forceinline__ int mn_offset(int k, int r) {
+        return (r >> 6) * (128 * kGemmBK) + k * 128 + 16 * (((r & 63) >> 3) ^ mn_swizzle(k)) + 2 * (r & 7);
+    }
+};
+
+// The fragments are read by asm statements that wait for their own reads: for a load or a builtin the compiler
+// would add a wait for every copy into LDS in flight.
+
+// Fragments of a K-contiguous stage tile: lane l's eight K values 32 half + 8 (l / 16) .. + 8 of row l % 16 of
+// 16-row tiles, 2048 bytes apart.  k_base is the lane's place for the first of them.
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+    return uint32_t(uintptr_t((const __attribute__((address_space(3))) char*)p));
+}
+__device__ __forceinline__ uint32_t k_base(const char* t, int first, int half, int lane) {
+    return lds_address(t + CeStage::kc_offset(first + (lane & 15), half * 4 + (lane >> 4)));
+}
+// Four tiles from each of two places.
+__device__ __forceinline__ void fragments_k(uint32_t at0, uint32_t at1, uint4 (&x)[4], uint4 (&y)[4]) {
+    u32x4 v[8];
+    asm volatile(
+        "ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:2048\n\t"
+        "ds_read_b128 %2, %8 offset:4096\n\tds_read_b128 %3, %8 offset:6144\n\t"
+        "ds_read_b128 %4, %9\n\tds_read_b128 %5, %9 offset:2048\n\t"
+        "ds_read_b128 %6, %9 offset:4096\n\tds_read_b128 %7, %9 offset:6144\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+        : "v"(at0), "v"(at1)
+        : "memory");
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        x[c] = __builtin_bit_cast(uint4, v[c]);
+        y[c] = __builtin_bit_cast(uint4, v[4 + c]);
+    }
+}
+// From each of four places.
+__device__ __forceinline__ void fragments_k(uint32_t at0, uint32_t at1, uint32_t at2, uint32_t at3, uint4 (&x)[4],
+                                            uint4 (&y)[4], uint4 (&z)[4], uint4 (&w)[4]) {
+    u32x4 v[16];
+    asm volatile(
+        "ds_read_b128 %0, %16\n\tds_read_b128 %1, %16 offset:2048\n\t"
+        "ds_read_b128 %2, %16 offset:4096\n\tds_read_b128 %3, %16 offset:6144\n\t"
+        "ds_read_b128 %4, %17\n\tds_read_b128 %5, %17 offset:2048\n\t"
+        "ds_read_b128 %6, %17 offset:4096\n\tds_read_b128 %7, %17 offset:6144\n\t"
+        "ds_read_b128 %8, %18\n\tds_read_b128 %9, %18 offset:2048\n\t"
+        "ds_read_b128 %10, %18 offset:4096\n\tds_read_b128 %11, %18 offset:6144\n\t"
+        "ds_read_b128 %12, %19\n\tds_read_b128 %13, %19 offset:2048\n\t"
+        "ds_read_b128 %14, %19 offset:4096\n\tds_read_b128 %15, %19 offset:6144\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7]),
+          "=&v"(v[8]), "=&v"(v[9]), "=&v"(v[10]), "=&v"(v[11]), "=&v"(v[12]), "=&v"(v[13]), "=&v"(v[14]), "=&v"(v[15])
+        : "v"(at0), "v"(at1), "v"(at2), "v"(at3)
+        : "memory");
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        x[c] = __builtin_bit_cast(uint4, v[c]);
+        y[c] = __builtin_bit_cast(uint4, v[4 + c]);
+        z[c] = __builtin_bit_cast(uint4, v[8 + c]);
+        w[c] = __builtin_bit_cast(uint4, v[12 + c]);
+    }
+}
+
+// Fragments of an MN-contiguous stage tile, by transposing reads: in a group of 16 lanes, lane q = 4j + c
+// points at K row j, columns 4c .. 4c + 3, and lane i gets the four K rows of column i.  `mn_base` is the
+// lane's place for the 16 columns 16 c (c < 4) of a block of 64; the eight fragments are those columns at
+// byte offsets FIRST and SECOND (blocks are 8192 bytes apart, halves of K 4096).
+__device__ __forceinline__ uint32_t mn_base(const char* t, int c, int lane) {
+    const int q = lane & 15, r = 16 * c + 4 * (q & 3), k = 8 * (lane >> 4) + (q >> 2);
+    return lds_address(t + CeStage::mn_offset(k, r));
+}
+template <int FIRST, int SECOND>
+__device__ __forceinline__ void fragments_mn(const uint32_t (&at)[4], uint4 (&first)[4], uint4 (&second)[4]) {
+    uint2 v[16];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %16 offset:%20\n\tds_read_b64_tr_b16 %1, %16 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %2, %17 offset:%20\n\tds_read_b64_tr_b16 %3, %17 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %4, %18 offset:%20\n\tds_read_b64_tr_b16 %5, %18 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %6, %19 offset:%20\n\tds_read_b64_tr_b16 %7, %19 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %8, %16 offset:%22\n\tds_read_b64_tr_b16 %9, %16 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %10, %17 offset:%22\n\tds_read_b64_tr_b16 %11, %17 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %12, %18 offset:%22\n\tds_read_b64_tr_b16 %13, %18 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %14, %19 offset:%22\n\tds_read_b64_tr_b16 %15, %19 offset:%23\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7]),
+          "=&v"(v[8]), "=&v"(v[9]), "=&v"(v[10]), "=&v"(v[11]), "=&v"(v[12]), "=&v"(v[13]), "=&v"(v[14]), "=&v"(v[15])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "n"(FIRST), "n"(FIRST + 512), "n"(SECOND), "n"(SECOND + 512)
+        : "memory");
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        first[c] = make_uint4(v[2 * c].x, v[2 * c].y, v[2 * c + 1].x, v[2 * c + 1].y);
+        second[c] = make_uint4(v[8 + 2 * c].x, v[8 + 2 * c].y, v[9 + 2 * c].x, v[9 + 2 * c].y);
+    }
+}
+
+// The ring: three slots of the A operand's stages and two of the B operand's, all of a compute unit's LDS.
+constexpr int kSlotsA = 3, kSlotsB = 2;
+constexpr int kCopies = CeStage::kDmaA;    // 1 KB copies of a wavefront per operand and stage
+static_assert(CeStage::kDmaA == CeStage::kDmaB && kGemmWavesM == 2, "two groups of wavefronts");
+static_assert(kWaveM == 128 && kWaveN == 64 && kGemmBK == 64, "fragments_mn's places");
+static_assert(kSlotsA * CeStage::kBytesA + kSlotsB * CeStage::kBytesB == kCeDynLds, "the ring");
+
+// Waits for a wavefront's copies into LDS, the last PENDING excepted.
+template <int PENDING>
+__device__ __forceinline__ void wait_copies() {
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(PENDING));
+    asm volatile("" ::: "memory");
+}
+// The workgroup's barrier, with nothing moved across it.
+__device__ __forceinline__ void meet() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// A 256 x 256 tile of 16-bit results in LDS: 512-byte rows whose 32-byte pieces are swizzled by bits 0, 2 and
+// 3 of the row (a wavefront writes such a piece of eight rows at once).
+constexpr int kTileBytes = kGemmBM * kGemmBN * 2;
+__device__ __forceinline__ int tile_at(int row, int byte) {
+    return row * (2 * kGemmBN) + (byte ^ (((row & 1) | ((row >> 1) & 6)) << 5));
+}
+
+// The accumulators, rounded, into the tile: lanes 2c and 2c + 1 (adjacent columns) swap one value, so that
+// each writes two adjacent columns of one row as 32 bits.
+template <typename T, typename Row, typename Col, typename Value>
+__device__ __forceinline__ void stage_tile(char* tile, int lane, Row row_of, Col col_of, Value value) {
+    const int odd = lane & 1;
+#pragma unroll
+    for (int i = 0; i < kRowTiles; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+#pragma unroll
+            for (int j = 0; j < kColTiles; ++j) {
+                const float a = value(i, j, e), b = value(i, j, e + 1);
+                const float got = swap_pair(odd ? a : b);
+                *reinterpret_cast<uint32_t*>(tile + tile_at(row_of(i) + e + odd, 2 * (col_of(j) - odd))) =
+                    Elem<T>::pack(odd ? got : a, odd ? b : got);
+            }
+}
+
+// The tile's rows below M and columns below N (a multiple of 8) to memory: half a wavefront takes a row's 512 bytes.
+template <typename T>
+__device__ __forceinline__ void store_tile(const char* tile, T* out, int64_t ld, int m0, int M, int n0, int N) {
+    const int c = threadIdx.x & 31, col = n0 + 8 * c;
+#pragma unroll 4
+    for (int r = threadIdx.x >> 5; r < kGemmBM; r += kGemmThreads / 32)
+        if (m0 + r < M && col < N)
+            *reinterpret_cast<u32x4*>(out + int64_t(m0 + r) * ld + col) =
+                *reinterpret_cast<const u32x4*>(tile + tile_at(r, 16 * c));
+}
 
 }  // namespace
 
@@ -101,269 +272,302 @@ __global__ void __launch_bounds__(kCeThreads) ce_gather(const CeGatherArgs a) {
 template <typename T, int PRODUCT, bool A_KCONTIG, bool B_KCONTIG>
 __global__ void __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 ce_gemm(const CeGemmArgs g) {
-    extern __shared__ __attribute__((aligned(1024))) uint16_t ring[];
+    extern __shared__ __attribute__((aligned(1024))) char ring[];
     constexpr int BK = kGemmBK;
-    using St = Stage<BK>;
-    __shared__ float red_a[kGemmWavesM][kGemmBN];
-    __shared__ int tgt_col[kGemmBM];
 
     const int count = g.state->count;
     const int M = PRODUCT == kCeWeight ? g.M : min(g.M, count);
     const int K = PRODUCT == kCeWeight ? min(g.K, count) : g.K;
     const uint32_t tiles_m = uint32_t(M + kGemmBM - 1) / kGemmBM;
-    const uint32_t block = blockIdx.x + gridDim.x * blockIdx.z;
-    if (block >= tiles_m * g.tiles_n * gridDim.z) return;     // the launch was sized for every row
+    const uint32_t splits = PRODUCT == kCeHidden ? ce_splits(tiles_m, g.tiles_n, g.split_k, g.max_splits) : 1u;
+    if (blockIdx.x >= tiles_m * g.tiles_n * splits) return;   // the launch was sized for every row
     uint32_t tm, tn, split;
-    tile_of(block, tiles_m, g.tiles_n, gridDim.z, tm, tn, split);
+    tile_of(blockIdx.x, tiles_m, g.tiles_n, splits, tm, tn, split);
     const int m0 = int(tm) * kGemmBM, n0 = int(tn) * kGemmBN;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / kGemmWavesN, wn = wave % kGemmWavesN;
-    const int kb = PRODUCT == kCeHidden ? int(split) * g.k_split : 0;
-    const int ke = PRODUCT == kCeHidden ? min(K, kb + g.k_split) : K;
+    const int k_split = PRODUCT == kCeHidden ? ce_k_split(g.split_k, splits) : K;
+    const int kb = int(split) * k_split, ke = min(K, kb + k_split);
     const uint16_t* __restrict__ A = static_cast<const uint16_t*>(g.a);
     const uint16_t* __restrict__ B = static_cast<const uint16_t*>(g.b);
 
-    // Accumulator element e of tile (i, j) is tile row wm*kWaveM + i*32 + 8*(e/4) +
-    // 4*(lane/32) + e%4 and column wn*kWaveN + j*32 + lane%32.
-    auto row_of_e = [&](int i, int e) { return wm * kWaveM + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3); };
-    auto col_of_j = [&](int j) { return wn * kWaveN + j * 32 + (lane & 31); };
+    // Accumulator element e of tile (i, j) is the workgroup tile's row row_of(i) + e and column col_of(j).
+    auto row_of = [&](int i) { return wm * kWaveM + i * 16 + 4 * (lane >> 4); };
+    auto col_of = [&](int j) { return wn * kWaveN + j * 16 + (lane & 15); };
 
-    floatx16 acc[kFragM][kFragN];
+    floatx4 acc[kRowTiles][kColTiles];
 #pragma unroll
-    for (int i = 0; i < kFragM; ++i)
+    for (int i = 0; i < kRowTiles; ++i)
 #pragma unroll
-        for (int j = 0; j < kFragN; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+        for (int j = 0; j < kColTiles; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
     const int nst = kb < ke ? (ke - kb + BK - 1) / BK : 0;
-    auto issue = [&](int s) {
+    // Byte offsets of this lane's 16-byte pieces of the wavefront's copies, from an operand's tile at any stage.
+    uint32_t off_a[kCopies], off_b[kCopies];
+#pragma unroll
+    for (int u = 0; u < kCopies; ++u) {
+        off_a[u] = dma_source<A_KCONTIG, BK, CeStage>(wave * kCopies + u, lane, uint32_t(g.lda), M, INT32_MAX, m0, 0);
+        off_b[u] = dma_source<B_KCONTIG, BK, CeStage>(wave * kCopies + u, lane, uint32_t(g.ldb), g.N, INT32_MAX, n0, 0);
+    }
+    // The wavefront's copies of an operand's stage s into its ring; the last stage's K past ke read as zeros.
+    auto issue = [&](auto kcontig, const uint16_t* x, int64_t ld, int first, int R, const uint32_t (&off)[kCopies], int s,
+                     char* to) {
         const int k0 = kb + s * BK;
-        char* slot = reinterpret_cast<char*>(ring) + (s % St::kCount) * St::kBytes;
-        const __amdgpu_buffer_rsrc_t a0 =
-            buffer_at(A + (A_KCONTIG ? int64_t(m0) * g.lda + k0 : int64_t(k0) * g.lda + m0));
-        const __amdgpu_buffer_rsrc_t b0 =
-            buffer_at(B + (B_KCONTIG ? int64_t(n0) * g.ldb + k0 : int64_t(k0) * g.ldb + n0));
+        const __amdgpu_buffer_rsrc_t from =
+            buffer_at(x + (kcontig ? int64_t(first) * ld + k0 : int64_t(k0) * ld + first));
 #pragma unroll
-        for (int u = 0; u < St::kDmaA; ++u) {
-            const int q = wave * St::kDmaA + u;
-            dma16(a0, dma_source<A_KCONTIG, BK>(q, lane, uint32_t(g.lda), M, ke, m0, k0), slot + q * 1024);
-        }
-#pragma unroll
-        for (int u = 0; u < St::kDmaB; ++u) {
-            const int q = wave * St::kDmaB + u;
-            dma16(b0, dma_source<B_KCONTIG, BK>(q, lane, uint32_t(g.ldb), g.N, ke, n0, k0),
-                  slot + St::kBytesA + q * 1024);
+        for (int u = 0; u < kCopies; ++u) {
+            const int q = wave * kCopies + u;
+            const uint32_t o =
+                k0 + BK <= ke ? off[u] : dma_source<kcontig, BK, CeStage>(q, lane, uint32_t(ld), R, ke, first, k0);
+            dma16(from, o, to + q * 1024);
         }
     };
+    char* const ring_b = ring + kSlotsA * CeStage::kBytesA;
+    auto issue_a = [&](int s) {
+        if (s < nst)
+            issue(std::integral_constant<bool, A_KCONTIG>(), A, g.lda, m0, M, off_a, s, ring + s % kSlotsA * CeStage::kBytesA);
+    };
+    auto issue_b = [&](int s) {
+        if (s < nst)
+            issue(std::integral_constant<bool, B_KCONTIG>(), B, g.ldb, n0, g.N, off_b, s, ring_b + (s & 1) * CeStage::kBytesB);
+    };
+    uint4 af[2][kRowTiles / 2], bf[2][kColTiles];
+    auto stage_a = [&](int s) { return ring + s % kSlotsA * CeStage::kBytesA; };
+    auto stage_b = [&](int s) { return ring_b + (s & 1) * CeStage::kBytesB; };
+    auto read_a = [&](int s, auto half) {  // the fragments of 32 of stage s's K
+        if constexpr (A_KCONTIG) {
+            const uint32_t at = k_base(stage_a(s), wm * kWaveM, half, lane);
+            fragments_k(at, at + 8192, af[0], af[1]);
+        } else {
+            uint32_t at[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) at[c] = mn_base(stage_a(s) + wm * 2 * 8192, c, lane);
+            fragments_mn<4096 * half, 8192 + 4096 * half>(at, af[0], af[1]);
+        }
+    };
+    auto read_b = [&](int s) {             // of all of it
+        if constexpr (B_KCONTIG) {
+            fragments_k(k_base(stage_b(s), wn * kWaveN, 0, lane), k_base(stage_b(s), wn * kWaveN, 1, lane), bf[0], bf[1]);
+        } else {
+            uint32_t at[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) at[c] = mn_base(stage_b(s) + wn * 8192, c, lane);
+            fragments_mn<0, 4096>(at, bf[0], bf[1]);
+        }
+    };
+    auto multiply = [&](auto half) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 0; i < kRowTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < kColTiles; ++j) acc[i][j] = mfma16<T>(af[i / 4][i % 4], bf[half][j], acc[i][j]);
+        __builtin_amdgcn_s_setprio(0);
+    };
+    const std::integral_constant<int, 0> lower{};
+    const std::integral_constant<int, 1> upper{};
+    // Stage s has landed once only the copies of stage s + 1 are in flight.
+    auto wait_stage = [&](int s) {
+        if (s + 1 < nst) wait_copies<2 * kCopies>();
+        else wait_copies<0>();
+    };
+    // A step in four turns, each ended by the workgroup's barrier: fragments of half a stage, their matrix
+    // instructions, and the same for the other half.  The wavefronts of the tile's lower half (one on
+    // each SIMD, as those of the upper) run one turn behind, so that one group reads LDS while the other
+    // multiplies.  Copies run two stages ahead: stage s + 2 of A goes to the slot that stage s - 1 left,
+    // that of B to stage s's own, whose fragments are all in registers after the step's first two turns.
     if (nst > 0) {
-        for (int s = 0; s < St::kCount - 1; ++s) issue(s);
+        issue_a(0);
+        issue_b(0);
+        issue_a(1);
+        issue_b(1);
+        wait_stage(0);
+        meet();
+        if (wm == 1) meet();
         for (int s = 0; s < nst; ++s) {
-            wait_stages<St::kCount - 2, BK>();
-            issue(s + St::kCount - 1);     // past the last stage: out of range, zeros
-            const uint16_t* at = ring + (s % St::kCount) * (St::kBytes / 2);
-            const uint16_t* bt = at + St::kBytesA / 2;
-#pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-                uint4 af[kFragM], bf[kFragN];
-#pragma unroll
-                for (int i = 0; i < kFragM; ++i) af[i] = fragment<A_KCONTIG, kWaveM, BK>(at, wm, i, kk, lane);
-#pragma unroll
-                for (int j = 0; j < kFragN; ++j) bf[j] = fragment<B_KCONTIG, kWaveN, BK>(bt, wn, j, kk, lane);
-#pragma unroll
-                for (int i = 0; i < kFragM; ++i)
-#pragma unroll
-                    for (int j = 0; j < kFragN; ++j) acc[i][j] = Mfma<uint16_t>::run(af[i], bf[j], acc[i][j], T());
+            issue_a(s + 2);
+            if constexpr (A_KCONTIG && B_KCONTIG) {
+                const uint32_t at = k_base(stage_a(s), wm * kWaveM, 0, lane);
+                fragments_k(at, at + 8192, k_base(stage_b(s), wn * kWaveN, 0, lane),
+                            k_base(stage_b(s), wn * kWaveN, 1, lane), af[0], af[1], bf[0], bf[1]);
+            } else {
+                read_b(s);
+                read_a(s, lower);
             }
+            meet();
+            multiply(lower);
+            meet();
+            issue_b(s + 2);
+            read_a(s, upper);
+            if (wm == 1) wait_stage(s + 1);
+            meet();
+            multiply(upper);
+            if (wm == 0) wait_stage(s + 1);
+            meet();
         }
+        if (wm == 0) meet();
     }
-    __syncthreads();
+    __syncthreads();                       // the ring is free
 
-    if constexpr (PRODUCT == kCeHidden) {
-        float* __restrict__ C = static_cast<float*>(g.c) + int64_t(split) * g.plane;
+    if constexpr (PRODUCT == kCeHidden || PRODUCT == kCeWeight) {
+        const bool f32 = PRODUCT == kCeHidden || g.out_f32;
+        const float scale = PRODUCT == kCeHidden ? 1.0f : g.state->scale;
+        if (f32) {
+            float* __restrict__ C = static_cast<float*>(g.c);
+            if (PRODUCT == kCeHidden) C += int64_t(split) * g.N * M;
+            // Half of the tile's rows at a time through LDS, so that a wavefront's access covers 1 KB of one row.
+            for (int w = 0; w < kGemmWavesM; ++w) {
+                __syncthreads();
+                if (wm == w) {
 #pragma unroll
-        for (int i = 0; i < kFragM; ++i) {
-            float old[16][kFragN] = {};
-            if (g.accumulate) {            // clamped to a valid element outside M x N, where nothing is stored
+                    for (int i = 0; i < kRowTiles; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int row = min(m0 + row_of_e(i, e), M - 1);
+                        for (int j = 0; j < kColTiles; ++j)
 #pragma unroll
-                    for (int j = 0; j < kFragN; ++j) old[e][j] = C[int64_t(row) * g.ldc + min(n0 + col_of_j(j), g.N - 1)];
+                            for (int e = 0; e < 4; ++e) {
+                                const int r = row_of(i) + e - w * kWaveM;
+                                *reinterpret_cast<float*>(ring + r * 1024 + ((4 * col_of(j)) ^ (((r >> 2) & 3) << 6))) =
+                                    acc[i][j][e] * scale;
+                            }
                 }
-            }
+                __syncthreads();
+                const int col = n0 + 4 * lane;
+                for (int r = wave; r < kWaveM; r += kGemmWaves) {
+                    const int row = m0 + w * kWaveM + r;
+                    if (row >= M || col >= g.N) continue;
+                    float v[4];
+                    load_row<4>(reinterpret_cast<const float*>(ring + r * 1024 + ((16 * lane) ^ (((r >> 2) & 3) << 6))), v);
+                    float* to = C + int64_t(row) * g.ldc + col;
+                    if (g.accumulate) {
+                        float old[4];
+                        load_row<4>(static_cast<const float*>(to), old);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = m0 + row_of_e(i, e);
-                if (row >= M) continue;
-#pragma unroll
-                for (int j = 0; j < kFragN; ++j) {
-                    const int col = n0 + col_of_j(j);
-                    if (col < g.N) C[int64_t(row) * g.ldc + col] = old[e][j] + acc[i][j][e];
-                }
-            }
-        }
-        return;
-    }
-
-    if constexpr (PRODUCT == kCeWeight) {
-        const float scale = g.state->scale;
-#pragma unroll
-        for (int i = 0; i < kFragM; ++i)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int row = m0 + row_of_e(i, e);
-                if (row >= M) continue;
-#pragma unroll
-                for (int j = 0; j < kFragN; ++j) {
-                    const int col = n0 + col_of_j(j);
-                    if (col >= g.N) continue;
-                    const int64_t at = int64_t(row) * g.ldc + col;
-                    const float v = acc[i][j][e] * scale;
-                    if (g.out_f32) {
-                        float* c = static_cast<float*>(g.c) + at;
-                        *c = g.accumulate ? *c + v : v;
-                    } else {
-                        static_cast<T*>(g.c)[at] = from_f<T>(v);
+                        for (int k = 0; k < 4; ++k) v[k] += old[k];
                     }
+                    store_row<4>(to, v);
                 }
             }
+            return;
+        }
+        stage_tile<T>(ring, lane, row_of, col_of, [&](int i, int j, int e) { return acc[i][j][e] * scale; });
+        __syncthreads();
+        store_tile<T>(ring, static_cast<T*>(g.c), g.ldc, m0, M, n0, g.N);
         return;
     }
 
     // Logits: z = acc + bias; columns past N are -inf.
     const T* __restrict__ bias = static_cast<const T*>(g.bias);
 #pragma unroll
-    for (int j = 0; j < kFragN; ++j) {
-        const int col = n0 + col_of_j(j);
+    for (int j = 0; j < kColTiles; ++j) {
+        const int col = n0 + col_of(j);
         const float b = col < g.N ? (bias ? to_f<T>(bias[col]) : 0.0f) : -__builtin_inff();
 #pragma unroll
-        for (int i = 0; i < kFragM; ++i)
+        for (int i = 0; i < kRowTiles; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] += b;
+            for (int e = 0; e < 4; ++e) acc[i][j][e] += b;
     }
 
     if constexpr (PRODUCT == kCeDlogits) {
-        float* row_lse = reinterpret_cast<float*>(ring);
+        float* row_lse = reinterpret_cast<float*>(ring + kTileBytes);
         float* row_f = row_lse + kGemmBM;
+        int* tgt_col = reinterpret_cast<int*>(row_f + kGemmBM);
+        float(*sums)[kGemmBN] = reinterpret_cast<float(*)[kGemmBN]>(tgt_col + kGemmBM);
         if (threadIdx.x < kGemmBM) {
             const int row = m0 + int(threadIdx.x);
             const float lse = row < M ? g.lse[row] : 0.0f;
             const int t = row < M ? g.target[row] - g.first - n0 : -1;
             row_lse[threadIdx.x] = lse;
-            row_f[threadIdx.x] = kDzScale<T> * (1.0f + g.z_loss2 * lse);
+            row_f[threadIdx.x] = row < M ? kDzScale<T> * (1.0f + g.z_loss2 * lse) : 0.0f;
             tgt_col[threadIdx.x] = t >= 0 && t < kGemmBN && n0 + t < g.N ? t : -1;
         }
         __syncthreads();
-        T* __restrict__ D = static_cast<T*>(g.c);
-        const bool odd = lane & 1;
-        float csum[kFragN] = {};
+        // rows past M have a factor of 0 and no target, columns past N a logit of -inf: exact zeros
 #pragma unroll
-        for (int i = 0; i < kFragM; ++i) {
+        for (int i = 0; i < kRowTiles; ++i)
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                float dz[2][kFragN];
+            for (int e = 0; e < 4; ++e) {
+                const int r = row_of(i) + e;
+                const float l = row_lse[r], f = row_f[r];
+                const int tc = tgt_col[r];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = row_of_e(i, e + h);
-                    const bool in = m0 + r < M;
-                    const float l = row_lse[r], f = row_f[r];
-                    const int tc = tgt_col[r];
-#pragma unroll
-                    for (int j = 0; j < kFragN; ++j) {
-                        const int c = col_of_j(j);
-                        const float p = __builtin_amdgcn_exp2f((acc[i][j][e + h] - l) * kLog2eG);
-                        dz[h][j] = (in && n0 + c < g.N) ? f * p - (c == tc ? kDzScale<T> : 0.0f) : 0.0f;
-                        csum[j] += dz[h][j];
-                    }
-                }
-                const int row = m0 + row_of_e(i, e) + (odd ? 1 : 0);
-#pragma unroll
-                for (int j = 0; j < kFragN; ++j) {
-                    const float got = swap_pair(odd ? dz[0][j] : dz[1][j]);
-                    const float lo = odd ? got : dz[0][j];
-                    const float hi = odd ? dz[1][j] : got;
-                    const int col = n0 + col_of_j(j) - (odd ? 1 : 0);
-                    // up to the row pitch: the padding past N is zeros, a K tail of the hidden product
-                    if (row < M && col < g.ldc)
-                        *reinterpret_cast<uint32_t*>(D + int64_t(row) * g.ldc + col) = Elem<T>::pack(lo, hi);
+                for (int j = 0; j < kColTiles; ++j) {
+                    const float p = __builtin_amdgcn_exp2f((acc[i][j][e] - l) * kLog2eG);
+                    acc[i][j][e] = (f != 0.0f ? f * p : 0.0f) - (col_of(j) == tc ? kDzScale<T> : 0.0f);
                 }
             }
-        }
         if (g.col_part) {
 #pragma unroll
-            for (int j = 0; j < kFragN; ++j) {
-                const float s = csum[j] + __shfl_xor(csum[j], 32, 64);
-                if (lane < 32) red_a[wm][col_of_j(j)] = s;
-            }
-            __syncthreads();
-            const int col = n0 + int(threadIdx.x);
-            if (threadIdx.x < kGemmBN && col < g.N) {
-                float t = red_a[0][threadIdx.x];
+            for (int j = 0; j < kColTiles; ++j) {
+                float s = 0.0f;
 #pragma unroll
-                for (int w = 1; w < kGemmWavesM; ++w) t += red_a[w][threadIdx.x];
-                g.col_part[int64_t(tm) * g.N + col] = t;
+                for (int i = 0; i < kRowTiles; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s += acc[i][j][e];
+                s += __shfl_xor(s, 16, 64);
+                s += __shfl_xor(s, 32, 64);
+                if (lane < 16) sums[wm][col_of(j)] = s;
             }
         }
+        stage_tile<T>(ring, lane, row_of, col_of, [&](int i, int j, int e) { return acc[i][j][e]; });
+        __syncthreads();
+        // the piece's columns past N too: their zeros are the hidden product's K tail
+        store_tile<T>(ring, static_cast<T*>(g.c), g.ldc, m0, M, n0, int(g.ldc));
+        const int col = n0 + int(threadIdx.x);
+        if (g.col_part && threadIdx.x < kGemmBN && col < g.N)
+            g.col_part[int64_t(tm) * g.N + col] = sums[0][threadIdx.x] + sums[1][threadIdx.x];
         return;
     }
 
-    // kCeLogits: a lane reduces its own columns of a row; the 128 partials of a row
-    // meet in LDS, half of the rows at a time, laid out [partial][row ^ part_swizzle(partial)]
-    // (writes and reads free of bank conflicts), and four neighbouring lanes merge a row.
-    constexpr int kParts = kGemmWavesN * 32;
-    constexpr int kRoundRows = kGemmBM / kGemmWavesM;
-    constexpr int kShare = kParts / 4;
-    static_assert(kGemmThreads == 4 * kRoundRows && kParts * kRoundRows * 8 <= kGemmDynLds && kParts <= 256,
-                  "four lanes a row; the partials fit");
+    // kCeLogits: a lane reduces its four columns of a row; the 64 partials of a row meet in LDS, laid out
+    // [partial][row ^ part_row(partial)] (writes and reads free of bank conflicts), and two neighbouring lanes
+    // merge a row.
+    constexpr int kParts = kGemmWavesN * 16;
+    constexpr int kShare = kParts / 2;
+    static_assert(kGemmThreads == 2 * kGemmBM && kParts * kGemmBM * 8 + kGemmBM * 4 <= kCeDynLds, "the partials fit");
+    const auto part_row = [](int p) { return (p & 3) | ((p & 12) << 1) ^ ((p >> 5) << 4); };
     float2* parts = reinterpret_cast<float2*>(ring);
+    int* tgt_col = reinterpret_cast<int*>(parts + kParts * kGemmBM);
     if (threadIdx.x < kGemmBM) {
         const int row = m0 + int(threadIdx.x);
         const int t = row < M ? g.target[row] - n0 : -1;
         tgt_col[threadIdx.x] = t >= 0 && t < kGemmBN && n0 + t < g.N ? t : -1;
     }
-    const int pidx = wn * 32 + (lane & 31);
+    __syncthreads();
+    const int pidx = wn * 16 + (lane & 15);
 #pragma unroll
-    for (int w = 0; w < kGemmWavesM; ++w) {
-        __syncthreads();                   // tgt_col written; parts free
-        if (wm == w) {
+    for (int i = 0; i < kRowTiles; ++i)
 #pragma unroll
-            for (int i = 0; i < kFragM; ++i)
+        for (int e = 0; e < 4; ++e) {
+            const int r = row_of(i) + e;
+            const float m = fmaxf(fmaxf(acc[i][0][e], acc[i][1][e]), fmaxf(acc[i][2][e], acc[i][3][e]));
+            float sum = 0.0f;
+            if (m != -__builtin_inff()) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int r = row_of_e(i, e);
-                    float m = acc[i][0][e];
+                for (int j = 0; j < kColTiles; ++j) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * kLog2eG);
+            }
+            parts[pidx * kGemmBM + (r ^ part_row(pidx))] = make_float2(m, sum);
+            const int tc = tgt_col[r];
 #pragma unroll
-                    for (int j = 1; j < kFragN; ++j) m = fmaxf(m, acc[i][j][e]);
-                    float sum = 0.0f;
-                    if (m != -__builtin_inff()) {
-#pragma unroll
-                        for (int j = 0; j < kFragN; ++j) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * kLog2eG);
-                    }
-                    parts[pidx * kRoundRows + ((r - w * kRoundRows) ^ part_swizzle(pidx))] = make_float2(m, sum);
-                    const int tc = tgt_col[r];
-#pragma unroll
-                    for (int j = 0; j < kFragN; ++j)
-                        if (col_of_j(j) == tc && m0 + r < M) g.target_logit[m0 + r] = acc[i][j][e];
-                }
+            for (int j = 0; j < kColTiles; ++j)
+                if (col_of(j) == tc && m0 + r < M) g.target_logit[m0 + r] = acc[i][j][e];
         }
-        __syncthreads();
-        const int rr = threadIdx.x / 4, qq = threadIdx.x % 4, row = m0 + w * kRoundRows + rr;
-        float top = -__builtin_inff();
-        for (int q = qq * kShare; q < (qq + 1) * kShare; ++q)
-            top = fmaxf(top, parts[q * kRoundRows + (rr ^ part_swizzle(q))].x);
-        top = fmaxf(top, quad_xor<1>(top));
-        top = fmaxf(top, quad_xor<2>(top));
-        float sum = 0.0f;
-        for (int q = top == -__builtin_inff() ? kParts : qq * kShare; q < (qq + 1) * kShare; ++q) {   // none where all are -inf
-            const float2 v = parts[q * kRoundRows + (rr ^ part_swizzle(q))];
+    __syncthreads();
+    const int rr = threadIdx.x / 2, first = threadIdx.x % 2 * kShare, row = m0 + rr;
+    float top = -__builtin_inff();
+#pragma unroll 8
+    for (int p = first; p < first + kShare; ++p) top = fmaxf(top, parts[p * kGemmBM + (rr ^ part_row(p))].x);
+    top = fmaxf(top, quad_xor<1>(top));
+    float sum = 0.0f;
+    if (top != -__builtin_inff()) {
+#pragma unroll 8
+        for (int p = first; p < first + kShare; ++p) {
+            const float2 v = parts[p * kGemmBM + (rr ^ part_row(p))];
             sum += v.y * __builtin_amdgcn_exp2f((v.x - top) * kLog2eG);
         }
-        sum += quad_xor<1>(sum);
-        sum += quad_xor<2>(sum);
-        if (qq == 0 && row < M)
-            reinterpret_cast<float2*>(g.part)[int64_t(row) * g.tiles_n + tn] = make_float2(top, sum);
     }
+    sum += quad_xor<1>(sum);
+    if (threadIdx.x % 2 == 0 && row < M)
+        reinterpret_cast<float2*>(g.part)[int64_t(row) * g.tiles_n + tn] = make_float2(top, sum);
 }
 
 // A workgroup joins a kept row's tiles (each lane's in order, then the lane tree).
@@ -415,6 +619,9 @@ __global__ void __launch_bounds__(kCeCompactThreads) ce_loss(const CeLossArgs a)
 template <typename T>
 __global__ void __launch_bounds__(kCeThreads) ce_hidden(const CeHiddenArgs a) {
     const float scale = a.state->scale;
+    const int count = a.state->count;
+    const int64_t plane = int64_t(count) * a.cols;
+    const int splits = ce_splits((count + kGemmBM - 1) / kGemmBM, (a.cols + kGemmBN - 1) / kGemmBN, a.split_k, a.max_splits);
     for (int row = blockIdx.x; row < a.n; row += gridDim.x) {
         const int k = a.place[row];
         T* out = static_cast<T*>(a.out) + int64_t(row) * a.cols;
@@ -422,9 +629,9 @@ __global__ void __launch_bounds__(kCeThreads) ce_hidden(const CeHiddenArgs a) {
             float v[8] = {};
             if (k >= 0) {
                 const float* p = a.part + int64_t(k) * a.cols + c;
-                for (int z = 0; z < a.splits; ++z) {
+                for (int z = 0; z < splits; ++z) {
                     float x[8];
-                    load_row<8>(p + z * a.plane, x);
+                    load_row<8>(p + z * plane, x);
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[q] += x[q];
                 }

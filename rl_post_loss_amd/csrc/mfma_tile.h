@@ -103,9 +103,8 @@ struct Stage {
 constexpr uint32_t kOutOfRange = 0xFFFFFFF0u;
 constexpr int kBufferRecords = 0x7FFFFFF0;
 
-template <bool KCONTIG, int BK>
+template <bool KCONTIG, int BK, typename St = Stage<BK>>
 __device__ __forceinline__ uint32_t dma_source(int q, int lane, uint32_t ld, int R, int ke, int r0, int k0) {
-    using St = Stage<BK>;
     if constexpr (KCONTIG) {
         const int r = St::kRowsPerCopy * q + lane / St::kC;
         const int c = (lane % St::kC) ^ St::kc_swizzle(r);

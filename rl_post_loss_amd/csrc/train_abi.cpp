@@ -45,7 +45,7 @@ int device(const Device** out) {
         for (int dt : {RLPL_F16, RLPL_BF16})
             for (int product = 0; product < 4; ++product)
                 if (hipFuncSetAttribute(pick_ce_gemm(dt, product), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                        kGemmDynLds) != hipSuccess)
+                                        kCeDynLds) != hipSuccess)
                     return;
         d.status = RLPL_OK;
     });
@@ -66,13 +66,13 @@ constexpr int64_t kCePieceCols = 8192;
 bool ce_shape_ok(int64_t n, int64_t h, int64_t vocab) {
     return n >= 1 && n <= kCeMaxRows && h >= 8 && h <= kCeMaxHidden && h % 8 == 0 && vocab >= 1 && vocab < kCeMaxVocab &&
            div_up(n, kGemmBM) * div_up(vocab, kGemmBN) < kCeMaxTiles &&
-           div_up(n, kGemmBM) * div_up(h, kGemmBN) < kCeMaxTiles;
+           div_up(n, kGemmBM) * div_up(h, kGemmBN) * kCeMaxSplits < kCeMaxTiles;
 }
 
 // Workspace of a call, sized for every row: what the compaction leaves and the kept hidden states, then
 // the loss's tile partials, whose place the gradient's dz, planes and column sums take afterwards.
 struct CeLayout {
-    int64_t piece, pieces, tiles_m, tiles_n, splits, k_split;
+    int64_t piece, tiles_m, tiles_n, splits;
     size_t row, place, target, lse, row_loss, target_logit, hidden, part, dz, planes, cols, total;   // offsets
 };
 CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
@@ -94,18 +94,17 @@ CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
         if (piece < kCePieceCols) piece = kCePieceCols;
         const int64_t all = L.tiles_n * kGemmBN;
         L.piece = piece < all ? piece : all;
-        L.pieces = div_up(vocab, L.piece);
-        // enough splits of K that the hidden product has a tile for every compute unit
-        const int64_t tiles = L.tiles_m * div_up(h, kGemmBN);
-        int64_t splits = 256 / tiles;
-        const int64_t most = L.piece / kGemmBN;
-        if (splits > kCeMaxSplits) splits = kCeMaxSplits;
-        if (splits > most) splits = most;
-        if (splits < 1) splits = 1;
-        L.splits = splits;
-        L.k_split = div_up(div_up(L.piece, splits), kGemmBK) * kGemmBK;
+        // planes for up to kCeMaxSplits splits of K, of as many rows as still leave a split its own round
+        const int64_t tiles_h = div_up(h, kGemmBN), most = L.piece / kGemmBN;
+        L.splits = most < kCeMaxSplits ? most : kCeMaxSplits;
+        int64_t rows = 0;              // largest number of rows times splits over the counts that may come
+        for (int64_t m = 1; m <= L.tiles_m; ++m) {
+            const int64_t r = m * kGemmBM < n ? m * kGemmBM : n;
+            const int64_t s = ce_splits(uint32_t(m), uint32_t(tiles_h), int32_t(L.piece), int32_t(L.splits));
+            if (r * s > rows) rows = r * s;
+        }
         L.dz = take(size_t(n) * size_t(L.piece) * 2);
-        L.planes = take(size_t(splits) * size_t(n) * size_t(h) * sizeof(float));
+        L.planes = take(size_t(rows) * size_t(h) * sizeof(float));
         L.cols = take(size_t(L.tiles_m) * size_t(L.piece) * sizeof(float));
     }
     L.total = at > after_loss ? at : after_loss;
@@ -139,7 +138,7 @@ int ce_check(const CeCall& c, bool grads) {
     if (grads && c.accumulate && c.weight_grad_dtype != RLPL_F32) return RLPL_ERR_PARAM;
     const size_t we = grads ? dtype_bytes(c.weight_grad_dtype) : 1;
     if (!is_aligned(c.hidden, 16) || !is_aligned(c.weight, 16) || !is_aligned(c.bias, 2) || !is_aligned(c.targets, 8) ||
-        !is_aligned(c.loss, 4) || !is_aligned(c.grad_hidden, 16) || !is_aligned(c.grad_weight, we < 4 ? 16 : 4) ||
+        !is_aligned(c.loss, 4) || !is_aligned(c.grad_hidden, 16) || !is_aligned(c.grad_weight, 16) ||
         !is_aligned(c.grad_bias, we))
         return RLPL_ERR_ALIGN;
     if (!c.workspace || c.workspace_bytes < ce_layout(c.n, c.h, c.vocab, grads).total) return RLPL_ERR_WORKSPACE;
@@ -147,8 +146,8 @@ int ce_check(const CeCall& c, bool grads) {
 }
 
 int ce_product(int dtype, int product, const CeGemmArgs& g, unsigned splits, hipStream_t stream) {
-    return enqueue(pick_ce_gemm(dtype, product), g, dim3(g.tiles_m * g.tiles_n, 1, splits), kGemmThreads, stream,
-                   kGemmDynLds);
+    return enqueue(pick_ce_gemm(dtype, product), g, dim3(g.tiles_m * g.tiles_n * splits), kGemmThreads, stream,
+                   kCeDynLds);
 }
 
 int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
@@ -175,7 +174,7 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     z.lda = z.ldb = c.h;
     z.M = int32_t(c.n);
     z.N = int32_t(c.vocab);
-    z.K = z.k_split = int32_t(c.h);
+    z.K = int32_t(c.h);
     z.tiles_m = uint32_t(L.tiles_m);
     z.tiles_n = uint32_t(L.tiles_n);
     z.state = state;
@@ -216,12 +215,12 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
             g.M = int32_t(c.n);
             g.N = int32_t(c.h);
             g.K = int32_t(cols);
-            g.k_split = int32_t(L.k_split);
+            g.split_k = int32_t(L.piece);
+            g.max_splits = int32_t(L.splits);
             g.tiles_m = uint32_t(L.tiles_m);
             g.tiles_n = uint32_t(div_up(c.h, kGemmBN));
             g.state = state;
             g.c = ws + L.planes;
-            g.plane = c.n * c.h;
             g.accumulate = v0 > 0 ? 1 : 0;
             if ((st = ce_product(c.dtype, kCeHidden, g, unsigned(L.splits), stream)) != RLPL_OK) return st;
         }
@@ -233,7 +232,7 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
             g.ldb = g.ldc = c.h;
             g.M = int32_t(cols);
             g.N = int32_t(c.h);
-            g.K = g.k_split = int32_t(c.n);
+            g.K = int32_t(c.n);
             g.tiles_m = uint32_t(div_up(cols, kGemmBM));
             g.tiles_n = uint32_t(div_up(c.h, kGemmBN));
             g.state = state;
@@ -250,8 +249,8 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         }
     }
     if (!c.grad_hidden) return RLPL_OK;
-    const CeHiddenArgs h{floats(L.planes), ints(L.place), state, c.grad_hidden, c.n * c.h, int32_t(c.n), int32_t(c.h),
-                         int32_t(L.splits)};
+    const CeHiddenArgs h{floats(L.planes), ints(L.place), state, c.grad_hidden, int32_t(c.n), int32_t(c.h),
+                         int32_t(L.piece), int32_t(L.splits)};
     return enqueue(pick_ce_hidden(c.dtype), h, dim3(capped(c.n, 1 << 16)), kCeThreads, stream);
 }
 

@@ -404,7 +404,7 @@ def test_refusals_of_the_c_entry_points():
         assert call(False, **over) == want, over
     for want, over in [("RLPL_ERR_DTYPE", dict(wdt=1)), ("RLPL_ERR_PARAM", dict(acc=1)),
                        ("RLPL_ERR_ALIGN", dict(dh=A + 0x500008)), ("RLPL_ERR_ALIGN", dict(dw=A + 0x600008)),
-                       ("RLPL_ERR_ALIGN", dict(wdt=0, dw=A + 0x600002)), ("RLPL_ERR_ALIGN", dict(db=A + 0x700001))]:
+                       ("RLPL_ERR_ALIGN", dict(wdt=0, dw=A + 0x600004)), ("RLPL_ERR_ALIGN", dict(db=A + 0x700001))]:
         assert call(True, **over) == want, over
     size = rl.library().linear_cross_entropy_workspace_bytes
     assert size(0, 64, 100, 1) == 0 and size(8, 60, 100, 1) == 0
@@ -413,7 +413,7 @@ def test_refusals_of_the_c_entry_points():
     if not torch.cuda.is_available():
         assert call(True) == "RLPL_ERR_DEVICE" and call(False) == "RLPL_ERR_DEVICE"
         assert call(True, dh=None, dw=None, db=None, b=None) == "RLPL_ERR_DEVICE"
-        assert call(True, wdt=0, acc=1, dw=A + 0x600004) == "RLPL_ERR_DEVICE"
+        assert call(True, wdt=0, acc=1, dw=A + 0x600010) == "RLPL_ERR_DEVICE"
 
 
 def test_constants_match_the_header():

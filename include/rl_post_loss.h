@@ -393,9 +393,8 @@ int linear_cross_entropy(const void* hidden, const void* weight, const void* bia
  * workspace            : layer_norm_workspace_bytes(rows, cols) bytes, 256-byte
  *                        aligned, no initial contents needed; one call in flight per workspace
  *
- * 1 <= rows < 2^31, 1 <= cols <= 65536.  Pointers aligned to their elements;
- * 16-byte aligned pointers with a row pitch of a multiple of 16 bytes are read
- * faster.  y may be x; the backward's outputs must not overlap its inputs.
+ * 1 <= rows < 2^31, 1 <= cols <= 65536.  Pointers aligned to their elements
+ * (any number of columns is read 16 bytes at a time).  y may be x; the backward's outputs must not overlap its inputs.
  */
 int layer_norm_fwd(const void* x, const void* weight, const void* bias, int64_t rows, int64_t cols, int dtype,
                    int weight_dtype, float eps, void* y, float* mean_out, float* rstd_out, hipStream_t stream);

@@ -24,13 +24,16 @@ struct NormFwdArgs {
     float eps;
 };
 
-// A forward kernel: `threads` lanes per row (64: four rows per workgroup of
-// 256), each holding up to `chunks` vectors of `vec` elements.
-struct NormFwdKernel {
+// A kernel whose workgroups of `threads` lanes hold rows_per_group rows at a time.
+struct NormRowKernel {
     const void* kernel;
     int threads, rows_per_group;
 };
-NormFwdKernel pick_norm_fwd(int dtype, int wdtype, bool vector, int64_t cols);
+NormRowKernel pick_norm_fwd(int dtype, int wdtype, int64_t cols);
+
+constexpr int64_t kNormHeldCols = 16384;   // longest row of the backward kernel that holds rows
+constexpr int64_t kNormHeldElements = 1 << 21;   // its workgroups times columns at most,
+constexpr int64_t kNormHeldGrid = 1024;          // and its workgroups
 
 struct NormBwdArgs {
     const void* dy;            // (rows, cols) dtype
@@ -39,14 +42,15 @@ struct NormBwdArgs {
     const float* mean;         // (rows)
     const float* rstd;         // (rows)
     void* dx;                  // (rows, cols) dtype, or NULL
-    float2* row_sums;          // (rows): mean over the columns of (dy w, dy w xhat)
-    float* part;               // (slabs, 2, cols): column sums of dy xhat and dy over a slab's rows, or NULL
+    float2* row_sums;          // (rows), rows longer than kNormHeldCols: mean over the columns of (dy w, dy w xhat)
+    float* part;               // (slabs or workgroups, 2, cols): column sums of dy xhat and dy over their rows, or NULL
     int64_t rows;
     int64_t slab_rows;         // rows per slab
     int32_t cols;
 };
-const void* pick_norm_row_sums(int dtype, int wdtype, bool vector);
-const void* pick_norm_bwd(int dtype, int wdtype, bool vector);
+NormRowKernel pick_norm_bwd_held(int dtype, int wdtype, int64_t cols);
+const void* pick_norm_row_sums(int dtype, int wdtype, int64_t cols);
+const void* pick_norm_bwd(int dtype, int wdtype, int64_t cols);
 
 // Sums the slabs' partials in slab order into the weight's and bias's gradients.
 struct NormReduceArgs {
@@ -56,10 +60,10 @@ struct NormReduceArgs {
     int32_t slabs, cols;
 };
 constexpr int kNormReduceCols = 32;        // columns per workgroup
+constexpr int kNormReduceThreads = 1024;
 const void* pick_norm_reduce(int wdtype);
 
-// Columns a workgroup of the column kernel covers, and how many slabs of rows
-// a (rows, cols) problem is split into (shared by the workspace's size and the launch).
-inline int64_t norm_col_tile(int dtype, bool vector) { return 64 * (vector ? (dtype == 0 ? 4 : 8) : 1); }
+// Columns a workgroup of norm_bwd covers.
+inline int64_t norm_col_tile(int dtype) { return 64 * (dtype == 0 ? 4 : 8); }
 
 }  // namespace rlpl

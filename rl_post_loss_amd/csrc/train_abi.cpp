@@ -264,15 +264,7 @@ bool norm_shape_ok(int64_t rows, int64_t cols) {
     return rows >= 1 && rows < kMaxRows && cols >= 1 && cols <= kNormMaxCols;
 }
 
-// Rows start on 16 bytes where every pointer does and the pitch is a multiple of 16 bytes.
-bool norm_vector(int64_t cols, int dtype, const void* p0, const void* p1, const void* p2, const void* p3,
-                 const void* p4) {
-    return (size_t(cols) * dtype_bytes(dtype)) % 16 == 0 && is_aligned(p0, 16) && is_aligned(p1, 16) &&
-           is_aligned(p2, 16) && is_aligned(p3, 16) && is_aligned(p4, 16);
-}
-
-// Slabs of rows of the backward pass: about 2048 workgroups, at least 16 rows
-// each (four a wavefront).  The narrow tile of unaligned rows bounds the workspace's size.
+// Slabs of rows of the backward pass of long rows: about 2048 workgroups, at least 16 rows each (four a wavefront).
 int64_t norm_slabs(int64_t rows, int64_t col_tiles) {
     int64_t slabs = 2048 / col_tiles;
     const int64_t most = div_up(rows, 16);
@@ -287,14 +279,29 @@ unsigned row_grid(int64_t rows, int per_group) {
     return unsigned(g < kNormMaxGrid ? g : kNormMaxGrid);
 }
 
+// Workgroups of the backward kernel that holds rows: four rows at least for each row a workgroup has at a time, so
+// that a row's loads overlap another's sums and the partials stay few, and more of them the shorter a row is
+// (shorter rows take fewer registers).
+int64_t norm_held_grid(int64_t rows, int64_t cols, int rows_per_group) {
+    const int64_t g = div_up(rows, 4 * rows_per_group);
+    int64_t most = kNormHeldElements / cols;
+    if (most > kNormHeldGrid) most = kNormHeldGrid;
+    return g < most ? g : most;
+}
+
 struct NormLayout {
     size_t sums, part, total;
 };
 NormLayout norm_layout(int64_t rows, int64_t cols) {
     NormLayout L{};
-    L.sums = up256(size_t(rows) * sizeof(float2));
-    // the widest column tile (512) gives the most slabs
-    L.part = up256(size_t(norm_slabs(rows, div_up(cols, 512))) * 2 * size_t(cols) * sizeof(float));
+    int64_t parts;
+    if (cols <= kNormHeldCols) {
+        parts = norm_held_grid(rows, cols, 1);                    // the most a kernel's shape asks for
+    } else {
+        L.sums = up256(size_t(rows) * sizeof(float2));
+        parts = norm_slabs(rows, div_up(cols, norm_col_tile(RLPL_F16)));   // so does the widest column tile
+    }
+    L.part = up256(size_t(parts) * 2 * size_t(cols) * sizeof(float));
     L.total = L.sums + L.part;
     return L;
 }
@@ -497,8 +504,7 @@ int layer_norm_fwd(const void* x, const void* weight, const void* bias, int64_t 
     const Device* d = nullptr;
     const int st = device(&d);
     if (st != RLPL_OK) return st;
-    const NormFwdKernel k =
-        pick_norm_fwd(dtype, weight_dtype, norm_vector(cols, dtype, x, y, weight, bias, nullptr), cols);
+    const NormRowKernel k = pick_norm_fwd(dtype, weight_dtype, cols);
     if (!k.kernel) return RLPL_ERR_DTYPE;
     const NormFwdArgs a{x, weight, bias, y, mean_out, rstd_out, rows, int32_t(cols), eps};
     return enqueue(k.kernel, a, dim3(row_grid(rows, k.rows_per_group)), k.threads, stream);
@@ -524,10 +530,8 @@ int layer_norm_bwd(const void* grad_y, const void* x, const void* weight, const 
     const Device* d = nullptr;
     int st = device(&d);
     if (st != RLPL_OK) return st;
-    const bool vector = norm_vector(cols, dtype, grad_y, x, grad_x, weight, nullptr);
-    const int64_t col_tiles = div_up(cols, norm_col_tile(dtype, vector));
-    const int64_t slabs = norm_slabs(rows, col_tiles);
     const bool sums = grad_weight || grad_bias;
+    if (!grad_x && !sums) return RLPL_OK;
     NormBwdArgs a{};
     a.dy = grad_y;
     a.x = x;
@@ -538,19 +542,26 @@ int layer_norm_bwd(const void* grad_y, const void* x, const void* weight, const 
     a.row_sums = static_cast<float2*>(workspace);
     a.part = sums ? reinterpret_cast<float*>(static_cast<char*>(workspace) + L.sums) : nullptr;
     a.rows = rows;
-    a.slab_rows = div_up(rows, slabs);
     a.cols = int32_t(cols);
-    if (grad_x) {
-        st = enqueue(pick_norm_row_sums(dtype, weight_dtype, vector), a, dim3(row_grid(rows, kNormThreads / 64)),
-                     kNormThreads, stream);
-        if (st != RLPL_OK) return st;
+    int64_t slabs;
+    if (cols <= kNormHeldCols) {
+        const NormRowKernel k = pick_norm_bwd_held(dtype, weight_dtype, cols);
+        slabs = norm_held_grid(rows, cols, k.rows_per_group);
+        st = enqueue(k.kernel, a, dim3(unsigned(slabs)), k.threads, stream);
+    } else {
+        const int64_t col_tiles = div_up(cols, norm_col_tile(dtype));
+        slabs = norm_slabs(rows, col_tiles);
+        a.slab_rows = div_up(rows, slabs);
+        if (grad_x) {
+            st = enqueue(pick_norm_row_sums(dtype, weight_dtype, cols), a, dim3(row_grid(rows, kNormThreads / 64)), kNormThreads,
+                         stream);
+            if (st != RLPL_OK) return st;
+        }
+        st = enqueue(pick_norm_bwd(dtype, weight_dtype, cols), a, dim3(unsigned(col_tiles), unsigned(slabs)), kNormThreads, stream);
     }
-    if (!grad_x && !sums) return RLPL_OK;
-    st = enqueue(pick_norm_bwd(dtype, weight_dtype, vector), a, dim3(unsigned(col_tiles), unsigned(slabs)), kNormThreads,
-                 stream);
     if (st != RLPL_OK || !sums) return st;
     const NormReduceArgs r{a.part, grad_weight, grad_bias, int32_t(slabs), int32_t(cols)};
-    return enqueue(pick_norm_reduce(weight_dtype), r, dim3(unsigned(div_up(cols, kNormReduceCols)), 2), kNormThreads,
+    return enqueue(pick_norm_reduce(weight_dtype), r, dim3(unsigned(div_up(cols, kNormReduceCols)), 2), kNormReduceThreads,
                    stream);
 }
 

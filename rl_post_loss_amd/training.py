@@ -33,7 +33,7 @@ def _on(device: torch.device):
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)   # the current stream's handle, without a Stream object
 
 
 def _ptr(t: Optional[torch.Tensor]):

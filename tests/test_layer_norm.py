@@ -104,7 +104,7 @@ def backward_case(c, mean, rstd, out):
 
 
 SHAPES = [(1, 1), (1, 4096), (3, 2), (5, 7), (4, 64), (17, 1000), (33, 512), (9, 513), (130, 1024), (7, 2048), (6, 2056),
-          (257, 96), (3, 4100), (5, 8192), (2, 16384), (2, 16385), (3, 12345), (1, 65536), (2, 65535), (1500, 40)]
+          (257, 96), (3, 4100), (5, 8192), (2, 16384), (2, 16385), (3, 12345), (40, 16384), (9, 12000), (300, 130), (100, 15), (40, 9000), (1, 65536), (2, 65535), (1500, 40)]
 
 
 @gpu
@@ -313,4 +313,5 @@ def test_refusals_of_the_binding():
     with pytest.raises(rl.RlplError, match="SHAPE"):
         rl.layer_norm_fwd(torch.zeros(0, 32, device=DEV))
     with pytest.raises(rl.RlplError, match="WORKSPACE"):
-        rl.layer_norm_bwd(c["dy"], c["x"], c["w"], mean, rstd, workspace=torch.empty(300, dtype=torch.uint8, device=DEV))
+        rl.layer_norm_bwd(c["dy"], c["x"], c["w"], mean, rstd, workspace=torch.empty(
+            rl.library().layer_norm_workspace_bytes(4, 32) - 1, dtype=torch.uint8, device=DEV))

@@ -33,7 +33,8 @@ NormRowKernel pick_norm_fwd(int dtype, int wdtype, int64_t cols);
 
 constexpr int64_t kNormHeldCols = 16384;   // longest row of the backward kernel that holds rows
 constexpr int64_t kNormHeldElements = 1 << 21;   // its workgroups times columns at most,
-constexpr int64_t kNormHeldGrid = 1024;          // and its workgroups
+constexpr int64_t kNormHeldGrid = 1024;          // and its workgroups, which may be one a compute unit
+constexpr int64_t kNormHeldLeast = 256;
 
 struct NormBwdArgs {
     const void* dy;            // (rows, cols) dtype

@@ -286,6 +286,7 @@ int64_t norm_held_grid(int64_t rows, int64_t cols, int rows_per_group) {
     const int64_t g = div_up(rows, 4 * rows_per_group);
     int64_t most = kNormHeldElements / cols;
     if (most > kNormHeldGrid) most = kNormHeldGrid;
+    if (most < kNormHeldLeast) most = kNormHeldLeast;
     return g < most ? g : most;
 }
 

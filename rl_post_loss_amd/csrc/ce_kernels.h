@@ -15,15 +15,17 @@ constexpr int kCeDynLds = 160 * 1024;      // the products' LDS ring: all of a c
 constexpr int64_t kCeMaxRows = int64_t(1) << 24;
 constexpr int kCeMaxSplits = 16;
 
-// What the compaction leaves on the device: the number of rows that count, and (after
-// the loss) the factor of the gradients: 1 / max(count, 1) or 1, over the scale dz is held at.
+// What the compaction leaves on the device: the number of rows that count, (after the loss) the
+// factor of the gradients: 1 / max(count, 1) or 1, over the scale dz is held at, and how many workgroups
+// of ce_row are done with their rows.
 struct CeState {
     int32_t count;
     float scale;
+    uint32_t done;
 };
 
-// Rows whose target is not ignore_index, in order.
-struct CeCompactArgs {
+// The rows whose target is not ignore_index, in order, and their hidden states side by side.
+struct CePrepareArgs {
     const int64_t* targets;    // (n)
     int64_t ignore_index, vocab;
     int32_t n;
@@ -31,17 +33,16 @@ struct CeCompactArgs {
     int32_t* place;            // (n): place of a row among the kept ones, or -1
     int32_t* target;           // (n): target of the k-th kept row, -1 where it is outside [0, vocab)
     CeState* state;
-};
-const void* ce_compact_kernel();
-
-// The kept rows of hidden, side by side.
-struct CeGatherArgs {
     const void* hidden;        // (n, cols) 2-byte elements, cols a multiple of 8
-    void* out;
-    const int32_t* row;
-    const CeState* state;
+    void* out;                 // (kept rows, cols)
     int32_t cols;
 };
+// Up to kCePrepareRows rows in one kernel, a workgroup a row, each counting the kept rows before its own; more in
+// two: one workgroup's scan, then the copy.  The one kernel's time grows with n^2: it takes 3.0 us at 200
+// rows, 4.8 at 1024 and 8 at 2048, where the two take 6 to 7, and a launch more.
+constexpr int64_t kCePrepareRows = 2048;
+const void* ce_prepare_kernel();
+const void* ce_compact_kernel();
 const void* ce_gather_kernel();
 
 // One of the step's four products (the kernel's template argument):
@@ -97,54 +98,51 @@ struct CeGemmArgs {
     float z_loss2;             // 2 z_loss (kCeDlogits)
     float* part;               // (kept rows, tiles_n, 2) (kCeLogits)
     float* target_logit;       // (kept rows) (kCeLogits)
-    float* col_part;           // (tiles_m, N) column sums of dz over a tile's rows, or NULL (kCeDlogits)
+    float* col_part;           // (tiles_m, col_ld) from column 0 on: sums of dz over a tile's rows, or NULL (kCeDlogits)
+    int64_t col_ld;
 };
-const void* pick_ce_gemm(int dtype, int product);
+const void* pick_ce_gemm(int dtype, int product);   // kCeLogits or kCeDlogits
+
+// The two products that take dz, in one launch: the first hidden_blocks workgroups (a multiple of 8, or 0) are the
+// hidden product's, the others the weight's.  Their tiles share the chip, so neither ends with idle compute units.
+struct CeGradArgs {
+    CeGemmArgs hidden, weight;
+    uint32_t hidden_blocks;
+};
+const void* pick_ce_grads(int dtype);
 
 // dz is held at this scale (the onehot's 1), so that small probabilities stay
 // above fp16's subnormals; bf16 has float32's range.
 inline float ce_dz_scale(int dtype) { return dtype == 1 ? 256.0f : 1.0f; }
 
-// A kept row's log-sum-exp and loss.
+// A kept row's log-sum-exp and loss; the workgroup that is done last sums the rows' losses.
 struct CeRowArgs {
     const float* part;
     const float* target_logit;
     const int32_t* target;
-    const CeState* state;
+    CeState* state;
     float* lse;                // (kept rows)
     float* row_loss;           // (kept rows)
-    float z_loss;
-    int32_t tiles;
+    float* loss;
+    float z_loss, inv_dz_scale;
+    int32_t tiles, mean;
 };
+constexpr int64_t kCeRowGrid = 512;
 const void* ce_row_kernel();
 
-// The loss from the rows', and the gradients' factor.
-struct CeLossArgs {
-    const float* row_loss;
-    CeState* state;
-    float* loss;
-    float inv_dz_scale;
-    int32_t mean;
-};
-const void* ce_loss_kernel();
-
-// The hidden gradient: the splits' planes of a kept row summed in order and scaled, zeros in an ignored row.
-struct CeHiddenArgs {
+// The hidden gradient: the splits' planes of a kept row summed in order and scaled, zeros in an ignored row; and, by
+// the workgroups after the first row_blocks, the bias's gradient: the row tiles' column sums, likewise.
+struct CeFinishArgs {
     const float* part;
     const int32_t* place;
     const CeState* state;
     void* out;                 // (n, cols)
     int32_t n, cols, split_k, max_splits;
+    uint32_t row_blocks;       // 0: no hidden gradient
+    const float* col_part;     // (tiles, vocab)
+    void* bias;                // (vocab) operand dtype or float32
+    int32_t vocab, out_f32, accumulate;
 };
-const void* pick_ce_hidden(int dtype);
-
-// The bias's gradient of a piece: the row tiles' column sums added in order and scaled.
-struct CeBiasArgs {
-    const float* part;         // (tiles, cols)
-    const CeState* state;
-    void* out;                 // (cols) operand dtype or float32
-    int32_t cols, out_f32, accumulate;
-};
-const void* pick_ce_bias(int dtype);
+const void* pick_ce_finish(int dtype);
 
 }  // namespace rlpl

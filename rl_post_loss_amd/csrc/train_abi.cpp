@@ -130,6 +130,10 @@ CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
     if (grads) {
         int64_t piece = kCePieceElements / n / large * large;
         if (piece < kCePieceCols) piece = kCePieceCols;
+        // whole rounds of 256 tiles where a piece has several (6001 x 2048 x 50021 with half of the rows ignored: ten
+        // rounds of logits instead of twelve)
+        const int64_t row_tiles = div_up(n, large), rounds = piece / large * row_tiles / 256;
+        if (rounds > 0) piece = rounds * 256 / row_tiles * large;
         const int64_t all = div_up(vocab, large) * large;
         L.piece = piece < all ? piece : all;
         // planes for up to kCeMaxSplits splits of K, for as many rows as may come with each number of splits

@@ -245,6 +245,7 @@ class AdamWPlan:
             _pointers(exp_avg_sq_scale) if eight else None, 8 if eight else 32,
             (ctypes.c_double * count)(*weight_decay)))
         self._device = torch.from_numpy(self._host.view(np.int64)).to(self.device)
+        self._made_on = _stream(self.device)
 
     def moments(self, i: int):
         """The first and second moment of tensor i in float32, in its shape (8-bit states as the values they stand for)."""
@@ -370,8 +371,11 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], *, step
     step_at = _device_scalar(step, "step", torch.int64, dev) if isinstance(step, torch.Tensor) else None
     lr_at = _device_scalar(lr, "lr", torch.float32, dev) if isinstance(lr, torch.Tensor) else None
     scale_at = None if grad_scale is None else _device_scalar(grad_scale, "grad_scale", torch.float32, dev)
+    stream = _stream(dev)
+    if stream != plan._made_on and not torch.cuda.is_current_stream_capturing():
+        plan._device.record_stream(torch.cuda.current_stream(dev))   # a plan dropped right after is still read there
     with _on(dev):
         _check("rlpl_adamw_step", library().rlpl_adamw_step(
             plan._host.ctypes.data, plan._device.data_ptr(), pointers, DTYPE[gdt], 0.0 if lr_at else float(lr), lr_at,
             float(beta1), float(beta2), float(eps), 1 if step_at else int(step), step_at, scale_at,
-            int(seed) & 0xFFFFFFFF, _stream(dev)))
+            int(seed) & 0xFFFFFFFF, stream))

@@ -16,9 +16,10 @@ def mix(x):
     return x ^ (x >> np.uint64(16))
 
 
-def random_words(seed, step, tensor, n):
+def random_words(seed, step, tensor, n, start=0):
+    """The words of elements start .. start + n (which share their upper 32 bits)."""
     key = mix(mix(mix(seed) ^ np.uint64(step & 0xFFFFFFFF)) ^ np.uint64(tensor))
-    i = np.arange(n, dtype=np.uint64)
+    i = np.arange(n, dtype=np.uint64) + np.uint64(start)
     return mix((i & np.uint64(0xFFFFFFFF)) ^ mix(key + (i >> np.uint64(32))))
 
 

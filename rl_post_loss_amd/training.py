@@ -27,13 +27,21 @@ REDUCTION = {"mean": 0, "sum": 1}
 BLOCK = 256   # values of an 8-bit moment that share one scale
 
 
+_HERE = nullcontext()
+
+
 def _on(device: torch.device):
     """The device as the current one: the library launches on the current device."""
-    return nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)   # the current stream's handle, without a Stream object
+
+
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    t = t if t.is_contiguous() else t.contiguous()
+    return t.detach() if t.requires_grad else t
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -145,7 +153,7 @@ def _norm_rows(x: torch.Tensor, name: str) -> torch.Tensor:
         raise TypeError(f"{name} must be float32, float16 or bfloat16")
     if x.numel() == 0:
         _check("layer_norm", 2)
-    return x.detach().contiguous()
+    return _dense(x)
 
 
 def _norm_vector(v: Optional[torch.Tensor], name: str, x: torch.Tensor) -> Optional[torch.Tensor]:
@@ -153,9 +161,9 @@ def _norm_vector(v: Optional[torch.Tensor], name: str, x: torch.Tensor) -> Optio
         return None
     if not isinstance(v, torch.Tensor) or v.dtype not in (x.dtype, torch.float32):
         raise TypeError(f"{name} must be a tensor of the input's dtype or float32")
-    if tuple(v.shape) != (x.shape[-1],) or v.device != x.device:
+    if v.dim() != 1 or v.shape[0] != x.shape[-1] or v.device != x.device:
         raise ValueError(f"{name} must have shape ({x.shape[-1]},) on the input's device")
-    return v.detach().contiguous()
+    return _dense(v)
 
 
 def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5):
@@ -169,7 +177,7 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5):
     H = x.shape[-1]
     rows = x.numel() // H
     y = torch.empty_like(x)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
     rstd = torch.empty_like(mean)
     wt = w if w is not None else b
     with _on(x.device):
@@ -191,13 +199,13 @@ def layer_norm_bwd(grad_y, x, weight, mean, rstd, *, need_x=True, need_weight=Tr
     for name, t in (("mean", mean), ("rstd", rstd)):
         if t.dtype != torch.float32 or t.shape != x.shape[:-1] or t.device != x.device:
             raise ValueError(f"{name} must be the forward's float32 tensor of shape {tuple(x.shape[:-1])}")
-    mean, rstd = mean.detach().contiguous(), rstd.detach().contiguous()
+    mean, rstd = _dense(mean), _dense(rstd)
     H = x.shape[-1]
     rows = x.numel() // H
     wdt = x.dtype if w is None else w.dtype
     dx = torch.empty_like(x) if need_x else None
-    dw = torch.empty(H, dtype=wdt, device=x.device) if need_weight and w is not None else None
-    db = torch.empty(H, dtype=wdt, device=x.device) if need_bias else None
+    dw = torch.empty_like(w) if need_weight and w is not None else None
+    db = (x.new_empty(H) if w is None else torch.empty_like(w)) if need_bias else None
     lib = library()
     ws = _scratch(lib.layer_norm_workspace_bytes(rows, H), workspace, x.device, "layer_norm_workspace_bytes")
     wp, wn = _ws_ptr(ws)

@@ -315,7 +315,7 @@ enum rlpl_reduction { RLPL_REDUCE_MEAN = 0, RLPL_REDUCE_SUM = 1 };
 /*
  * Softmax cross entropy of an output projection over a large vocabulary, with
  * its gradients, in pieces of the vocabulary (the supervised sibling of the
- * selective log-probabilities: the logits are never kept).  Over the rows i
+ * selective log-probabilities: no more than one piece's logits are held).  Over the rows i
  * whose target y_i is not ignore_index, N of them,
  *
  *   z_i  = hidden[i] . weight^T + bias,   lse_i = log sum_v exp(z_i[v])
@@ -350,8 +350,9 @@ enum rlpl_reduction { RLPL_REDUCE_MEAN = 0, RLPL_REDUCE_SUM = 1 };
  * accumulate  : nonzero adds to grad_weight and grad_bias (RLPL_F32 only), else they are overwritten
  * workspace   : linear_cross_entropy_workspace_bytes(n, hidden_size, vocab, gradients wanted) bytes,
  *               256-byte aligned, no initial contents needed; one call in flight
- *               per workspace.  With gradients it holds one piece of dz: 256 MiB, or 16 KiB a row
- *               where that is more
+ *               per workspace.  With gradients it holds one piece: up to 256 MiB of dz and 512 MiB of
+ *               logits, or 16 KiB of dz a row where that is more
+ * Outputs overlap neither each other nor an input.
  *
  * Shapes: 1 <= n <= 2^24, hidden_size a multiple of 8 in [8, 65536], 1 <= vocab < 2^22 and fewer than 2^22
  * tiles of 256 rows by 256 vocabulary entries, 2^18 of 256 rows by 256 hidden values; 0 <= z_loss <= 1.

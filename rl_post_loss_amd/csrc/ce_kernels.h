@@ -46,8 +46,8 @@ struct CePrepareArgs {
     int32_t cols;
 };
 // Up to kCePrepareRows rows in one kernel, a workgroup a row, each counting the kept rows before its own; more in
-// two: one workgroup's scan, then the copy.  The one kernel's time grows with n^2: it takes 3.0 us at 200
-// rows, 4.8 at 1024 and 8 at 2048, where the two take 6 to 7, and a launch more.
+// two: one workgroup's scan, then the copy.  The one kernel's counting grows with n^2: 200 rows of 512 take 2.8 us,
+// 1024 of 4096 7.6 and 2048 of 4096 10.7; the two kernels take 10.8 + 7.4 for 6001 rows of 2048, half of them kept.
 constexpr int64_t kCePrepareRows = 2048;
 const void* ce_prepare_kernel();
 const void* ce_compact_kernel();
@@ -116,8 +116,11 @@ struct CeGemmArgs {
     float* target_logit;       // (kept rows) (kCeLogits)
     float* col_part;           // (tiles_m, col_ld) from column 0 on: sums of dz over a tile's rows, or NULL (kCeDlogits)
     int64_t col_ld;
+    float* kept;               // the logits of the first kept_cols columns (a multiple of 256, or 0) and M rows, up to a
+    int32_t kept_cols;         // multiple of 16; written by kCeLogits
 };
 const void* pick_ce_gemm(int dtype, bool small, int product);   // kCeLogits or kCeDlogits
+const void* pick_ce_dz(int dtype, bool small);                  // kCeDlogits of the kept columns
 
 // The two products that take dz, in one launch: the first hidden_blocks workgroups (a multiple of 8, or 0) are the
 // hidden product's, the others the weight's.  Their tiles share the chip, so neither ends with idle compute units.

@@ -1,6 +1,6 @@
 // Softmax cross entropy of an output projection over a large vocabulary on
-// gfx950, with its gradients, in pieces of the vocabulary: no kernel writes
-// logits.  For the rows i whose target y_i is not ignored (N of them),
+// gfx950, with its gradients, in pieces of the vocabulary: never more than one
+// piece's logits are held.  For the rows i whose target y_i is not ignored (N of them),
 //
 //   z_i = hidden_i . weight^T + bias,   lse_i = log sum_v exp(z_iv)
 //   loss = s sum_i (lse_i - z_i[y_i] + c lse_i^2),   s = 1 / max(N, 1) or 1
@@ -13,15 +13,21 @@
 //
 // Loss: each 256 x 256 tile of logits is reduced in registers to its rows'
 // (max, sum exp) and target logit; one kernel joins a row's tiles.  Gradient,
-// per piece of the vocabulary: the piece's logits are formed again (less
-// traffic and memory than keeping n x V of them), dz goes to the workspace in
-// the operand dtype, and two products take it from there.  The weight's
-// gradient of a piece comes out whole, so it is rounded once and written once;
+// per piece of the vocabulary: dz goes to the workspace in the operand dtype,
+// from the float32 logits that the loss's pass left of the first piece, or from logits
+// formed again (n x V of them would take 4 bytes each), and two products take
+// it from there.  The weight's gradient of a piece comes out whole, so it is rounded once and written once;
 // the hidden states' is summed over the pieces in float32.
 //
 // dz is formed without s and held at a fixed scale (its largest value is
 // about 1): s would push a long batch's small probabilities under fp16's
 // range.  The factor is applied to the float32 results.
+//
+// What bounds it: the products, 6 n H V operations (8 where logits are formed again), where n is large, and
+// there the port of LDS.  A step of 64 of K over a 256 x 256 tile has 2048 cycles of matrix instructions;
+// its fragment reads take 1573 alone and its copies 1863, both 2575 together, the step 2860 (8192^3,
+// 1.37 PFLOP/s; 1.22 at 1024 x 4096 x 128256).  Few rows are bound by the weight's bytes: 16 rows of 4096 x 128256
+// read it at 4.4 to 5.5 TB/s (logits 190 to 237 us), and write its gradient beside (483 to 525).
 //
 // The contraction and its tiles are those of mfma_tile.h.
 #include <hip/hip_runtime.h>
@@ -336,6 +342,14 @@ __global__ void __launch_bounds__(kCeThreads) ce_gather(const CePrepareArgs a) {
     for (int k = blockIdx.x; k < count; k += gridDim.x) copy_row(a, a.row[k], k);
 }
 
+// The first piece's logits, kept as the lanes hold them: 16 x 16 blocks of 64 lanes' four values, a wavefront's
+// columns side by side, rows in blocks of 16 after one another.
+template <typename S>
+__device__ __forceinline__ float* kept_at(const CeGemmArgs& g, int m0, uint32_t tn, int wm, int wn, int i, int lane) {
+    const int64_t rows = int64_t(tn * S::kWavesN + wn) * ((g.M + 15) / 16) + (m0 + wm * S::kWaveM) / 16 + i;
+    return g.kept + rows * (S::kColTiles * 256) + 4 * lane;
+}
+
 // One tile of a product: workgroup `block` of those the launch has for it.  A_KCONTIG, B_KCONTIG: the operands'
 // layouts (mfma_tile.h).
 template <typename T, typename S, int PRODUCT, bool A_KCONTIG, bool B_KCONTIG>
@@ -571,6 +585,16 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
             for (int e = 0; e < 4; ++e) acc[i][j][e] += b;
     }
 
+    if (PRODUCT == kCeLogits && n0 < g.kept_cols) {
+#pragma unroll
+        for (int i = 0; i < S::kRowTiles; ++i) {
+            if (m0 + wm * S::kWaveM + i * 16 >= M) break;
+            float* to = kept_at<S>(g, m0, tn, wm, wn, i, lane);
+#pragma unroll
+            for (int j = 0; j < S::kColTiles; ++j) *reinterpret_cast<floatx4*>(to + 256 * j) = acc[i][j];
+        }
+    }
+
     if constexpr (PRODUCT == kCeDlogits) {
         float* row_lse = reinterpret_cast<float*>(ring + kTileBytes<S>);
         float* row_f = row_lse + S::BM;
@@ -677,6 +701,77 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
     if constexpr (kMerge == 4) sum += quad_xor<2>(sum);
     if (threadIdx.x % kMerge == 0 && row < M)
         reinterpret_cast<float2*>(g.part)[int64_t(row) * g.tiles_n + tn] = make_float2(top, sum);
+}
+
+// dz of the piece whose logits were kept (the first one), bit for bit what ce_tile forms: a workgroup a tile, a wavefront its own
+// blocks of it, each turned to whole rows in a strip of LDS of its own (1024 x 128256: 150 us, 5.3 TB/s).
+template <typename T, typename S>
+__global__ void __launch_bounds__(S::kThreads) ce_dz(const CeGemmArgs g) {
+    constexpr int kPitch = 2 * S::kWaveN + 16, kLanes = S::kWaveN / 8;      // bytes of a row in the strip, lanes of its store
+    __shared__ __attribute__((aligned(16))) char strips[S::kWaves][16 * kPitch];
+    __shared__ float sums[S::kWavesM][S::BN];
+    const int M = min(g.M, g.state->count);
+    const uint32_t tiles_m = uint32_t(M + S::BM - 1) / uint32_t(S::BM);
+    if (blockIdx.x >= tiles_m * g.tiles_n) return;
+    const uint32_t tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
+    const int m0 = int(tm) * S::BM, n0 = int(tn) * S::BN;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / S::kWavesN, wn = wave % S::kWavesN, odd = lane & 1;
+    char* strip = strips[wave];
+    float sum[S::kColTiles] = {};
+#pragma unroll 2
+    for (int i = 0; i < S::kRowTiles; ++i) {
+        const int row0 = m0 + wm * S::kWaveM + i * 16;
+        if (row0 >= M) break;
+        const float* from = kept_at<S>(g, m0, tn, wm, wn, i, lane);
+        floatx4 z[S::kColTiles];
+#pragma unroll
+        for (int j = 0; j < S::kColTiles; ++j) z[j] = *reinterpret_cast<const floatx4*>(from + 256 * j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = row0 + 4 * (lane >> 4) + e;
+            const float lse = row < M ? g.lse[row] : 0.0f;
+            const float f = row < M ? kDzScale<T> * (1.0f + g.z_loss2 * lse) : 0.0f;
+            const int target = row < M ? g.target[row] : -1;
+#pragma unroll
+            for (int j = 0; j < S::kColTiles; ++j) {
+                const int col = n0 + wn * S::kWaveN + j * 16 + (lane & 15);
+                const float p = __builtin_amdgcn_exp2f((z[j][e] - lse) * kLog2eG);
+                z[j][e] = (f != 0.0f ? f * p : 0.0f) - (col == target && col < g.N ? kDzScale<T> : 0.0f);
+                sum[j] += z[j][e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+#pragma unroll
+            for (int j = 0; j < S::kColTiles; ++j) {
+                const float a = z[j][e], b = z[j][e + 1], got = swap_pair(odd ? a : b);
+                *reinterpret_cast<uint32_t*>(strip + (4 * (lane >> 4) + e + odd) * kPitch + 32 * j + 2 * ((lane & 15) - odd)) =
+                    Elem<T>::pack(odd ? got : a, odd ? b : got);
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int c = lane % kLanes;
+#pragma unroll
+        for (int r = lane / kLanes; r < 16; r += 64 / kLanes)
+            if (row0 + r < M)
+                *reinterpret_cast<u32x4*>(static_cast<T*>(g.c) + int64_t(row0 + r) * g.ldc + n0 + wn * S::kWaveN + 8 * c) =
+                    *reinterpret_cast<const u32x4*>(strip + r * kPitch + 16 * c);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    if (!g.col_part) return;
+#pragma unroll
+    for (int j = 0; j < S::kColTiles; ++j) {
+        float s = sum[j];
+        s += __shfl_xor(s, 16, 64);
+        s += __shfl_xor(s, 32, 64);
+        if (lane < 16) sums[wm][wn * S::kWaveN + j * 16 + lane] = s;
+    }
+    __syncthreads();
+    const int col = n0 + int(threadIdx.x);
+    if (threadIdx.x < S::BN && col < g.N)
+        g.col_part[int64_t(tm) * g.col_ld + col] = sums[0][threadIdx.x] + sums[1][threadIdx.x];
 }
 
 template <typename T, typename S, int PRODUCT>
@@ -819,6 +914,12 @@ const void* pick_ce_grads(int dtype, bool small) {
                      : reinterpret_cast<const void*>(&ce_grads<_Float16, Large>);
     return small ? reinterpret_cast<const void*>(&ce_grads<__bf16, Small>)
                  : reinterpret_cast<const void*>(&ce_grads<__bf16, Large>);
+}
+const void* pick_ce_dz(int dtype, bool small) {
+    if (dtype == kF16)
+        return small ? reinterpret_cast<const void*>(&ce_dz<_Float16, Small>)
+                     : reinterpret_cast<const void*>(&ce_dz<_Float16, Large>);
+    return small ? reinterpret_cast<const void*>(&ce_dz<__bf16, Small>) : reinterpret_cast<const void*>(&ce_dz<__bf16, Large>);
 }
 const void* ce_prepare_kernel() { return reinterpret_cast<const void*>(&ce_prepare); }
 const void* ce_compact_kernel() { return reinterpret_cast<const void*>(&ce_compact); }

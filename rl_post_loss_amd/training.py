@@ -18,6 +18,8 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
+from torch.autograd.graph import increment_version
+
 from . import DTYPE, _aligned, _check, _ws_ptr, library
 
 __all__ = ["linear_cross_entropy", "linear_cross_entropy_fwd", "layer_norm_fwd", "layer_norm_bwd", "adamw_plan", "adamw_step", "AdamWPlan"]
@@ -103,8 +105,8 @@ def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_
                          need_hidden=True, need_weight=True, need_bias=True, weight_grad_dtype=None, grad_weight=None,
                          grad_bias=None, workspace=None):
     """Softmax cross entropy of the logits hidden . weight^T + bias, with its gradients, in pieces of the vocabulary
-    (no more than one piece's logits are held): (loss, grad_hidden, grad_weight, grad_bias), None for gradients not wanted and for
-    a bias that is not there.
+    (no more than one piece's logits are held): (loss, grad_hidden, grad_weight, grad_bias), None for gradients not
+    wanted and for a bias that is not there (unless its gradient is passed to be added to).
 
     hidden (*, H) and weight (V, H) float16 or bfloat16, H a multiple of 8; bias (V,) or None; targets int64, of hidden's
     leading shape.  Rows whose target is ``ignore_index`` do not count.  loss is the mean (or sum) over the others of
@@ -114,7 +116,7 @@ def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_
     ``grad_weight`` / ``grad_bias`` (contiguous float32) adds to them, over groups of tokens or micro-batches."""
     x, w, b, y = _ce_operands(hidden, weight, bias, targets, reduction)
     (n, H), V, dev, lib = x.shape, w.shape[0], x.device, library()
-    need_bias = need_bias and b is not None
+    need_bias = need_bias and (b is not None or grad_bias is not None)
     accumulate = grad_weight is not None or grad_bias is not None
     if accumulate:
         if weight_grad_dtype not in (None, torch.float32):
@@ -387,3 +389,7 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], *, step
             plan._host.ctypes.data, plan._device.data_ptr(), pointers, DTYPE[gdt], 0.0 if lr_at else float(lr), lr_at,
             float(beta1), float(beta2), float(eps), 1 if step_at else int(step), step_at, scale_at,
             int(seed) & 0xFFFFFFFF, stream))
+    written = plan.params + (plan.copies or [])
+    if any(g is None for g in grads):
+        written = [p for p, g in zip(written, grads + grads) if g is not None]
+    increment_version(written)   # a graph that saved an old value says so in its backward pass

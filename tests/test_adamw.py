@@ -279,6 +279,23 @@ def test_moments_resumed_from_given_tensors_and_in_their_shape():
     same("exp_avg", a.exp_avg[0], b.exp_avg[0])
 
 
+@gpu
+def test_a_graph_that_saved_an_old_value_says_so():
+    p = torch.nn.Parameter(torch.ones(300, device=DEV))
+    copy = torch.ones(300, dtype=torch.bfloat16, device=DEV, requires_grad=True)
+    plan = rl.adamw_plan([p], copies=[copy])
+    losses = [(p * p).sum(), (copy * copy).sum()]
+    rl.adamw_step(plan, [torch.ones(300, device=DEV)], step=1, **HYPER)
+    for loss in losses:
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    (p * p).sum().backward()
+    assert torch.equal(p.grad, 2 * p.detach())
+    loss = (p * p).sum()
+    rl.adamw_step(plan, [None], step=2, **HYPER)         # nothing was written
+    loss.backward()
+
+
 # ------------------------------------------------------------------------------------------------------- refusals
 
 A = 0x7F0000001000

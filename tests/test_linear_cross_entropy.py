@@ -253,6 +253,20 @@ def test_wanted_gradients_leading_dimensions_and_repeats():
 
 
 @gpu
+def test_a_bias_gradient_passed_without_a_bias_is_added_to():
+    c = make(70, 40, 300, bias=False, seed=2)
+    args = on_device(c)
+    zero = torch.zeros(300, dtype=torch.bfloat16, device=DEV)
+    want = rl.linear_cross_entropy(args[0], args[1], zero, args[3], weight_grad_dtype=torch.float32)
+    dw, db = torch.ones(300, 40, device=DEV), torch.ones(300, device=DEV)
+    out = rl.linear_cross_entropy(*args, grad_weight=dw, grad_bias=db)
+    assert out[3] is db and torch.equal(db, 1.0 + want[3]) and torch.equal(dw, 1.0 + want[2])
+    only = torch.ones(300, device=DEV)
+    out = rl.linear_cross_entropy(*args, need_weight=False, grad_bias=only)
+    assert out[2] is None and torch.equal(only, db)
+
+
+@gpu
 def test_gradients_against_differences():
     """Central differences of the float64 loss, step 1e-5 (their own error is below 1e-8): what is left is the
     gradients' tolerance as above."""

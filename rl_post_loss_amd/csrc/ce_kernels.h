@@ -13,12 +13,13 @@ constexpr int kCeThreads = 256;            // workgroups of the row and column k
 constexpr int kCeCompactThreads = 1024;
 // The shapes of the products' tiles: `tile` rows by columns, workgroups of `threads` with a ring of `lds` bytes.  For
 // the splits of K: how many run at once, and, in quarters of a K step, what a workgroup's first copies and epilogue
-// cost and what a plane's sum at the end does.
+// cost (of the hidden product, of the weight's), what a plane's sum at the end does, and how many of a plane's
+// tiles take one more (their bytes).
 struct CeShape {
-    int tile, threads, lds, at_once, extra, plane;
+    int tile, threads, lds, at_once, extra, weight_extra, plane, plane_tiles;
 };
-constexpr CeShape kCeLarge{256, 512, 160 * 1024, 256, 48, 1};
-constexpr CeShape kCeSmall{64, 256, 32 * 1024, 1280, 24, 3};
+constexpr CeShape kCeLarge{256, 512, 160 * 1024, 256, 48, 28, 1, 3};
+constexpr CeShape kCeSmall{64, 256, 32 * 1024, 1280, 24, 24, 3, 32};
 constexpr int64_t kCeMaxRows = int64_t(1) << 24;
 constexpr int kCeMaxSplits = 64;
 
@@ -60,40 +61,6 @@ const void* ce_gather_kernel();
 //   kCeWeight   dz^T . hidden of a piece, scaled, in the gradient's dtype
 // with z = hidden . weight^T + bias.  A (M x K) and B (K x N) as in GemmArgs.
 enum { kCeLogits = 0, kCeDlogits = 1, kCeHidden = 2, kCeWeight = 3 };
-
-// Splits of the hidden product's K: the number, at most `most` (64), that takes the least time.  A piece's tiles
-// number as few as the rows that count allow, which the device alone knows: ce_row asks for them there (a lane a
-// number), the host for the planes that any count may need.
-#ifdef __HIPCC__
-__host__ __device__
-#endif
-inline uint32_t ce_split_time(uint32_t tiles, int32_t split_k, uint32_t s, const CeShape& shape) {
-    const uint32_t at_once = uint32_t(shape.at_once), steps = uint32_t(split_k + kGemmBK - 1) / kGemmBK;
-    return (tiles * s + at_once - 1) / at_once * (4 * ((steps + s - 1) / s) + uint32_t(shape.extra)) + s * uint32_t(shape.plane);
-}
-// Products of more tiles than this are not split.
-#ifdef __HIPCC__
-__host__ __device__
-#endif
-inline uint32_t ce_split_tiles(const CeShape& shape) { return 4 * uint32_t(shape.at_once); }
-inline uint32_t ce_splits(uint32_t tiles, int32_t split_k, int32_t most, const CeShape& shape) {
-    uint32_t best = 1, least = 0xFFFFFFFFu;
-    for (uint32_t s = 1; s <= uint32_t(most) && tiles < ce_split_tiles(shape); ++s) {
-        const uint32_t time = ce_split_time(tiles, split_k, s, shape);
-        if (time < least) {
-            least = time;
-            best = s;
-        }
-    }
-    return best;
-}
-#ifdef __HIPCC__
-__host__ __device__
-#endif
-inline int32_t ce_k_split(int32_t split_k, uint32_t splits) {
-    const int32_t steps = (split_k + kGemmBK - 1) / kGemmBK;
-    return (steps + int32_t(splits) - 1) / int32_t(splits) * kGemmBK;
-}
 
 struct CeGemmArgs {
     const void* a;
@@ -145,8 +112,10 @@ struct CeRowArgs {
     float* loss;
     float z_loss, inv_dz_scale;
     int32_t tiles, mean;
-    int32_t split_k, most;     // of the splits of the hidden product that follows: the longest piece's K, the planes there
-    uint32_t tiles_h;          // is room for (1 where none follows), its tiles along the hidden size, its shape
+    int32_t split_k, most;     // of the hidden product that follows: the longest piece's K, the most splits (1 where none
+    uint32_t plane_rows;       // follows), the rows of tiles that the planes have room for, its tiles along the hidden
+    uint32_t tiles_h;          // size, the weight product's tiles beside it, their shape
+    uint32_t weight_tiles;
     int32_t small;
 };
 constexpr int64_t kCeRowGrid = 512;

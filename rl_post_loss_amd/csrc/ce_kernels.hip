@@ -350,6 +350,11 @@ __device__ __forceinline__ float* kept_at(const CeGemmArgs& g, int m0, uint32_t 
     return g.kept + rows * (S::kColTiles * 256) + 4 * lane;
 }
 
+__device__ __forceinline__ int32_t ce_k_split(int32_t split_k, uint32_t splits) {
+    const int32_t steps = (split_k + kGemmBK - 1) / kGemmBK;
+    return (steps + int32_t(splits) - 1) / int32_t(splits) * kGemmBK;
+}
+
 // One tile of a product: workgroup `block` of those the launch has for it.  A_KCONTIG, B_KCONTIG: the operands'
 // layouts (mfma_tile.h).
 template <typename T, typename S, int PRODUCT, bool A_KCONTIG, bool B_KCONTIG>
@@ -370,6 +375,7 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
     const int wm = wave / S::kWavesN, wn = wave % S::kWavesN;
     const int k_split = PRODUCT == kCeHidden ? ce_k_split(g.split_k, splits) : K;
     const int kb = int(split) * k_split, ke = min(K, kb + k_split);
+    if (PRODUCT == kCeHidden && g.accumulate && kb >= ke) return;   // a short last piece adds nothing to this plane
     const uint16_t* __restrict__ A = static_cast<const uint16_t*>(g.a);
     const uint16_t* __restrict__ B = static_cast<const uint16_t*>(g.b);
 
@@ -784,6 +790,21 @@ __global__ void __launch_bounds__(S::kThreads, 2) ce_grads(const CeGradArgs a) {
     else ce_tile<T, S, kCeWeight, false, false>(a.weight, blockIdx.x - a.hidden_blocks);
 }
 
+// The time, in quarters of a K step, of the hidden product over `count` rows with its K (the longest piece's) in s
+// splits, beside the weight's product over the same rows where that is wanted.  Both products' workgroups
+// share the chip, so there a split pays only where a workgroup alone would outlast all of them; by themselves, the hidden
+// product's run in rounds.  6001 x 2048 x 50021 with half of the rows kept takes two splits (five, the best without
+// the weight's product, made the call 2.25 ms instead of 1.95), 16 x 4096 x 128256 six (690 us; 1548 with two, 745 with 32).
+__device__ __forceinline__ uint64_t split_time(const CeRowArgs& a, const CeShape& shape, uint32_t count, uint32_t s) {
+    const uint64_t tiles = uint64_t((count + shape.tile - 1) / shape.tile) * a.tiles_h, at_once = shape.at_once;
+    const uint32_t steps = uint32_t(a.split_k + kGemmBK - 1) / kGemmBK, row_steps = (count + kGemmBK - 1) / kGemmBK;
+    const uint64_t one = 4 * ((steps + s - 1) / s) + uint32_t(shape.extra);
+    const uint64_t weight = uint64_t(a.weight_tiles) * (4 * row_steps + uint32_t(shape.weight_extra));
+    const uint64_t all = (tiles * s * one + weight) / at_once, rounds = (tiles * s + at_once - 1) / at_once * one;
+    return (a.weight_tiles == 0 ? rounds : all > one ? all : one) +
+           s * (uint32_t(shape.plane) + tiles / uint32_t(shape.plane_tiles));
+}
+
 // A wavefront joins a kept row's tiles (each lane's in order, then the lane tree).  The workgroup that is done last
 // sums the rows' losses in double (each lane's in order, then a tree), whichever it is: the rows' losses are written to
 // and read from memory past the caches that compute units do not share, each before its workgroup counts itself
@@ -820,10 +841,10 @@ __global__ void __launch_bounds__(kCeThreads) ce_row(const CeRowArgs a) {
     if (!last) return;
     if (threadIdx.x < 64) {                // lane l: the time of l + 1 splits; the least, and of equal ones the fewest splits
         const CeShape shape = a.small ? kCeSmall : kCeLarge;
-        const uint32_t tiles = uint32_t((count + shape.tile - 1) / shape.tile) * a.tiles_h;
+        const uint32_t rows = uint32_t((count + shape.tile - 1) / shape.tile);
         uint64_t best = ~uint64_t(0);
-        if (lane < a.most && (lane == 0 || tiles < ce_split_tiles(shape)))
-            best = uint64_t(ce_split_time(tiles, a.split_k, lane + 1, shape)) << 8 | uint32_t(lane + 1);
+        if (lane == 0 || (lane < a.most && rows * uint32_t(lane + 1) <= a.plane_rows))
+            best = split_time(a, shape, uint32_t(count), uint32_t(lane + 1)) << 8 | uint32_t(lane + 1);
 #pragma unroll
         for (int off = 32; off > 0; off >>= 1) {
             const uint64_t other = __shfl_xor(best, off, 64);

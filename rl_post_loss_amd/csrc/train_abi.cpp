@@ -106,7 +106,7 @@ bool ce_shape_ok(int64_t n, int64_t h, int64_t vocab) {
 struct CeLayout {
     bool small_z, small_g;             // the shapes of the logits' products and of the gradients'
     CeShape z, g;
-    int64_t piece, tiles_m, tiles_n, splits, hidden_blocks;   // tiles of the logits
+    int64_t piece, tiles_m, tiles_n, splits, plane_rows;   // tiles of the logits
     bool keep;                         // the first piece's logits
     size_t row, place, target, lse, row_loss, target_logit, hidden, kept, part, dz, planes, cols, total;   // offsets
 };
@@ -145,19 +145,15 @@ CeLayout ce_layout(int64_t n, int64_t h, int64_t vocab, bool grads) {
     L.part = at;
     const size_t after_loss = at + up256(size_t(n) * size_t(L.tiles_n) * 8);
     if (grads) {
-        // planes for up to kCeMaxSplits splits of K, for as many rows as may come with each number of splits
+        // planes for up to kCeMaxSplits splits of K, and no more than twice the workgroups that run at once
         const int64_t tiles_h = div_up(h, L.g.tile), tiles_r = div_up(n, L.g.tile), most = L.piece / large * 2;
         L.splits = most < kCeMaxSplits ? most : kCeMaxSplits;
-        int64_t rows = n;
-        L.hidden_blocks = tiles_r * tiles_h;
-        for (int64_t m = 1; m <= tiles_r && m * tiles_h < int64_t(ce_split_tiles(L.g)); ++m) {
-            const int64_t r = m * L.g.tile < n ? m * L.g.tile : n;
-            const int64_t s = ce_splits(uint32_t(m * tiles_h), int32_t(L.piece), int32_t(L.splits), L.g);
-            if (r * s > rows) rows = r * s;
-            if (m * tiles_h * s > L.hidden_blocks) L.hidden_blocks = m * tiles_h * s;
-        }
+        L.plane_rows = div_up(2 * L.g.at_once, tiles_h);
+        if (L.plane_rows > tiles_r * L.splits) L.plane_rows = tiles_r * L.splits;
+        if (L.plane_rows < tiles_r) L.plane_rows = tiles_r;
+        const int64_t rows = L.plane_rows * L.g.tile < n * L.splits ? L.plane_rows * L.g.tile : n * L.splits;
         L.dz = take(size_t(n) * size_t(L.piece) * 2);
-        L.planes = take(size_t(rows) * size_t(h) * sizeof(float));
+        L.planes = take(size_t(rows < n ? n : rows) * size_t(h) * sizeof(float));
         L.cols = take(size_t(L.tiles_m) * size_t(vocab) * sizeof(float));
     }
     L.total = at > after_loss ? at : after_loss;
@@ -243,16 +239,19 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         z.kept_cols = int32_t(L.piece);
     }
     if ((st = product(pick_ce_gemm(c.dtype, L.small_z, kCeLogits), L.z, z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
+    const uint32_t tiles_h = uint32_t(div_up(c.h, L.g.tile));
     const CeRowArgs rows{floats(L.part), floats(L.target_logit), ints(L.target), state, floats(L.lse), floats(L.row_loss),
                          c.loss, c.z_loss, 1.0f / ce_dz_scale(c.dtype), int32_t(L.tiles_n),
                          c.reduction == RLPL_REDUCE_MEAN ? 1 : 0, int32_t(L.piece), grads ? int32_t(L.splits) : 1,
-                         uint32_t(div_up(c.h, L.g.tile)), L.small_g ? 1 : 0};
+                         uint32_t(L.plane_rows), tiles_h,
+                         c.grad_weight ? uint32_t(div_up(L.piece < c.vocab ? L.piece : c.vocab, L.g.tile)) * tiles_h : 0,
+                         L.small_g ? 1 : 0};
     if ((st = enqueue(ce_row_kernel(), rows, dim3(capped(div_up(c.n, kCeThreads / 64), kCeRowGrid)), kCeThreads, stream)) != RLPL_OK) return st;
     if (!any) return RLPL_OK;
 
     const size_t we = dtype_bytes(c.weight_grad_dtype);
     const int f32 = c.weight_grad_dtype == RLPL_F32 ? 1 : 0;
-    const uint32_t tiles_h = uint32_t(div_up(c.h, L.g.tile)), tiles_r = uint32_t(div_up(c.n, L.g.tile));
+    const uint32_t tiles_r = uint32_t(div_up(c.n, L.g.tile));
     for (int64_t v0 = 0; v0 < c.vocab; v0 += L.piece) {
         const int64_t cols = c.vocab - v0 < L.piece ? c.vocab - v0 : L.piece;
         const char* weight = static_cast<const char*>(c.weight) + size_t(v0) * size_t(c.h) * 2;
@@ -286,7 +285,7 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         hg.state = state;
         hg.c = ws + L.planes;
         hg.accumulate = v0 > 0 ? 1 : 0;
-        if (c.grad_hidden) g.hidden_blocks = uint32_t(div_up(L.hidden_blocks, 8) * 8);
+        if (c.grad_hidden) g.hidden_blocks = uint32_t(div_up(L.plane_rows * tiles_h, 8) * 8);
         CeGemmArgs& wg = g.weight;
         wg.a = ws + L.dz;
         wg.b = ws + L.hidden;

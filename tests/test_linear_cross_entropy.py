@@ -253,6 +253,18 @@ def test_wanted_gradients_leading_dimensions_and_repeats():
 
 
 @gpu
+@pytest.mark.parametrize("n,H,V", [(1, 64, 9000), (40, 256, 9000), (700, 72, 30000), (1500, 264, 3000), (12000, 32, 25000)])
+def test_the_hidden_gradient_alone(n, H, V):
+    """Without the weight's gradient the product is split over the vocabulary in its own way."""
+    c = make(n, H, V, ignored=0.98 if n > 2000 else 0.3, seed=6)
+    if n == 1:
+        c["y"][0] = V - 1
+    _, dh, dw, db = rl.linear_cross_entropy(*on_device(c), need_weight=False, need_bias=False)
+    assert dw is None and db is None
+    check("grad_hidden", dh, expected(c)["grad_hidden"], U["bf16"])
+
+
+@gpu
 def test_a_bias_gradient_passed_without_a_bias_is_added_to():
     c = make(70, 40, 300, bias=False, seed=2)
     args = on_device(c)

@@ -83,11 +83,12 @@ struct CeGemmArgs {
     float* target_logit;       // (kept rows) (kCeLogits)
     float* col_part;           // (tiles_m, col_ld) from column 0 on: sums of dz over a tile's rows, or NULL (kCeDlogits)
     int64_t col_ld;
-    float* kept;               // the logits of the first kept_cols columns (a multiple of 256, or 0) and M rows, up to a
-    int32_t kept_cols;         // multiple of 16; written by kCeLogits
+    float* kept;               // room for the first columns' logits, kept_room blocks of 16 rows by 256 columns, written by
+    uint32_t kept_room;        // kCeLogits; or NULL
 };
 const void* pick_ce_gemm(int dtype, bool small, int product);   // kCeLogits or kCeDlogits
-const void* pick_ce_dz(int dtype, bool small);                  // kCeDlogits of the kept columns
+const void* pick_ce_dz(int dtype, bool small);                  // kCeDlogits of the tiles with kept logits (kCeDlogits of
+                                                                // a piece that has `kept` forms the others')
 
 // The two products that take dz, in one launch: the first hidden_blocks workgroups (a multiple of 8, or 0) are the
 // hidden product's, the others the weight's.  Their tiles share the chip, so neither ends with idle compute units.

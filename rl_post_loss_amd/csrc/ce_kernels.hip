@@ -1,6 +1,6 @@
 // Softmax cross entropy of an output projection over a large vocabulary on
 // gfx950, with its gradients, in pieces of the vocabulary: never more than one
-// piece's logits are held.  For the rows i whose target y_i is not ignored (N of them),
+// piece's worth of logits is held.  For the rows i whose target y_i is not ignored (N of them),
 //
 //   z_i = hidden_i . weight^T + bias,   lse_i = log sum_v exp(z_iv)
 //   loss = s sum_i (lse_i - z_i[y_i] + c lse_i^2),   s = 1 / max(N, 1) or 1
@@ -14,7 +14,7 @@
 // Loss: each 256 x 256 tile of logits is reduced in registers to its rows'
 // (max, sum exp) and target logit; one kernel joins a row's tiles.  Gradient,
 // per piece of the vocabulary: dz goes to the workspace in the operand dtype,
-// from the float32 logits that the loss's pass left of the first piece, or from logits
+// from the float32 logits that the loss's pass left of the first columns, or from logits
 // formed again (n x V of them would take 4 bytes each), and two products take
 // it from there.  The weight's gradient of a piece comes out whole, so it is rounded once and written once;
 // the hidden states' is summed over the pieces in float32.
@@ -342,11 +342,16 @@ __global__ void __launch_bounds__(kCeThreads) ce_gather(const CePrepareArgs a) {
     for (int k = blockIdx.x; k < count; k += gridDim.x) copy_row(a, a.row[k], k);
 }
 
-// The first piece's logits, kept as the lanes hold them: 16 x 16 blocks of 64 lanes' four values, a wavefront's
-// columns side by side, rows in blocks of 16 after one another.
+// The first columns' logits are kept as the lanes hold them: 16 x 16 blocks of 64 lanes' four values, a wavefront's
+// columns side by side, rows in blocks of 16 after one another, for as many columns as there is room for with M rows.
+// col: of the tile, from the vocabulary's start.
 template <typename S>
-__device__ __forceinline__ float* kept_at(const CeGemmArgs& g, int m0, uint32_t tn, int wm, int wn, int i, int lane) {
-    const int64_t rows = int64_t(tn * S::kWavesN + wn) * ((g.M + 15) / 16) + (m0 + wm * S::kWaveM) / 16 + i;
+__device__ __forceinline__ bool is_kept(const CeGemmArgs& g, int M, int col) {
+    return g.kept && col + S::BN <= int(min(g.kept_room / uint32_t((M + 15) / 16), 1u << 14)) * 256;
+}
+template <typename S>
+__device__ __forceinline__ float* kept_at(const CeGemmArgs& g, int M, int m0, int col, int wm, int wn, int i, int lane) {
+    const int64_t rows = int64_t(col / S::kWaveN + wn) * ((M + 15) / 16) + (m0 + wm * S::kWaveM) / 16 + i;
     return g.kept + rows * (S::kColTiles * 256) + 4 * lane;
 }
 
@@ -371,6 +376,7 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
     uint32_t tm, tn, split;
     tile_of(block, tiles_m, g.tiles_n, splits, tm, tn, split);
     const int m0 = int(tm) * S::BM, n0 = int(tn) * S::BN;
+    if (PRODUCT == kCeDlogits && is_kept<S>(g, M, g.first + n0)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::kWavesN, wn = wave % S::kWavesN;
     const int k_split = PRODUCT == kCeHidden ? ce_k_split(g.split_k, splits) : K;
@@ -591,11 +597,11 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
             for (int e = 0; e < 4; ++e) acc[i][j][e] += b;
     }
 
-    if (PRODUCT == kCeLogits && n0 < g.kept_cols) {
+    if (PRODUCT == kCeLogits && is_kept<S>(g, M, n0)) {
 #pragma unroll
         for (int i = 0; i < S::kRowTiles; ++i) {
             if (m0 + wm * S::kWaveM + i * 16 >= M) break;
-            float* to = kept_at<S>(g, m0, tn, wm, wn, i, lane);
+            float* to = kept_at<S>(g, M, m0, n0, wm, wn, i, lane);
 #pragma unroll
             for (int j = 0; j < S::kColTiles; ++j) *reinterpret_cast<floatx4*>(to + 256 * j) = acc[i][j];
         }
@@ -709,8 +715,8 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
         reinterpret_cast<float2*>(g.part)[int64_t(row) * g.tiles_n + tn] = make_float2(top, sum);
 }
 
-// dz of the piece whose logits were kept (the first one), bit for bit what ce_tile forms: a workgroup a tile, a wavefront its own
-// blocks of it, each turned to whole rows in a strip of LDS of its own (1024 x 128256: 150 us, 5.3 TB/s).
+// dz of a piece's tiles whose logits were kept, bit for bit what ce_tile forms: a workgroup a tile, a wavefront its
+// own blocks of it, each turned to whole rows in a strip of LDS of its own (1024 x 128256: 150 us, 5.3 TB/s).
 template <typename T, typename S>
 __global__ void __launch_bounds__(S::kThreads) ce_dz(const CeGemmArgs g) {
     constexpr int kPitch = 2 * S::kWaveN + 16, kLanes = S::kWaveN / 8;      // bytes of a row in the strip, lanes of its store
@@ -721,6 +727,7 @@ __global__ void __launch_bounds__(S::kThreads) ce_dz(const CeGemmArgs g) {
     if (blockIdx.x >= tiles_m * g.tiles_n) return;
     const uint32_t tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
     const int m0 = int(tm) * S::BM, n0 = int(tn) * S::BN;
+    if (!is_kept<S>(g, M, g.first + n0)) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::kWavesN, wn = wave % S::kWavesN, odd = lane & 1;
     char* strip = strips[wave];
@@ -729,7 +736,7 @@ __global__ void __launch_bounds__(S::kThreads) ce_dz(const CeGemmArgs g) {
     for (int i = 0; i < S::kRowTiles; ++i) {
         const int row0 = m0 + wm * S::kWaveM + i * 16;
         if (row0 >= M) break;
-        const float* from = kept_at<S>(g, m0, tn, wm, wn, i, lane);
+        const float* from = kept_at<S>(g, M, m0, g.first + n0, wm, wn, i, lane);
         floatx4 z[S::kColTiles];
 #pragma unroll
         for (int j = 0; j < S::kColTiles; ++j) z[j] = *reinterpret_cast<const floatx4*>(from + 256 * j);
@@ -738,7 +745,7 @@ __global__ void __launch_bounds__(S::kThreads) ce_dz(const CeGemmArgs g) {
             const int row = row0 + 4 * (lane >> 4) + e;
             const float lse = row < M ? g.lse[row] : 0.0f;
             const float f = row < M ? kDzScale<T> * (1.0f + g.z_loss2 * lse) : 0.0f;
-            const int target = row < M ? g.target[row] : -1;
+            const int target = row < M ? g.target[row] - g.first : -1;
 #pragma unroll
             for (int j = 0; j < S::kColTiles; ++j) {
                 const int col = n0 + wn * S::kWaveN + j * 16 + (lane & 15);

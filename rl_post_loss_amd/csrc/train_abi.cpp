@@ -62,9 +62,10 @@ constexpr int64_t kCeMaxHidden = 65536;
 constexpr int64_t kCeMaxTiles = int64_t(1) << 22;     // workgroups of one launch (x 512 lanes < 2^32)
 // A piece of the vocabulary: kCePieceElements of dz (256 MiB), at least kCePieceCols columns, so that
 // adding a piece's hidden gradient to the float32 planes stays small beside its product.  Where that least number
-// does not make it larger, the loss's pass leaves the first piece's logits (512 MiB), whose dz is then a pass over
-// them (1024 x 4096 x 128256 bf16: 150 us, where forming them again took 957; 3.64 -> 2.92 ms for the call; 16 rows:
-// 868 -> 735 us).
+// does not make it larger, the loss's pass leaves the logits of the first columns, as many as a piece of all rows has
+// (512 MiB), and their dz is a pass over them (1024 x 4096 x 128256 bf16: 150 us, where forming them again took 957;
+// 3.64 -> 2.92 ms for the call; 16 rows: 868 -> 735 us).  Where rows do not count, more columns fit (6001 x 2048 x
+// 50021, half of the rows: 135 us less).
 constexpr int64_t kCePieceElements = int64_t(1) << 27;
 constexpr int64_t kCePieceCols = 8192;
 
@@ -236,7 +237,7 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     const bool any = grads && (c.grad_hidden || c.grad_weight || c.grad_bias);
     if (any && L.keep) {
         z.kept = floats(L.kept);
-        z.kept_cols = int32_t(L.piece);
+        z.kept_room = uint32_t(div_up(c.n, 16) * (L.piece / 256));
     }
     if ((st = product(pick_ce_gemm(c.dtype, L.small_z, kCeLogits), L.z, z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
     const uint32_t tiles_h = uint32_t(div_up(c.h, L.g.tile));
@@ -267,8 +268,9 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         z.col_part = c.grad_bias ? floats(L.cols) + v0 : nullptr;
         z.col_ld = c.vocab;
         const uint32_t tiles = z.tiles_m * z.tiles_n;
-        st = v0 == 0 && L.keep ? enqueue(pick_ce_dz(c.dtype, L.small_z), z, dim3(tiles), L.z.threads, stream)
-                               : product(pick_ce_gemm(c.dtype, L.small_z, kCeDlogits), L.z, z, tiles);
+        // Kept logits reach beyond the first piece where rows do not count: both kernels pass over the other's tiles.
+        if (L.keep) st = enqueue(pick_ce_dz(c.dtype, L.small_z), z, dim3(tiles), L.z.threads, stream);
+        if (st == RLPL_OK && (v0 > 0 || !L.keep)) st = product(pick_ce_gemm(c.dtype, L.small_z, kCeDlogits), L.z, z, tiles);
         if (st != RLPL_OK) return st;
         CeGradArgs g{};
         CeGemmArgs& hg = g.hidden;

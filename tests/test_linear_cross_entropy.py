@@ -215,18 +215,24 @@ def test_more_than_one_piece_of_the_vocabulary():
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_pieces_with_kept_and_formed_logits(dtype):
-    """12,000 rows: pieces are 9,728 columns, and only the first one's logits are kept.  Columns of equal weights
-    and no target get equal gradients in any piece."""
-    c = make(12000, 32, 25000, dtype, ignored=0.98, seed=11)
-    c["w"][12500:] = c["w"][:12500]
-    c["b"][12500:] = c["b"][:12500]
-    _, (_, _, dw, db) = run_case(c)
-    free = torch.ones(12500, dtype=torch.bool)
-    free[c["y"][c["y"] != IGNORE] % 12500] = False
-    assert int(free.sum()) > 12000
-    dw, db = dw.cpu(), db.cpu()
-    assert torch.equal(dw[:12500][free], dw[12500:][free]) and torch.equal(db[:12500][free], db[12500:][free])
+@pytest.mark.parametrize("ignored", [0.0, 0.4, 0.98])
+def test_pieces_with_kept_and_formed_logits(ignored, dtype):
+    """9,000 rows: pieces are 14,336 columns.  The logits that are kept are those of the first piece, of the second's
+    first columns too, or all, by the rows that count.  Columns of equal weights and no target get equal gradients
+    whichever way, and rows their own hidden gradient."""
+    V = 36000
+    c = make(9000, 32, V, dtype, ignored=ignored, seed=11)
+    c["y"][c["y"] != IGNORE] = c["y"][c["y"] != IGNORE] % 500 + 17900      # in columns that have no equal without targets
+    c["w"][18000:] = c["w"][:18000]
+    c["b"][18000:] = c["b"][:18000]
+    _, dh, dw, db = rl.linear_cross_entropy(*on_device(c), reduction="sum")
+    free = torch.ones(18000, dtype=torch.bool, device=DEV)
+    free[17900:] = free[:400] = False
+    assert torch.equal(dw[:18000][free], dw[18000:][free]) and torch.equal(db[:18000][free], db[18000:][free])
+    assert dw[17900:18400].any()
+    rows = torch.cat([torch.arange(3), torch.arange(4000, 4040), torch.arange(8990, 9000)])
+    want = expected(dict(c, h=c["h"][rows], y=c["y"][rows]), reduction="sum")["grad_hidden"]
+    check("grad_hidden", dh[rows.to(DEV)], want, U[dtype], SUB[dtype])
 
 
 @gpu

@@ -35,6 +35,7 @@ constexpr int64_t kNormHeldCols = 16384;   // longest row of the backward kernel
 constexpr int64_t kNormHeldElements = 1 << 21;   // its workgroups times columns at most,
 constexpr int64_t kNormHeldGrid = 1024;          // and its workgroups, which may be one a compute unit
 constexpr int64_t kNormHeldLeast = 256;
+constexpr int64_t kNormHeldFew = 128;
 
 struct NormBwdArgs {
     const void* dy;            // (rows, cols) dtype

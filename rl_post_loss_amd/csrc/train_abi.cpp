@@ -339,10 +339,13 @@ unsigned row_grid(int64_t rows, int per_group) {
 }
 
 // Workgroups of the backward kernel that holds rows: four rows at least for each row a workgroup has at a time, so
-// that a row's loads overlap another's sums and the partials stay few, and more of them the shorter a row is
+// that a row's loads overlap another's sums and the partials stay few (of a short batch fewer, up to kNormHeldFew
+// workgroups: 100 x 768 bf16 8.4 -> 6.6 us, 17 x 8192 17.5 -> 13.4), and more of them the shorter a row is
 // (shorter rows take fewer registers).
 int64_t norm_held_grid(int64_t rows, int64_t cols, int rows_per_group) {
-    const int64_t g = div_up(rows, 4 * rows_per_group);
+    const int64_t each = div_up(rows, rows_per_group), few = each < kNormHeldFew ? each : kNormHeldFew;
+    int64_t g = div_up(rows, 4 * rows_per_group);
+    if (g < few) g = few;
     int64_t most = kNormHeldElements / cols;
     if (most > kNormHeldGrid) most = kNormHeldGrid;
     if (most < kNormHeldLeast) most = kNormHeldLeast;

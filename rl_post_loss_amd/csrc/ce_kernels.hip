@@ -208,6 +208,8 @@ struct Shape {
 };
 using Large = Shape<256, 256, 2, 4, 3, 2>;
 using Small = Shape<64, 64, 2, 2, 2, 2>;
+using Deep = Shape<64, 64, 2, 2, 4, 4>;
+static_assert(Deep::kLds == kCeDeepLds, "as launched");
 static_assert(Large::BM == kCeLarge.tile && Large::kThreads == kCeLarge.threads && Large::kLds == kCeLarge.lds, "as launched");
 static_assert(Small::BM == kCeSmall.tile && Small::kThreads == kCeSmall.threads && Small::kLds == kCeSmall.lds, "as launched");
 static_assert(Large::kWaveM == 128 && Large::kWaveN == 64 && Small::kWaveM == 32 && Small::kWaveN == 32 && kGemmBK == 64,
@@ -935,6 +937,10 @@ const void* pick_ce_gemm(int dtype, bool small, int product) {
     case kBF16: return small ? ce_gemm_for<__bf16, Small>(product) : ce_gemm_for<__bf16, Large>(product);
     }
     return nullptr;
+}
+const void* pick_ce_deep_logits(int dtype) {
+    return dtype == kF16 ? reinterpret_cast<const void*>(&ce_gemm<_Float16, Deep, kCeLogits>)
+                         : reinterpret_cast<const void*>(&ce_gemm<__bf16, Deep, kCeLogits>);
 }
 const void* pick_ce_grads(int dtype, bool small) {
     if (dtype == kF16)

@@ -49,6 +49,10 @@ int device(const Device** out) {
                     if (hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize,
                                             small ? kCeSmall.lds : kCeLarge.lds) != hipSuccess)
                         return;
+        for (int dt : {RLPL_F16, RLPL_BF16})
+            if (hipFuncSetAttribute(pick_ce_deep_logits(dt), hipFuncAttributeMaxDynamicSharedMemorySize, kCeDeepLds) !=
+                hipSuccess)
+                return;
         d.status = RLPL_OK;
     });
     *out = &d;
@@ -239,7 +243,11 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         z.kept = floats(L.kept);
         z.kept_room = uint32_t(div_up(c.n, 16) * (L.piece / 256));
     }
-    if ((st = product(pick_ce_gemm(c.dtype, L.small_z, kCeLogits), L.z, z, z.tiles_m * z.tiles_n)) != RLPL_OK) return st;
+    const uint32_t tiles_z = z.tiles_m * z.tiles_n;
+    st = L.small_z && tiles_z <= kCeDeepTiles
+             ? enqueue(pick_ce_deep_logits(c.dtype), z, dim3(tiles_z), L.z.threads, stream, size_t(kCeDeepLds))
+             : product(pick_ce_gemm(c.dtype, L.small_z, kCeLogits), L.z, z, tiles_z);
+    if (st != RLPL_OK) return st;
     const uint32_t tiles_h = uint32_t(div_up(c.h, L.g.tile));
     const CeRowArgs rows{floats(L.part), floats(L.target_logit), ints(L.target), state, floats(L.lse), floats(L.row_loss),
                          c.loss, c.z_loss, 1.0f / ce_dz_scale(c.dtype), int32_t(L.tiles_n),

@@ -62,27 +62,35 @@ def _scratch(nbytes: int, workspace: Optional[torch.Tensor], device: torch.devic
 
 # ------------------------------------------------------------------------------------- vocabulary cross entropy
 
+def _plain(t: torch.Tensor) -> torch.Tensor:
+    return t.detach() if t.requires_grad else t
+
+
 def _ce_operands(hidden, weight, bias, targets, reduction):
-    x, w, b = hidden.detach(), weight.detach(), None
-    for name, t in (("hidden", x), ("weight", w)):
+    for name, t in (("hidden", hidden), ("weight", weight)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if x.dtype not in (torch.float16, torch.bfloat16) or w.dtype != x.dtype:
+    x, w, b, y = _plain(hidden), _plain(weight), None, targets
+    dt, dev, shape, wshape = x.dtype, x.device, x.shape, w.shape
+    if dt not in (torch.float16, torch.bfloat16) or w.dtype != dt:
         raise TypeError("hidden and weight must share a float16 or bfloat16 dtype")
-    if x.dim() < 1 or w.dim() != 2 or x.shape[-1] != w.shape[1] or w.device != x.device:
+    if len(shape) < 1 or len(wshape) != 2 or shape[-1] != wshape[1] or w.device != dev:
         raise ValueError("hidden (*, H) and weight (V, H) must agree in H and device")
     if bias is not None:
-        b = bias.detach().contiguous()
-        if b.dtype != x.dtype or tuple(b.shape) != (w.shape[0],) or b.device != x.device:
-            raise ValueError(f"bias must be a ({w.shape[0]},) tensor of the operands' dtype and device")
-    y = targets.detach()
-    if y.dtype != torch.int64 or y.shape != x.shape[:-1] or y.device != x.device:
-        raise ValueError(f"targets must be an int64 {tuple(x.shape[:-1])} tensor on the operands' device")
+        b = _plain(bias)
+        if b.dtype != dt or b.dim() != 1 or b.shape[0] != wshape[0] or b.device != dev:
+            raise ValueError(f"bias must be a ({wshape[0]},) tensor of the operands' dtype and device")
+        b = b.contiguous()
+    if y.dtype != torch.int64 or y.shape != shape[:-1] or y.device != dev:
+        raise ValueError(f"targets must be an int64 {tuple(shape[:-1])} tensor on the operands' device")
     if reduction not in REDUCTION:
         raise ValueError(f"reduction must be one of {sorted(REDUCTION)}")
     if x.numel() == 0 or w.numel() == 0:
         _check("linear_cross_entropy", 2)
-    return _aligned(x).view(-1, x.shape[-1]), _aligned(w), b, y.contiguous().view(-1)
+    x, y = _aligned(x), y.contiguous()
+    if len(shape) != 2:
+        x, y = x.view(-1, shape[-1]), y.view(-1)
+    return x, _aligned(w), b, y
 
 
 def linear_cross_entropy_fwd(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean",
@@ -143,7 +151,7 @@ def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_
             x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr(), n, H, V, DTYPE[x.dtype], int(ignore_index), float(z_loss),
             REDUCTION[reduction], loss.data_ptr(), _ptr(dh), _ptr(dw), _ptr(db), DTYPE[wdt], int(accumulate), wp, wn,
             _stream(dev)))
-    return loss, None if dh is None else dh.view(hidden.shape), dw, db
+    return loss, dh if dh is None or hidden.dim() == 2 else dh.view(hidden.shape), dw, db
 
 
 # ------------------------------------------------------------------------------------------------------- layer norm

@@ -192,8 +192,9 @@ __device__ __forceinline__ void fragments_mn2(uint32_t at0, uint32_t at1, uint4 
 }
 
 // The shapes of a tile (ce_kernels.h says which a launch takes), as wavefronts along M and N, and their rings:
-// three slots of the A operand's stages and two of the B operand's, all of a compute unit's LDS; or two of both, so that five workgroups fit one
-// (16 rows of 4096 x 128256: 905 us, against 1001 with three slots and 1110 with four).
+// three slots of the A operand's stages and two of the B operand's, all of a compute unit's LDS; or two of both, so that
+// five workgroups fit one (16 rows of 4096 x 128256, all products by this tile and the logits formed twice: 905 us,
+// against 1001 with three slots and 1110 with four); or four, where a launch has no more workgroups than those.
 template <int BM_, int BN_, int WAVES_M, int WAVES_N, int SLOTS_A, int SLOTS_B>
 struct Shape {
     static constexpr int BM = BM_, BN = BN_, kWavesM = WAVES_M, kWavesN = WAVES_N;

@@ -686,11 +686,10 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
             float m = acc[i][0][e];
 #pragma unroll
             for (int j = 1; j < S::kColTiles; ++j) m = fmaxf(m, acc[i][j][e]);
+            const float from = sum_from(m);
             float sum = 0.0f;
-            if (m != -__builtin_inff()) {
 #pragma unroll
-                for (int j = 0; j < S::kColTiles; ++j) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * kLog2eG);
-            }
+            for (int j = 0; j < S::kColTiles; ++j) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - from) * kLog2eG);
             parts[pidx * S::BM + (r ^ part_row(pidx))] = make_float2(m, sum);
             const int tc = tgt_col[r];
 #pragma unroll
@@ -704,13 +703,12 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
     for (int p = first; p < first + kShare; ++p) top = fmaxf(top, parts[p * S::BM + (rr ^ part_row(p))].x);
     top = fmaxf(top, quad_xor<1>(top));
     if constexpr (kMerge == 4) top = fmaxf(top, quad_xor<2>(top));
+    const float from = sum_from(top);
     float sum = 0.0f;
-    if (top != -__builtin_inff()) {
 #pragma unroll 8
-        for (int p = first; p < first + kShare; ++p) {
-            const float2 v = parts[p * S::BM + (rr ^ part_row(p))];
-            sum += v.y * __builtin_amdgcn_exp2f((v.x - top) * kLog2eG);
-        }
+    for (int p = first; p < first + kShare; ++p) {
+        const float2 v = parts[p * S::BM + (rr ^ part_row(p))];
+        sum += v.y * __builtin_amdgcn_exp2f((v.x - from) * kLog2eG);
     }
     sum += quad_xor<1>(sum);
     if constexpr (kMerge == 4) sum += quad_xor<2>(sum);

@@ -185,6 +185,10 @@ __device__ __forceinline__ float quad_xor(float v) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), X == 1 ? 0xB1 : 0x4E, 0xF, 0xF, false));
 }
 
+// What a sum of exponentials counts from, given its largest term (by fmaxf, which passes over NaN): that term, or 0
+// where it is -inf, so that terms of -inf add 0 and a NaN among them stays one.
+__device__ __forceinline__ float sum_from(float top) { return top == -__builtin_inff() ? 0.0f : top; }
+
 // XCD-aware tile order: consecutive block indices go to different XCDs, so
 // XCD x (block % 8) takes a contiguous run of the (split, tile) pairs, split
 // slowest (a split-K product gives each split's tiles to whole XCDs).

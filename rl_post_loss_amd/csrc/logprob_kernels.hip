@@ -307,11 +307,10 @@ gemm_kernel(const GemmArgs g) {
                     float m = acc[i][0][e];
 #pragma unroll
                     for (int j = 1; j < kFragN; ++j) m = fmaxf(m, acc[i][j][e]);
+                    const float from = sum_from(m);
                     float sum = 0.0f;
-                    if (m != -__builtin_inff()) {
 #pragma unroll
-                        for (int j = 0; j < kFragN; ++j) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - m) * kLog2eG);
-                    }
+                    for (int j = 0; j < kFragN; ++j) sum += __builtin_amdgcn_exp2f((acc[i][j][e] - from) * kLog2eG);
                     const int rr = r - w * kRoundRows;
                     parts[pidx * kRoundRows + (rr ^ part_swizzle(pidx))] = make_float2(m, sum);
                     const int tc = tgt_col[r];
@@ -331,10 +330,11 @@ gemm_kernel(const GemmArgs g) {
                 M = fmaxf(M, parts[q * kRoundRows + (rr ^ part_swizzle(q))].x);
             M = fmaxf(M, quad_xor<1>(M));
             if constexpr (kQ == 4) M = fmaxf(M, quad_xor<2>(M));
+            const float from = sum_from(M);
             float S = 0.0f;
             for (int q = qq * kShare; q < (qq + 1) * kShare; ++q) {
                 const float2 v = parts[q * kRoundRows + (rr ^ part_swizzle(q))];
-                S += v.y * __builtin_amdgcn_exp2f((v.x - M) * kLog2eG);
+                S += v.y * __builtin_amdgcn_exp2f((v.x - from) * kLog2eG);
             }
             S += quad_xor<1>(S);
             if constexpr (kQ == 4) S += quad_xor<2>(S);

@@ -8,7 +8,8 @@ loss and keeps the gradient the launch wrote; backward multiplies that
 gradient by the incoming scalar gradient of the loss (the chain rule for a
 scalar loss), in float32, rounding once to the gradient's dtype.  There is no
 other computation and no fallback: the ops call the same HIP kernels as the
-direct entry points.
+direct entry points.  The gradient is an output of the op beside the loss; no
+tensor is made for its own gradient, which a first backward pass does not ask for.
 
 The direct entry points stay the lowest-overhead path; these add the custom-op
 dispatch (and, under compile, a graph break-free call).
@@ -56,9 +57,12 @@ def _policy_op(op: str):
         return (policy_logprobs.new_empty((), dtype=torch.float32), torch.empty_like(policy_logprobs))
 
     def setup_context(ctx, inputs, output):
+        ctx.set_materialize_grads(False)
         ctx.save_for_backward(output[1])
 
     def backward(ctx, grad_loss, _grad_of_grad):
+        if grad_loss is None:
+            return (None,) * 9
         (g,) = ctx.saved_tensors
         return (_scaled(g, grad_loss), None, None, None, None, None, None, None, None)
 
@@ -78,9 +82,12 @@ def _rkl_op(name: str, direct):
         return student.new_empty((), dtype=torch.float32), torch.empty_like(student)
 
     def setup_context(ctx, inputs, output):
+        ctx.set_materialize_grads(False)
         ctx.save_for_backward(output[1])
 
     def backward(ctx, grad_loss, _grad_of_grad):
+        if grad_loss is None:
+            return None, None, None
         (g,) = ctx.saved_tensors
         return _scaled(g, grad_loss), None, None
 
@@ -216,6 +223,7 @@ def _(grad_y, x, weight, mean, rstd, need_x, need_weight, need_bias):
 
 def _norm_setup(ctx, inputs, output):
     x, weight, bias, _ = inputs
+    ctx.set_materialize_grads(False)
     ctx.bias_dtype = None if bias is None else bias.dtype
     ctx.save_for_backward(x, weight, output[1], output[2])
 
@@ -224,7 +232,7 @@ def _norm_backward(ctx, grad_y, _grad_mean, _grad_rstd):
     x, weight, mean, rstd = ctx.saved_tensors
     need_x, need_w = ctx.needs_input_grad[0], weight is not None and ctx.needs_input_grad[1]
     need_b = ctx.bias_dtype is not None and ctx.needs_input_grad[2]
-    if not (need_x or need_w or need_b):
+    if grad_y is None or not (need_x or need_w or need_b):
         return None, None, None, None
     dx, dw, db = _norm_bwd(grad_y, x, weight, mean, rstd, need_x, need_w, need_b)
     return dx if need_x else None, dw if need_w else None, db.to(ctx.bias_dtype) if need_b else None, None
@@ -258,6 +266,7 @@ def _(hidden, weight, bias, targets, ignore_index, z_loss, reduction, need_hidde
 
 
 def _ce_setup(ctx, inputs, output):
+    ctx.set_materialize_grads(False)
     ctx.save_for_backward(*output[1:])
     ctx.need = inputs[7:9] + (inputs[9] and inputs[2] is not None,)
 
@@ -270,6 +279,8 @@ def _scaled_once(g, grad_loss):
 
 
 def _ce_backward(ctx, grad_loss, *_grads_of_grads):
+    if grad_loss is None:
+        return (None,) * 10
     grads = [_scaled_once(g, grad_loss) if need else None for g, need in zip(ctx.saved_tensors, ctx.need)]
     return (*grads, None, None, None, None, None, None, None)
 

@@ -1,0 +1,113 @@
+"""What the autograd forms do in a backward pass besides the gradients: on the CPU, with the operators' bodies replaced
+by their formulas in torch (the ops, their fakes and their autograd formulas are the package's own)."""
+import pytest
+import torch
+from torch.utils._python_dispatch import TorchDispatchMode
+
+import rl_post_loss_amd as rl
+import rl_post_loss_amd.autograd as ag
+
+
+def ce_formula(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean", need_hidden=True,
+               need_weight=True, need_bias=True, weight_grad_dtype=None, hidden_grad_dtype=None, **_):
+    h, w, keep = hidden.double(), weight.double(), targets != ignore_index
+    z = h @ w.t() if bias is None else h @ w.t() + bias.double()
+    scale = keep.double() / (keep.sum().clamp(min=1) if reduction == "mean" else 1)
+    at = torch.where(keep, targets, 0)[:, None]
+    lse = torch.logsumexp(z, 1)
+    loss = (scale * (lse - z.gather(1, at)[:, 0] + z_loss * lse ** 2)).sum()
+    dz = (1 + 2 * z_loss * lse)[:, None] * torch.exp(z - lse[:, None])
+    dz = scale[:, None] * dz.scatter_add(1, at, -torch.ones_like(scale)[:, None])
+    wdt = weight_grad_dtype or hidden.dtype
+    return (loss.float(), (dz @ w).to(hidden_grad_dtype or hidden.dtype) if need_hidden else None,
+            (dz.t() @ h).to(wdt) if need_weight else None, dz.sum(0).to(wdt) if need_bias and bias is not None else None)
+
+
+def norm_formula(x, weight=None, bias=None, *, eps=1e-5):
+    mean = x.float().mean(-1)
+    rstd = (x.float().var(-1, unbiased=False) + eps).rsqrt()
+    y = (x.float() - mean[..., None]) * rstd[..., None]
+    y = y if weight is None else y * weight.float()
+    return (y if bias is None else y + bias.float()).to(x.dtype), mean, rstd
+
+
+def norm_backward_formula(grad_y, x, weight, mean, rstd, *, need_x=True, need_weight=True, need_bias=True, **_):
+    h = (x.float() - mean[..., None]) * rstd[..., None]
+    g = grad_y.float() if weight is None else grad_y.float() * weight.float()
+    dx = rstd[..., None] * (g - g.mean(-1, keepdim=True) - h * (g * h).mean(-1, keepdim=True))
+    rows = tuple(range(x.dim() - 1))
+    wdt = x.dtype if weight is None else weight.dtype
+    return (dx.to(x.dtype) if need_x else None,
+            (grad_y.float() * h).sum(rows).to(wdt) if need_weight and weight is not None else None,
+            grad_y.float().sum(rows).to(wdt) if need_bias else None)
+
+
+def policy_formula(op, fused, lp, *rest):
+    return (lp.detach().float() ** 2).sum(), 2 * lp.detach()
+
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    monkeypatch.setattr(ag, "linear_cross_entropy", ce_formula)
+    monkeypatch.setattr(ag, "linear_cross_entropy_fwd", lambda *a, **k: ce_formula(*a, **k)[0])
+    monkeypatch.setattr(ag, "layer_norm_fwd", norm_formula)
+    monkeypatch.setattr(ag, "layer_norm_bwd", norm_backward_formula)
+    monkeypatch.setattr(ag, "_policy", policy_formula)
+
+
+class Made(TorchDispatchMode):
+    """Sizes of the tensors filled with zeros while the mode is on."""
+
+    def __init__(self):
+        super().__init__()
+        self.zeros = []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        out = func(*args, **(kwargs or {}))
+        if "zero" in func._schema.name:
+            self.zeros.append(out.numel())
+        return out
+
+
+def case(n=6, H=8, V=40, dtype=torch.bfloat16, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g).to(dtype)  # noqa: E731
+    return r(n, H), r(V, H), r(V), torch.randint(0, V, (n,), generator=g)
+
+
+def test_no_tensor_of_zeros_stands_for_an_unused_gradient(on_cpu):
+    """The ops return the gradients beside the loss; their own gradients, which nobody asks for, are not made up."""
+    h, w, b, y = case()
+    h, w, b = (t.requires_grad_() for t in (h, w, b))
+    loss = rl.linear_cross_entropy_autograd(h, w, b, y)
+    with Made() as made:
+        loss.backward()
+    assert not made.zeros
+    assert h.grad is not None and w.grad is not None and b.grad is not None
+    x = torch.randn(5, 7, requires_grad=True)
+    out = rl.layer_norm_autograd(x)
+    with Made() as made:
+        out.backward(torch.ones(5, 7))
+    assert not made.zeros
+    lp = torch.randn(3, 4, requires_grad=True)
+    loss = rl.bnpo_loss_autograd(lp, lp.detach(), None, torch.ones(3), torch.ones(3, 4, dtype=torch.bool))
+    with Made() as made:
+        loss.backward()
+    assert not made.zeros and torch.equal(lp.grad, 2 * lp.detach())
+
+
+@pytest.mark.gpu
+def test_memory_of_the_backward_pass():
+    """Beside what the forward pass left, a backward pass takes the gradients it returns: less than half a projection
+    more than the one gradient wanted."""
+    n, H, V = 64, 512, 32768
+    r = lambda *s: torch.randn(*s, device="cuda:0").bfloat16()  # noqa: E731
+    h, w, y = r(n, H), r(V, H).requires_grad_(), torch.randint(0, V, (n,), device="cuda:0")
+    loss = rl.linear_cross_entropy_autograd(h, w, None, y)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    loss.backward()
+    torch.cuda.synchronize()
+    assert torch.cuda.max_memory_allocated() - before < 3 * V * H
+    assert torch.equal(w.grad, rl.linear_cross_entropy(h, w, None, y)[2])

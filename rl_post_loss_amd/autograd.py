@@ -9,7 +9,8 @@ gradient by the incoming scalar gradient of the loss (the chain rule for a
 scalar loss), in float32, rounding once to the gradient's dtype.  There is no
 other computation and no fallback: the ops call the same HIP kernels as the
 direct entry points.  The gradient is an output of the op beside the loss; no
-tensor is made for its own gradient, which a first backward pass does not ask for.
+tensor is made for its own gradient, which a first backward pass does not ask
+for.  It is a value, not a function of the inputs, so a second derivative raises.
 
 The direct entry points stay the lowest-overhead path; these add the custom-op
 dispatch (and, under compile, a graph break-free call).
@@ -40,6 +41,12 @@ def _scaled(g: torch.Tensor, grad_loss: torch.Tensor) -> torch.Tensor:
     return (g.float() * grad_loss.float()).to(g.dtype)
 
 
+def _first_only(form: str, *grads) -> None:
+    """Raises where a gradient arrives for an output that has no formula for it (a gradient's own, a statistic's)."""
+    if any(g is not None for g in grads):
+        raise RuntimeError(f"{form} gives first derivatives of its result only")
+
+
 def _policy_op(op: str):
     @torch.library.custom_op(f"{_LIB}::{op}_loss", mutates_args=())
     def fused(policy_logprobs: torch.Tensor, old_policy_logprobs: torch.Tensor,
@@ -60,7 +67,8 @@ def _policy_op(op: str):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(output[1])
 
-    def backward(ctx, grad_loss, _grad_of_grad):
+    def backward(ctx, grad_loss, grad_of_grad):
+        _first_only(f"{op}_loss_autograd", grad_of_grad)
         if grad_loss is None:
             return (None,) * 9
         (g,) = ctx.saved_tensors
@@ -85,7 +93,8 @@ def _rkl_op(name: str, direct):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(output[1])
 
-    def backward(ctx, grad_loss, _grad_of_grad):
+    def backward(ctx, grad_loss, grad_of_grad):
+        _first_only(f"{name}_autograd", grad_of_grad)
         if grad_loss is None:
             return None, None, None
         (g,) = ctx.saved_tensors
@@ -168,16 +177,18 @@ def _(hidden, weight, bias, targets, lse, grad_logp, need_hidden, need_weight):
 
 
 def _selective_setup(ctx, inputs, output):
+    ctx.set_materialize_grads(False)
     hidden, weight, bias, targets = inputs
     ctx.has_bias = bias is not None
     ctx.save_for_backward(hidden, weight, bias, targets, output[1])
 
 
-def _selective_backward(ctx, grad_logp, _grad_lse):
+def _selective_backward(ctx, grad_logp, grad_lse):
+    _first_only("selective_logprob_autograd", grad_lse)
     hidden, weight, bias, targets, lse = ctx.saved_tensors
     need_h, need_w = ctx.needs_input_grad[0], ctx.needs_input_grad[1]
     need_b = ctx.has_bias and ctx.needs_input_grad[2]
-    if not (need_h or need_w or need_b):
+    if grad_logp is None or not (need_h or need_w or need_b):
         return None, None, None, None
     dh, dw, db = _selective_bwd(hidden, weight, bias, targets, lse, grad_logp, need_h, need_w)
     return (dh if need_h else None, dw.to(weight.dtype) if need_w else None,
@@ -228,7 +239,8 @@ def _norm_setup(ctx, inputs, output):
     ctx.save_for_backward(x, weight, output[1], output[2])
 
 
-def _norm_backward(ctx, grad_y, _grad_mean, _grad_rstd):
+def _norm_backward(ctx, grad_y, grad_mean, grad_rstd):
+    _first_only("layer_norm_autograd", grad_mean, grad_rstd)
     x, weight, mean, rstd = ctx.saved_tensors
     need_x, need_w = ctx.needs_input_grad[0], weight is not None and ctx.needs_input_grad[1]
     need_b = ctx.bias_dtype is not None and ctx.needs_input_grad[2]
@@ -278,7 +290,8 @@ def _scaled_once(g, grad_loss):
     return torch.mul(g, grad_loss.float().view(1), out=torch.empty_like(g))
 
 
-def _ce_backward(ctx, grad_loss, *_grads_of_grads):
+def _ce_backward(ctx, grad_loss, *grads_of_grads):
+    _first_only("linear_cross_entropy_autograd", *grads_of_grads)
     if grad_loss is None:
         return (None,) * 10
     grads = [_scaled_once(g, grad_loss) if need else None for g, need in zip(ctx.saved_tensors, ctx.need)]

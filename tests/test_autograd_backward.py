@@ -111,3 +111,49 @@ def test_memory_of_the_backward_pass():
     torch.cuda.synchronize()
     assert torch.cuda.max_memory_allocated() - before < 3 * V * H
     assert torch.equal(w.grad, rl.linear_cross_entropy(h, w, None, y)[2])
+
+
+def test_second_derivatives_are_refused(on_cpu):
+    """The gradients are values, not functions of the inputs: asking for their own gradient raises."""
+    h, w, b, y = case()
+    h, w, b = (t.requires_grad_() for t in (h, w, b))
+    for wanted in (h, w, b):
+        (d,) = torch.autograd.grad(rl.linear_cross_entropy_autograd(h, w, b, y), wanted, create_graph=True)
+        with pytest.raises(RuntimeError, match="linear_cross_entropy_autograd.*first derivatives"):
+            d.float().square().sum().backward()
+    lp = torch.randn(3, 4, requires_grad=True)
+    for op in ("bnpo", "grpo"):
+        loss = getattr(rl, f"{op}_loss_autograd")(lp, lp.detach(), None, torch.ones(3), torch.ones(3, 4, dtype=torch.bool))
+        (d,) = torch.autograd.grad(loss, lp, create_graph=True)
+        with pytest.raises(RuntimeError, match=f"{op}_loss_autograd.*first derivatives"):
+            torch.autograd.grad(d.sum(), lp)
+    x = torch.randn(5, 7, requires_grad=True)
+    (d,) = torch.autograd.grad(rl.layer_norm_autograd(x).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        d.square().sum().backward()
+    with pytest.raises(RuntimeError, match="layer_norm_autograd"):
+        torch.ops.rlpl.layer_norm(x, None, None, 1e-5)[1].sum().backward()    # the statistics
+
+
+def test_a_gradient_with_respect_to_the_factor_of_the_loss(on_cpu):
+    """d (s * loss) / d hidden is linear in s, and its gradient in s is the loss's own."""
+    h, w, b, y = case(dtype=torch.float32)
+    h.requires_grad_()
+    s = torch.tensor(0.5, requires_grad=True)
+    (d,) = torch.autograd.grad(s * rl.linear_cross_entropy_autograd(h, w, b, y), h, create_graph=True)
+    (ds,) = torch.autograd.grad(d.sum(), s)
+    assert torch.allclose(ds, ce_formula(h.detach(), w, b, y)[1].sum(), atol=1e-6)
+
+
+@pytest.mark.gpu
+def test_second_derivatives_are_refused_on_the_device():
+    s = torch.randn(4, 9, device="cuda:0").log_softmax(-1).requires_grad_()
+    loss = rl.reverse_kl_autograd(s, s.detach() - 0.1, torch.ones(4, 9, dtype=torch.bool, device="cuda:0"))
+    (d,) = torch.autograd.grad(loss, s, create_graph=True)
+    with pytest.raises(RuntimeError, match="reverse_kl_autograd.*first derivatives"):
+        d.square().sum().backward()
+    z = torch.randn(4, 300, device="cuda:0", requires_grad=True)
+    loss = rl.reverse_kl_logits_autograd(z, z.detach().flip(0), torch.ones(4, dtype=torch.bool, device="cuda:0"))
+    (d,) = torch.autograd.grad(loss, z, create_graph=True)
+    with pytest.raises(RuntimeError, match="reverse_kl_logits_autograd.*first derivatives"):
+        d.square().sum().backward()

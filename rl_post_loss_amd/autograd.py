@@ -301,11 +301,22 @@ def _ce_backward(ctx, grad_loss, *grads_of_grads):
 _ce.register_autograd(_ce_backward, setup_context=_ce_setup)
 
 
+@torch.library.custom_op(f"{_LIB}::linear_cross_entropy_loss", mutates_args=())
+def _ce_loss(hidden: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], targets: torch.Tensor,
+             ignore_index: int, z_loss: float, reduction: str) -> torch.Tensor:
+    return linear_cross_entropy_fwd(hidden, weight, bias, targets, ignore_index=ignore_index, z_loss=z_loss,
+                                    reduction=reduction)
+
+
+@_ce_loss.register_fake
+def _(hidden, weight, bias, targets, ignore_index, z_loss, reduction):
+    return hidden.new_empty((), dtype=torch.float32)
+
+
 def linear_cross_entropy_autograd(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean"):
     """The loss of ``linear_cross_entropy`` as a differentiable 0-d float32 tensor: gradients flow to hidden, weight and
     bias.  They are formed with the loss, for the inputs that need one; where none does, the loss alone is."""
     needs = [t is not None and t.requires_grad and torch.is_grad_enabled() for t in (hidden, weight, bias)]
     if not any(needs):
-        return linear_cross_entropy_fwd(hidden, weight, bias, targets, ignore_index=ignore_index, z_loss=z_loss,
-                                        reduction=reduction)
+        return _ce_loss(hidden, weight, bias, targets, int(ignore_index), float(z_loss), reduction)
     return _ce(hidden, weight, bias, targets, int(ignore_index), float(z_loss), reduction, *needs)[0]

@@ -157,3 +157,33 @@ def test_second_derivatives_are_refused_on_the_device():
     (d,) = torch.autograd.grad(loss, z, create_graph=True)
     with pytest.raises(RuntimeError, match="reverse_kl_logits_autograd.*first derivatives"):
         d.square().sum().backward()
+
+
+def test_the_loss_alone_traces(on_cpu):
+    """Where no input needs a gradient the loss is an op of its own, with a fake: it traces as the other forms do."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        h, w, y = torch.empty(4, 5, 16, dtype=torch.bfloat16), torch.empty(30, 16, dtype=torch.bfloat16), torch.empty(4, 5, dtype=torch.int64)
+        loss = rl.linear_cross_entropy_autograd(h, w, None, y, z_loss=1e-3, reduction="sum")
+        assert loss.shape == () and loss.dtype == torch.float32
+        with torch.no_grad():
+            assert rl.linear_cross_entropy_autograd(h.requires_grad_(), w, w[:, 0], y).shape == ()
+    h, w, b, y = case()
+    h.requires_grad_()
+    want = ce_formula(h.detach(), w, b, y, z_loss=0.01)[0]
+    compiled = torch.compile(lambda *a: 2 * rl.linear_cross_entropy_autograd(*a, z_loss=0.01), fullgraph=True, backend="aot_eager")
+    with torch.no_grad():
+        assert torch.equal(compiled(h, w, b, y), 2 * want)
+    assert torch.equal(rl.linear_cross_entropy_autograd(h.detach(), w, b, y, z_loss=0.01), want)
+
+
+@pytest.mark.gpu
+def test_the_loss_alone_traces_on_the_device():
+    h, w, b, y = (t.to("cuda:0") for t in case(70, 64, 300))
+    compiled = torch.compile(lambda *a: rl.linear_cross_entropy_autograd(*a, z_loss=0.01), fullgraph=True, backend="aot_eager")
+    want = rl.linear_cross_entropy_fwd(h, w, b, y, z_loss=0.01)
+    assert torch.equal(compiled(h, w, b, y), want)
+    w.requires_grad_()
+    with torch.inference_mode():
+        assert torch.equal(rl.linear_cross_entropy_autograd(h, w, b, y, z_loss=0.01), want)
+    assert torch.equal(compiled(h, w, b, y).detach(), want)                  # and with a gradient

@@ -10,7 +10,8 @@ scalar loss), in float32, rounding once to the gradient's dtype.  There is no
 other computation and no fallback: the ops call the same HIP kernels as the
 direct entry points.  The gradient is an output of the op beside the loss; no
 tensor is made for its own gradient, which a first backward pass does not ask
-for.  It is a value, not a function of the inputs, so a second derivative raises.
+for.  It is a value, not a function of the inputs, so a second derivative raises,
+and so does a forward-mode one.
 
 The direct entry points stay the lowest-overhead path; these add the custom-op
 dispatch (and, under compile, a graph break-free call).
@@ -24,6 +25,7 @@ from __future__ import annotations
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import _policy, _rkl, _rkl_logits, selective_logprob_bwd, selective_logprob_fwd
 from .training import layer_norm_bwd, layer_norm_fwd, linear_cross_entropy, linear_cross_entropy_fwd
@@ -45,6 +47,12 @@ def _first_only(form: str, *grads) -> None:
     """Raises where a gradient arrives for an output that has no formula for it (a gradient's own, a statistic's)."""
     if any(g is not None for g in grads):
         raise RuntimeError(f"{form} gives first derivatives of its result only")
+
+
+def _no_tangents(*inputs) -> None:
+    """Raises where an input carries a forward-mode tangent: an op without a formula for it would drop it."""
+    if any(t is not None and unpack_dual(t).tangent is not None for t in inputs):
+        raise RuntimeError("the autograd forms have no forward-mode derivatives")
 
 
 def _policy_op(op: str):
@@ -113,6 +121,7 @@ _rkl_vocab = _rkl_op("reverse_kl_logits", _rkl_logits)
 def bnpo_loss_autograd(policy_logprobs, old_policy_logprobs, ref_logprobs, advantages, completions_mask, *,
                        epsilon=0.2, epsilon_high=None, beta=0.0, clip="literal"):
     """BNPO loss as a differentiable 0-d float32 tensor (gradient flows to policy_logprobs)."""
+    _no_tangents(policy_logprobs, old_policy_logprobs, ref_logprobs, advantages)
     eh = epsilon if epsilon_high is None else epsilon_high
     return _bnpo(policy_logprobs, old_policy_logprobs, ref_logprobs, advantages, completions_mask,
                  float(epsilon), float(eh), float(beta), _sign_aware(clip))[0]
@@ -121,6 +130,7 @@ def bnpo_loss_autograd(policy_logprobs, old_policy_logprobs, ref_logprobs, advan
 def grpo_loss_autograd(policy_logprobs, old_policy_logprobs, ref_logprobs, advantages, completions_mask, *,
                        epsilon=0.2, epsilon_high=None, beta=0.0, clip="literal"):
     """GRPO loss as a differentiable 0-d float32 tensor."""
+    _no_tangents(policy_logprobs, old_policy_logprobs, ref_logprobs, advantages)
     eh = epsilon if epsilon_high is None else epsilon_high
     return _grpo(policy_logprobs, old_policy_logprobs, ref_logprobs, advantages, completions_mask,
                  float(epsilon), float(eh), float(beta), _sign_aware(clip))[0]
@@ -134,11 +144,13 @@ def _sign_aware(clip: str) -> bool:
 
 def reverse_kl_autograd(student_logprobs, teacher_logprobs, completions_mask):
     """Per-token reverse KL as a differentiable 0-d float32 tensor (gradient flows to the student)."""
+    _no_tangents(student_logprobs, teacher_logprobs)
     return _rkl_tok(student_logprobs, teacher_logprobs, completions_mask)[0]
 
 
 def reverse_kl_logits_autograd(student_logits, teacher_logits, completions_mask):
     """Full-vocab reverse KL as a differentiable 0-d float32 tensor (gradient flows to the student logits)."""
+    _no_tangents(student_logits, teacher_logits)
     return _rkl_vocab(student_logits, teacher_logits, completions_mask)[0]
 
 
@@ -201,6 +213,7 @@ _selective.register_autograd(_selective_backward, setup_context=_selective_setup
 def selective_logprob_autograd(hidden, weight, bias, targets):
     """Per-token target log-probabilities (float32, (n,)) as a differentiable tensor: gradients flow to
     hidden, weight and bias (the weight and bias gradients are formed in float32, then cast to their dtype)."""
+    _no_tangents(hidden, weight, bias)
     return _selective(hidden, weight, bias, targets)[0]
 
 
@@ -256,6 +269,7 @@ _norm.register_autograd(_norm_backward, setup_context=_norm_setup)
 def layer_norm_autograd(x, weight=None, bias=None, *, eps=1e-5):
     """Layer norm over the last dimension as a differentiable tensor of x's shape and dtype (gradients flow to x,
     weight and bias; the saved statistics are float32)."""
+    _no_tangents(x, weight, bias)
     return _norm(x, weight, bias, float(eps))[0]
 
 
@@ -316,6 +330,7 @@ def _(hidden, weight, bias, targets, ignore_index, z_loss, reduction):
 def linear_cross_entropy_autograd(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean"):
     """The loss of ``linear_cross_entropy`` as a differentiable 0-d float32 tensor: gradients flow to hidden, weight and
     bias.  They are formed with the loss, for the inputs that need one; where none does, the loss alone is."""
+    _no_tangents(hidden, weight, bias)
     needs = [t is not None and t.requires_grad and torch.is_grad_enabled() for t in (hidden, weight, bias)]
     if not any(needs):
         return _ce_loss(hidden, weight, bias, targets, int(ignore_index), float(z_loss), reduction)

@@ -187,3 +187,28 @@ def test_the_loss_alone_traces_on_the_device():
     with torch.inference_mode():
         assert torch.equal(rl.linear_cross_entropy_autograd(h, w, b, y, z_loss=0.01), want)
     assert torch.equal(compiled(h, w, b, y).detach(), want)                  # and with a gradient
+
+
+def test_forward_mode_tangents_are_refused(on_cpu):
+    """An input that carries a tangent would lose it in the op: the result's derivative would be taken for zero."""
+    import torch.autograd.forward_ad as forward
+    h, w, b, y = case(dtype=torch.float32)
+    ones = torch.ones(3, 4, dtype=torch.bool)
+    lp = torch.randn(3, 4)
+    forms = [(rl.linear_cross_entropy_autograd, [h, w, b, y], (0, 1, 2)),
+             (rl.selective_logprob_autograd, [h, w, b, y], (0, 1, 2)),
+             (rl.layer_norm_autograd, [h, w[0], b[:8]], (0, 1, 2)),
+             (rl.reverse_kl_autograd, [lp, lp, ones], (0, 1)), (rl.reverse_kl_logits_autograd, [lp, lp, ones[:, 0]], (0, 1)),
+             (rl.bnpo_loss_autograd, [lp, lp, None, lp[:, 0], ones], (0, 1, 3)),
+             (rl.grpo_loss_autograd, [lp, lp, lp, lp[:, 0], ones], (0, 1, 2, 3))]
+    for form, args, places in forms:
+        for i in places:
+            for needs in (False, True):
+                with forward.dual_level():
+                    dual = forward.make_dual(args[i].clone().requires_grad_(needs), torch.ones_like(args[i]))
+                    with pytest.raises(RuntimeError, match="forward-mode"):
+                        form(*args[:i], dual, *args[i + 1:])
+    with forward.dual_level():
+        assert torch.equal(rl.linear_cross_entropy_autograd(h, w, b, y), ce_formula(h, w, b, y)[0])
+    with pytest.raises(RuntimeError, match="forward-mode"):
+        torch.func.jvp(lambda t: rl.linear_cross_entropy_autograd(t, w, b, y), (h,), (h,))

@@ -369,6 +369,22 @@ int linear_cross_entropy(const void* hidden, const void* weight, const void* bia
                          float* loss_out, void* grad_hidden, void* grad_weight, void* grad_bias, int weight_grad_dtype,
                          int accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* Flags of rlpl_linear_cross_entropy. */
+enum rlpl_ce_flags {
+    RLPL_CE_HIDDEN_F32 = 1     /* grad_hidden is float32 */
+};
+
+/*
+ * linear_cross_entropy with options; flags 0 gives exactly that entry point.  RLPL_CE_HIDDEN_F32: the sums that
+ * grad_hidden holds are not rounded to `dtype`, for callers that scale them first (a mean's 1 / N and a small
+ * probability take fp16 gradients below its normal range).  Unknown flag bits give RLPL_ERR_PARAM.
+ */
+int rlpl_linear_cross_entropy(uint32_t flags, const void* hidden, const void* weight, const void* bias,
+                              const int64_t* targets, int64_t n, int64_t hidden_size, int64_t vocab, int dtype,
+                              int64_t ignore_index, float z_loss, int reduction, float* loss_out, void* grad_hidden,
+                              void* grad_weight, void* grad_bias, int weight_grad_dtype, int accumulate, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
 /*
  * Layer norm of rows, forward:
  *

@@ -136,6 +136,7 @@ def _declare(lib):
     lib.linear_cross_entropy_workspace_bytes.restype = sz
     lib.linear_cross_entropy_fwd.argtypes = lp_common + [i64, i64, i64, i32, i64, f32, i32, vp, vp, sz, vp]
     lib.linear_cross_entropy.argtypes = lp_common + [i64, i64, i64, i32, i64, f32, i32, vp, vp, vp, vp, i32, i32, vp, sz, vp]
+    lib.rlpl_linear_cross_entropy.argtypes = [ctypes.c_uint32] + lib.linear_cross_entropy.argtypes
     lib.layer_norm_fwd.argtypes = [vp, vp, vp, i64, i64, i32, i32, f32, vp, vp, vp, vp]
     lib.layer_norm_workspace_bytes.argtypes, lib.layer_norm_workspace_bytes.restype = [i64, i64], sz
     lib.layer_norm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, i32, vp, vp, vp, vp, sz, vp]
@@ -143,7 +144,8 @@ def _declare(lib):
     lib.rlpl_adamw_plan_bytes.argtypes, lib.rlpl_adamw_plan_bytes.restype = [vp, i64], sz
     lib.rlpl_adamw_plan_build.argtypes = [vp, sz, vp, i64, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp]
     lib.rlpl_adamw_step.argtypes = [vp, vp, vp, i32, f64, vp, f64, f64, f64, i64, vp, vp, ctypes.c_uint32, vp]
-    for name in ("linear_cross_entropy_fwd", "linear_cross_entropy", "layer_norm_fwd", "layer_norm_bwd", "rlpl_adamw_plan_build", "rlpl_adamw_step"):
+    for name in ("linear_cross_entropy_fwd", "linear_cross_entropy", "rlpl_linear_cross_entropy", "layer_norm_fwd",
+                 "layer_norm_bwd", "rlpl_adamw_plan_build", "rlpl_adamw_step"):
         getattr(lib, name).restype = ctypes.c_int
     lib.rlpl_policy_loss.argtypes = [i32, ctypes.c_uint32] + policy
     lib.rlpl_policy_loss.restype = ctypes.c_int

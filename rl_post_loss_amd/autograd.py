@@ -273,42 +273,51 @@ def layer_norm_autograd(x, weight=None, bias=None, *, eps=1e-5):
     return _norm(x, weight, bias, float(eps))[0]
 
 
+def _ce_held(dtype: torch.dtype) -> torch.dtype:
+    """What the gradients are held in between the two passes.  A mean's 1 / N takes many of them below fp16's normal
+    range, and the incoming gradient, which may be a loss scale against that, comes later: they stay in float32."""
+    return torch.float32 if dtype == torch.float16 else dtype
+
+
 @torch.library.custom_op(f"{_LIB}::linear_cross_entropy", mutates_args=())
 def _ce(hidden: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor], targets: torch.Tensor,
         ignore_index: int, z_loss: float, reduction: str, need_hidden: bool, need_weight: bool,
         need_bias: bool) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    held = _ce_held(hidden.dtype)
     loss, *grads = linear_cross_entropy(hidden, weight, bias, targets, ignore_index=ignore_index, z_loss=z_loss,
                                         reduction=reduction, need_hidden=need_hidden, need_weight=need_weight,
-                                        need_bias=need_bias)
+                                        need_bias=need_bias, weight_grad_dtype=held, hidden_grad_dtype=held)
     return (loss, *(hidden.new_empty((0,)) if g is None else g for g in grads))
 
 
 @_ce.register_fake
 def _(hidden, weight, bias, targets, ignore_index, z_loss, reduction, need_hidden, need_weight, need_bias):
+    held = _ce_held(hidden.dtype)
     none = lambda: hidden.new_empty((0,))  # noqa: E731
-    return (hidden.new_empty((), dtype=torch.float32), hidden.new_empty(hidden.shape) if need_hidden else none(),
-            weight.new_empty(weight.shape) if need_weight else none(),
-            bias.new_empty(bias.shape) if need_bias and bias is not None else none())
+    return (hidden.new_empty((), dtype=torch.float32), hidden.new_empty(hidden.shape, dtype=held) if need_hidden else none(),
+            weight.new_empty(weight.shape, dtype=held) if need_weight else none(),
+            bias.new_empty(bias.shape, dtype=held) if need_bias and bias is not None else none())
 
 
 def _ce_setup(ctx, inputs, output):
     ctx.set_materialize_grads(False)
     ctx.save_for_backward(*output[1:])
+    ctx.dtype = inputs[0].dtype
     ctx.need = inputs[7:9] + (inputs[9] and inputs[2] is not None,)
 
 
-def _scaled_once(g, grad_loss):
-    """_scaled in one pass, without float32 tensors of g's size (128256 x 4096 bf16: 462 us instead of 1758)."""
+def _scaled_once(g, grad_loss, dtype):
+    """_scaled to dtype in one pass, without float32 tensors of g's size (128256 x 4096 bf16: 462 us instead of 1758)."""
     if torch.is_grad_enabled():            # the formula's own gradient is wanted
-        return _scaled(g, grad_loss)
-    return torch.mul(g, grad_loss.float().view(1), out=torch.empty_like(g))
+        return _scaled(g, grad_loss).to(dtype)
+    return torch.mul(g, grad_loss.float().view(1), out=torch.empty_like(g, dtype=dtype))
 
 
 def _ce_backward(ctx, grad_loss, *grads_of_grads):
     _first_only("linear_cross_entropy_autograd", *grads_of_grads)
     if grad_loss is None:
         return (None,) * 10
-    grads = [_scaled_once(g, grad_loss) if need else None for g, need in zip(ctx.saved_tensors, ctx.need)]
+    grads = [_scaled_once(g, grad_loss, ctx.dtype) if need else None for g, need in zip(ctx.saved_tensors, ctx.need)]
     return (*grads, None, None, None, None, None, None, None)
 
 
@@ -329,7 +338,8 @@ def _(hidden, weight, bias, targets, ignore_index, z_loss, reduction):
 
 def linear_cross_entropy_autograd(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean"):
     """The loss of ``linear_cross_entropy`` as a differentiable 0-d float32 tensor: gradients flow to hidden, weight and
-    bias.  They are formed with the loss, for the inputs that need one; where none does, the loss alone is."""
+    bias.  They are formed with the loss, for the inputs that need one (fp16 ones are held in float32 until the incoming
+    gradient, a loss scale for instance, has been applied); where none does, the loss alone is."""
     _no_tangents(hidden, weight, bias)
     needs = [t is not None and t.requires_grad and torch.is_grad_enabled() for t in (hidden, weight, bias)]
     if not any(needs):

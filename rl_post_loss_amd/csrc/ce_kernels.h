@@ -133,9 +133,10 @@ struct CeFinishArgs {
     const float* part;
     const int32_t* place;
     const CeState* state;
-    void* out;                 // (n, cols)
+    void* out;                 // (n, cols) operand dtype or float32
     int32_t n, cols;
     uint32_t row_blocks;       // 0: no hidden gradient
+    int32_t hidden_f32;
     const float* col_part;     // (tiles of col_tile rows, vocab)
     void* bias;                // (vocab) operand dtype or float32
     int32_t vocab, out_f32, accumulate;

@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(kCeThreads) ce_finish(const CeFinishArgs a) {
     const int splits = int(a.state->splits);
     for (int row = blockIdx.x; row < a.n; row += a.row_blocks) {
         const int k = a.place[row];
-        T* out = static_cast<T*>(a.out) + int64_t(row) * a.cols;
+        const int64_t at = int64_t(row) * a.cols;
         for (int c = threadIdx.x * 8; c < a.cols; c += kCeThreads * 8) {
             float v[8] = {};
             if (k >= 0) {
@@ -914,7 +914,8 @@ __global__ void __launch_bounds__(kCeThreads) ce_finish(const CeFinishArgs a) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] *= scale;
             }
-            store_row<8>(out + c, v);
+            if (a.hidden_f32) store_row<8>(static_cast<float*>(a.out) + at + c, v);
+            else store_row<8>(static_cast<T*>(a.out) + at + c, v);
         }
     }
 }

@@ -180,6 +180,7 @@ struct CeCall {
     int weight_grad_dtype, accumulate;
     void* workspace;
     size_t workspace_bytes;
+    uint32_t flags = 0;
 };
 
 int ce_check(const CeCall& c, bool grads) {
@@ -189,6 +190,7 @@ int ce_check(const CeCall& c, bool grads) {
     if (grads && c.weight_grad_dtype != RLPL_F32 && c.weight_grad_dtype != c.dtype) return RLPL_ERR_DTYPE;
     if (!std::isfinite(c.z_loss) || c.z_loss < 0.0f || c.z_loss > 1.0f) return RLPL_ERR_PARAM;
     if (c.reduction != RLPL_REDUCE_MEAN && c.reduction != RLPL_REDUCE_SUM) return RLPL_ERR_PARAM;
+    if (c.flags & ~uint32_t(RLPL_CE_HIDDEN_F32)) return RLPL_ERR_PARAM;
     if (grads && c.accumulate && c.weight_grad_dtype != RLPL_F32) return RLPL_ERR_PARAM;
     const size_t we = grads ? dtype_bytes(c.weight_grad_dtype) : 1;
     if (!is_aligned(c.hidden, 16) || !is_aligned(c.weight, 16) || !is_aligned(c.bias, 2) || !is_aligned(c.targets, 8) ||
@@ -314,7 +316,7 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
         if (blocks > 0 && (st = product(pick_ce_grads(c.dtype, L.small_g), L.g, g, blocks)) != RLPL_OK) return st;
     }
     const CeFinishArgs f{floats(L.planes), ints(L.place), state, c.grad_hidden, int32_t(c.n), int32_t(c.h),
-                         c.grad_hidden ? capped(c.n, 1 << 16) : 0, floats(L.cols),
+                         c.grad_hidden ? capped(c.n, 1 << 16) : 0, c.flags & RLPL_CE_HIDDEN_F32 ? 1 : 0, floats(L.cols),
                          c.grad_bias, int32_t(c.vocab), f32, c.accumulate ? 1 : 0, L.z.tile};
     const unsigned bias_blocks = c.grad_bias ? unsigned(div_up(c.vocab, kCeThreads)) : 0;
     if (f.row_blocks + bias_blocks == 0) return RLPL_OK;
@@ -430,8 +432,18 @@ int linear_cross_entropy(const void* hidden, const void* weight, const void* bia
                          int64_t hidden_size, int64_t vocab, int dtype, int64_t ignore_index, float z_loss, int reduction,
                          float* loss_out, void* grad_hidden, void* grad_weight, void* grad_bias, int weight_grad_dtype,
                          int accumulate, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    return rlpl_linear_cross_entropy(0, hidden, weight, bias, targets, n, hidden_size, vocab, dtype, ignore_index, z_loss,
+                                     reduction, loss_out, grad_hidden, grad_weight, grad_bias, weight_grad_dtype,
+                                     accumulate, workspace, workspace_bytes, stream);
+}
+
+int rlpl_linear_cross_entropy(uint32_t flags, const void* hidden, const void* weight, const void* bias,
+                              const int64_t* targets, int64_t n, int64_t hidden_size, int64_t vocab, int dtype,
+                              int64_t ignore_index, float z_loss, int reduction, float* loss_out, void* grad_hidden,
+                              void* grad_weight, void* grad_bias, int weight_grad_dtype, int accumulate, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
     const CeCall c{hidden, weight, bias, targets, n, hidden_size, vocab, dtype, ignore_index, z_loss, reduction, loss_out,
-                   grad_hidden, grad_weight, grad_bias, weight_grad_dtype, accumulate, workspace, workspace_bytes};
+                   grad_hidden, grad_weight, grad_bias, weight_grad_dtype, accumulate, workspace, workspace_bytes, flags};
     return ce_run(c, true, stream);
 }
 

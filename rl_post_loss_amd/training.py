@@ -25,6 +25,7 @@ from . import DTYPE, _aligned, _check, _ws_ptr, library
 __all__ = ["linear_cross_entropy", "linear_cross_entropy_fwd", "layer_norm_fwd", "layer_norm_bwd", "adamw_plan", "adamw_step", "AdamWPlan"]
 
 REDUCTION = {"mean": 0, "sum": 1}
+CE_HIDDEN_F32 = 1    # rlpl_linear_cross_entropy flags (RLPL_CE_HIDDEN_F32)
 
 BLOCK = 256   # values of an 8-bit moment that share one scale
 
@@ -111,7 +112,7 @@ def linear_cross_entropy_fwd(hidden, weight, bias, targets, *, ignore_index=-100
 
 def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean",
                          need_hidden=True, need_weight=True, need_bias=True, weight_grad_dtype=None, grad_weight=None,
-                         grad_bias=None, workspace=None):
+                         grad_bias=None, workspace=None, hidden_grad_dtype=None):
     """Softmax cross entropy of the logits hidden . weight^T + bias, with its gradients, in pieces of the vocabulary
     (no more than one piece's logits are held): (loss, grad_hidden, grad_weight, grad_bias), None for gradients not
     wanted and for a bias that is not there (unless its gradient is passed to be added to).
@@ -120,8 +121,9 @@ def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_
     leading shape.  Rows whose target is ``ignore_index`` do not count.  loss is the mean (or sum) over the others of
     lse - z[target] + z_loss * lse^2, a 0-d float32 tensor, and 0 where no row counts.
 
-    weight_grad_dtype: the operands' dtype (the default) or torch.float32, of grad_weight and grad_bias.  Passing
-    ``grad_weight`` / ``grad_bias`` (contiguous float32) adds to them, over groups of tokens or micro-batches."""
+    weight_grad_dtype: the operands' dtype (the default) or torch.float32, of grad_weight and grad_bias;
+    hidden_grad_dtype: likewise, of grad_hidden.  Passing ``grad_weight`` / ``grad_bias`` (contiguous float32) adds to
+    them, over groups of tokens or micro-batches."""
     x, w, b, y = _ce_operands(hidden, weight, bias, targets, reduction)
     (n, H), V, dev, lib = x.shape, w.shape[0], x.device, library()
     need_bias = need_bias and (b is not None or grad_bias is not None)
@@ -135,22 +137,26 @@ def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_
     wdt = x.dtype if weight_grad_dtype is None else weight_grad_dtype
     if wdt not in (x.dtype, torch.float32):
         raise TypeError("weight_grad_dtype must be the operands' dtype or float32")
+    if hidden_grad_dtype not in (None, x.dtype, torch.float32):
+        raise TypeError("hidden_grad_dtype must be the operands' dtype or float32")
+    wide = hidden_grad_dtype is torch.float32
     for name, t, shape in (("grad_weight", grad_weight, (V, H)), ("grad_bias", grad_bias, (V,))):
         if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()
                               or t.device != dev):
             raise ValueError(f"{name} must be a contiguous float32 {shape} tensor on the operands' device")
-    dh = torch.empty_like(x) if need_hidden else None
+    dh = torch.empty_like(x, dtype=hidden_grad_dtype) if need_hidden else None
     dw = (grad_weight if accumulate else torch.empty((V, H), dtype=wdt, device=dev)) if need_weight else None
     db = (grad_bias if accumulate else torch.empty(V, dtype=wdt, device=dev)) if need_bias else None
     ws = _scratch(lib.linear_cross_entropy_workspace_bytes(n, H, V, 1), workspace, dev,
                   "linear_cross_entropy_workspace_bytes")
     wp, wn = _ws_ptr(ws)
     loss = torch.empty((), dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check("linear_cross_entropy", lib.linear_cross_entropy(
-            x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr(), n, H, V, DTYPE[x.dtype], int(ignore_index), float(z_loss),
+    args = (x.data_ptr(), w.data_ptr(), _ptr(b), y.data_ptr(), n, H, V, DTYPE[x.dtype], int(ignore_index), float(z_loss),
             REDUCTION[reduction], loss.data_ptr(), _ptr(dh), _ptr(dw), _ptr(db), DTYPE[wdt], int(accumulate), wp, wn,
-            _stream(dev)))
+            _stream(dev))
+    with _on(dev):
+        _check("linear_cross_entropy",
+               lib.rlpl_linear_cross_entropy(CE_HIDDEN_F32, *args) if wide else lib.linear_cross_entropy(*args))
     return loss, dh if dh is None or hidden.dim() == 2 else dh.view(hidden.shape), dw, db
 
 

@@ -231,15 +231,16 @@ def _(x, weight, bias, eps):
 
 @torch.library.custom_op(f"{_LIB}::layer_norm_backward", mutates_args=())
 def _norm_bwd(grad_y: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tensor], mean: torch.Tensor,
-              rstd: torch.Tensor, need_x: bool, need_weight: bool,
-              need_bias: bool) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
-    out = layer_norm_bwd(grad_y, x, weight, mean, rstd, need_x=need_x, need_weight=need_weight, need_bias=need_bias)
+              rstd: torch.Tensor, need_x: bool, need_weight: bool, need_bias: bool,
+              bias_dtype: Optional[torch.dtype] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    out = layer_norm_bwd(grad_y, x, weight, mean, rstd, need_x=need_x, need_weight=need_weight, need_bias=need_bias,
+                         bias_dtype=bias_dtype)
     return tuple(x.new_empty((0,)) if t is None else t for t in out)
 
 
 @_norm_bwd.register_fake
-def _(grad_y, x, weight, mean, rstd, need_x, need_weight, need_bias):
-    vec = x.new_empty(x.shape[-1:], dtype=x.dtype if weight is None else weight.dtype)
+def _(grad_y, x, weight, mean, rstd, need_x, need_weight, need_bias, bias_dtype=None):
+    vec = x.new_empty(x.shape[-1:], dtype=weight.dtype if weight is not None else bias_dtype or x.dtype)
     none = x.new_empty((0,))
     return (x.new_empty(x.shape) if need_x else none, vec if need_weight and weight is not None else none.clone(),
             torch.empty_like(vec) if need_bias else none.clone())
@@ -259,8 +260,8 @@ def _norm_backward(ctx, grad_y, grad_mean, grad_rstd):
     need_b = ctx.bias_dtype is not None and ctx.needs_input_grad[2]
     if grad_y is None or not (need_x or need_w or need_b):
         return None, None, None, None
-    dx, dw, db = _norm_bwd(grad_y, x, weight, mean, rstd, need_x, need_w, need_b)
-    return dx if need_x else None, dw if need_w else None, db.to(ctx.bias_dtype) if need_b else None, None
+    dx, dw, db = _norm_bwd(grad_y, x, weight, mean, rstd, need_x, need_w, need_b, ctx.bias_dtype)
+    return dx if need_x else None, dw if need_w else None, db if need_b else None, None
 
 
 _norm.register_autograd(_norm_backward, setup_context=_norm_setup)

@@ -203,10 +203,12 @@ def layer_norm_fwd(x, weight=None, bias=None, *, eps=1e-5):
     return y, mean, rstd
 
 
-def layer_norm_bwd(grad_y, x, weight, mean, rstd, *, need_x=True, need_weight=True, need_bias=True, workspace=None):
+def layer_norm_bwd(grad_y, x, weight, mean, rstd, *, need_x=True, need_weight=True, need_bias=True, workspace=None,
+                   bias_dtype=None):
     """Gradients of sum(grad_y * y): (grad_x, grad_weight, grad_bias), None where not wanted.  mean and rstd are the
-    forward's.  grad_x has x's dtype, the other two the weight's (float32 sums over the rows, rounded once; without a
-    weight, x's dtype and no grad_weight)."""
+    forward's.  grad_x has x's dtype, the other two the weight's (float32 sums over the rows, rounded once).  Without a
+    weight there is no grad_weight, and grad_bias has ``bias_dtype``: x's dtype (the default) or torch.float32, the
+    bias's own; with one, bias_dtype is the weight's if it is given."""
     x = _norm_rows(x, "x")
     w = _norm_vector(weight, "weight", x)
     gy = _norm_rows(grad_y, "grad_y")
@@ -218,10 +220,12 @@ def layer_norm_bwd(grad_y, x, weight, mean, rstd, *, need_x=True, need_weight=Tr
     mean, rstd = _dense(mean), _dense(rstd)
     H = x.shape[-1]
     rows = x.numel() // H
-    wdt = x.dtype if w is None else w.dtype
+    wdt = w.dtype if w is not None else x.dtype if bias_dtype is None else bias_dtype
+    if wdt not in (x.dtype, torch.float32) or bias_dtype not in (None, wdt):
+        raise TypeError("bias_dtype must be the weight's dtype, or without a weight the input's or float32")
     dx = torch.empty_like(x) if need_x else None
     dw = torch.empty_like(w) if need_weight and w is not None else None
-    db = (x.new_empty(H) if w is None else torch.empty_like(w)) if need_bias else None
+    db = (x.new_empty(H, dtype=wdt) if w is None else torch.empty_like(w)) if need_bias else None
     lib = library()
     ws = _scratch(lib.layer_norm_workspace_bytes(rows, H), workspace, x.device, "layer_norm_workspace_bytes")
     wp, wn = _ws_ptr(ws)

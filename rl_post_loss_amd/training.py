@@ -248,9 +248,10 @@ class AdamWPlan:
 
     ``params``, ``copies`` and the moments (``exp_avg``, ``exp_avg_sq``, and with 8-bit states ``exp_avg_scale``,
     ``exp_avg_sq_scale``) are lists of tensors that share storage with those given or made, so the plan keeps the
-    memory it updates alive.  A parameter whose storage is replaced (``p.data = ...``) needs a new plan."""
+    memory it updates alive.  A parameter whose storage is replaced (``p.data = ...``) needs a new plan.  A plan may be
+    dropped right after a step is enqueued, on any stream; a captured step needs its plan until the last replay."""
 
-    def __init__(self, params, copies, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, weight_decay):
+    def __init__(self, params, copies, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, weight_decay, made=()):
         self.params, self.copies = params, copies
         self.exp_avg, self.exp_avg_sq = exp_avg, exp_avg_sq
         self.exp_avg_scale, self.exp_avg_sq_scale = exp_avg_scale, exp_avg_sq_scale
@@ -273,7 +274,14 @@ class AdamWPlan:
             _pointers(exp_avg_sq_scale) if eight else None, 8 if eight else 32,
             (ctypes.c_double * count)(*weight_decay)))
         self._device = torch.from_numpy(self._host.view(np.int64)).to(self.device)
-        self._made_on = _stream(self.device)
+        self._made = [self._device, *made]       # allocated here, on the current stream
+        self._streams = {_stream(self.device)}   # streams that the allocator knows to use them
+
+    def _used_on_current_stream(self, stream: int) -> None:
+        """Tells the allocator, once a stream, that a plan dropped right after a step is still in use there."""
+        for t in self._made:
+            t.record_stream(torch.cuda.current_stream(self.device))
+        self._streams.add(stream)
 
     def moments(self, i: int):
         """The first and second moment of tensor i in float32, in its shape (8-bit states as the values they stand for)."""
@@ -328,7 +336,7 @@ def adamw_plan(params: Sequence[torch.Tensor], *, state_dtype=torch.float32, wei
         exp_avg, exp_avg_sq = list(exp_avg), list(exp_avg_sq)
         if len(exp_avg) != len(params) or len(exp_avg_sq) != len(params):
             raise ValueError("exp_avg and exp_avg_sq need one tensor per parameter")
-        state_dtype = exp_avg[0].dtype
+        state_dtype, made = exp_avg[0].dtype, []
     if state_dtype not in (torch.float32, torch.float8_e4m3fn):
         raise TypeError("moments must be float32 or float8_e4m3fn")
     eight = state_dtype == torch.float8_e4m3fn
@@ -353,6 +361,7 @@ def adamw_plan(params: Sequence[torch.Tensor], *, state_dtype=torch.float32, wei
         exp_avg, exp_avg_sq = zeros(), zeros()
         if eight:
             exp_avg_scale, exp_avg_sq_scale = ([torch.zeros(b, device=dev) for b in blocks] for _ in range(2))
+        made = [*exp_avg, *exp_avg_sq, *(exp_avg_scale or ()), *(exp_avg_sq_scale or ())]
     decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * len(params)
     if len(decay) != len(params):
         raise ValueError("weight_decay must be a number or one per parameter")
@@ -361,7 +370,7 @@ def adamw_plan(params: Sequence[torch.Tensor], *, state_dtype=torch.float32, wei
     spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in buffers)
     if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
         raise ValueError("the tensors of a plan must not overlap")
-    return AdamWPlan(params, copies, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, [float(d) for d in decay])
+    return AdamWPlan(params, copies, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, [float(d) for d in decay], made)
 
 
 def _device_scalar(t, name, dtype, device):
@@ -400,9 +409,9 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], *, step
     lr_at = _device_scalar(lr, "lr", torch.float32, dev) if isinstance(lr, torch.Tensor) else None
     scale_at = None if grad_scale is None else _device_scalar(grad_scale, "grad_scale", torch.float32, dev)
     stream = _stream(dev)
-    if stream != plan._made_on and not torch.cuda.is_current_stream_capturing():
-        plan._device.record_stream(torch.cuda.current_stream(dev))   # a plan dropped right after is still read there
     with _on(dev):
+        if stream not in plan._streams and not torch.cuda.is_current_stream_capturing():
+            plan._used_on_current_stream(stream)
         _check("rlpl_adamw_step", library().rlpl_adamw_step(
             plan._host.ctypes.data, plan._device.data_ptr(), pointers, DTYPE[gdt], 0.0 if lr_at else float(lr), lr_at,
             float(beta1), float(beta2), float(eps), 1 if step_at else int(step), step_at, scale_at,

@@ -7,6 +7,7 @@
 // stream.
 #include "train_abi.h"
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -23,40 +24,48 @@ constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxRows = int64_t(1) << 31;
 
 struct Device {
-    std::once_flag once;
-    int status = RLPL_ERR_DEVICE;
-    int cus = 0;
+    std::mutex lock;
+    std::atomic<bool> ready{false};
 };
 Device g_devices[kMaxDevices];
 
-// The current device, checked once: a gfx950 with a known number of compute units.
-int device(const Device** out) {
+// Whether device dev is a gfx950 with a known number of compute units, set up for the kernels.
+bool set_up(int dev) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess || std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return false;
+    int cus = 0;
+    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 1) return false;
+    // the contractions take their LDS ring beyond the default limit
+    for (int dt : {RLPL_F16, RLPL_BF16})
+        for (bool small : {false, true})
+            for (const void* k :
+                 {pick_ce_gemm(dt, small, kCeLogits), pick_ce_gemm(dt, small, kCeDlogits), pick_ce_grads(dt, small)})
+                if (hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                        small ? kCeSmall.lds : kCeLarge.lds) != hipSuccess)
+                    return false;
+    for (int dt : {RLPL_F16, RLPL_BF16})
+        if (hipFuncSetAttribute(pick_ce_deep_logits(dt), hipFuncAttributeMaxDynamicSharedMemorySize, kCeDeepLds) != hipSuccess)
+            return false;
+    return true;
+}
+
+// The current device, set up once.  A failure is not kept: the next call tries again.
+int device() {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
         (void)hipGetLastError();
         return RLPL_ERR_DEVICE;
     }
     Device& d = g_devices[dev];
-    std::call_once(d.once, [&d, dev] {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess || std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return;
-        if (hipDeviceGetAttribute(&d.cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || d.cus < 1) return;
-        // the contractions take their LDS ring beyond the default limit
-        for (int dt : {RLPL_F16, RLPL_BF16})
-            for (bool small : {false, true})
-                for (const void* k :
-                     {pick_ce_gemm(dt, small, kCeLogits), pick_ce_gemm(dt, small, kCeDlogits), pick_ce_grads(dt, small)})
-                    if (hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                            small ? kCeSmall.lds : kCeLarge.lds) != hipSuccess)
-                        return;
-        for (int dt : {RLPL_F16, RLPL_BF16})
-            if (hipFuncSetAttribute(pick_ce_deep_logits(dt), hipFuncAttributeMaxDynamicSharedMemorySize, kCeDeepLds) !=
-                hipSuccess)
-                return;
-        d.status = RLPL_OK;
-    });
-    *out = &d;
-    return d.status;
+    if (d.ready.load(std::memory_order_acquire)) return RLPL_OK;
+    const std::lock_guard<std::mutex> hold(d.lock);
+    if (d.ready.load(std::memory_order_relaxed)) return RLPL_OK;
+    if (!set_up(dev)) {
+        (void)hipGetLastError();
+        return RLPL_ERR_DEVICE;
+    }
+    d.ready.store(true, std::memory_order_release);
+    return RLPL_OK;
 }
 
 // ----------------------------------------------------------------------------- vocabulary cross entropy
@@ -204,8 +213,7 @@ int ce_check(const CeCall& c, bool grads) {
 int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     int st = ce_check(c, grads);
     if (st != RLPL_OK) return st;
-    const Device* d = nullptr;
-    if ((st = device(&d)) != RLPL_OK) return st;
+    if ((st = device()) != RLPL_OK) return st;
     const CeLayout L = ce_layout(c.n, c.h, c.vocab, grads);
     char* ws = static_cast<char*>(c.workspace);
     auto* state = reinterpret_cast<CeState*>(ws);
@@ -526,8 +534,7 @@ int rlpl_adamw_step(const void* plan, const void* plan_device, const void* const
     const auto* tensors = reinterpret_cast<const AdamTensor*>(static_cast<const char*>(plan) + h.tensors_at);
     for (int64_t i = 0; i < h.count; ++i)
         if (!is_aligned(grads[i], dtype_bytes(grad_dtype))) return RLPL_ERR_ALIGN;
-    const Device* d = nullptr;
-    const int st = device(&d);
+    const int st = device();
     if (st != RLPL_OK) return st;
     const char* dev = static_cast<const char*>(plan_device);
     AdamArgs a{};
@@ -584,8 +591,7 @@ int layer_norm_fwd(const void* x, const void* weight, const void* bias, int64_t 
     if (!is_aligned(x, e) || !is_aligned(y, e) || !is_aligned(weight, we) || !is_aligned(bias, we) ||
         !is_aligned(mean_out, 4) || !is_aligned(rstd_out, 4))
         return RLPL_ERR_ALIGN;
-    const Device* d = nullptr;
-    const int st = device(&d);
+    const int st = device();
     if (st != RLPL_OK) return st;
     const NormRowKernel k = pick_norm_fwd(dtype, weight_dtype, cols);
     if (!k.kernel) return RLPL_ERR_DTYPE;
@@ -610,8 +616,7 @@ int layer_norm_bwd(const void* grad_y, const void* x, const void* weight, const 
     const NormLayout L = norm_layout(rows, cols);
     if (!workspace || workspace_bytes < L.total) return RLPL_ERR_WORKSPACE;
     if (!is_aligned(workspace, 256)) return RLPL_ERR_ALIGN;
-    const Device* d = nullptr;
-    int st = device(&d);
+    int st = device();
     if (st != RLPL_OK) return st;
     const bool sums = grad_weight || grad_bias;
     if (!grad_x && !sums) return RLPL_OK;

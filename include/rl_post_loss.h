@@ -350,12 +350,15 @@ enum rlpl_reduction { RLPL_REDUCE_MEAN = 0, RLPL_REDUCE_SUM = 1 };
  * accumulate  : nonzero adds to grad_weight and grad_bias (RLPL_F32 only), else they are overwritten
  * workspace   : linear_cross_entropy_workspace_bytes(n, hidden_size, vocab, gradients wanted) bytes,
  *               256-byte aligned, no initial contents needed; one call in flight
- *               per workspace.  With gradients it holds one piece: up to 256 MiB of dz and 512 MiB of
- *               logits, or 16 KiB of dz a row where that is more
+ *               per workspace.  It holds a copy of the hidden states and 8 bytes a row and tile of
+ *               the vocabulary; with gradients also one piece's dz (up to 256 MiB, or 16 KiB a row where
+ *               that is more), the first columns' logits in float32 (up to 512 MiB), the hidden
+ *               gradient's float32 sums (n hidden_size of them, several times that for few rows) and
+ *               the bias gradient's, one for each vocabulary entry and tile of rows
  * Outputs overlap neither each other nor an input.
  *
- * Shapes: 1 <= n <= 2^24, hidden_size a multiple of 8 in [8, 65536], 1 <= vocab < 2^22 and fewer than 2^22
- * tiles of 256 rows by 256 vocabulary entries, 2^18 of 256 rows by 256 hidden values; 0 <= z_loss <= 1.
+ * Shapes: 1 <= n <= 2^24, hidden_size a multiple of 8 in [8, 65536], 1 <= vocab < 2^22; fewer than 2^22
+ * tiles of 256 rows by 256 vocabulary entries, and of 256 rows by 256 hidden values; 0 <= z_loss <= 1.
  */
 size_t linear_cross_entropy_workspace_bytes(int64_t n, int64_t hidden_size, int64_t vocab, int gradients);
 

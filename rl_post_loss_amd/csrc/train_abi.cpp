@@ -72,7 +72,10 @@ int device() {
 
 constexpr int64_t kCeMaxVocab = int64_t(1) << 22;     // a 256-row panel is addressed with 32-bit offsets
 constexpr int64_t kCeMaxHidden = 65536;
-constexpr int64_t kCeMaxTiles = int64_t(1) << 22;     // workgroups of one launch (x 512 lanes < 2^32)
+// Tiles of one product (x 512 lanes < 2^31).  The launch of both gradient products has the hidden product's and the
+// weight's, vocabulary by hidden tiles, which with at most 2^14 and 2^8 of those reach 2^22 only where the rows are
+// fewer than 2^8 tiles: the two together stay below 2^23.
+constexpr int64_t kCeMaxTiles = int64_t(1) << 22;
 // A piece of the vocabulary: kCePieceElements of dz (256 MiB), at least kCePieceCols columns, so that
 // adding a piece's hidden gradient to the float32 planes stays small beside its product.  Where that least number
 // does not make it larger, the loss's pass leaves the logits of the first columns, as many as a piece of all rows has

@@ -73,8 +73,45 @@ static int device_failures() {
     return 0;
 }
 
+// The header's bounds are the code's, and every launch of a shape within them has fewer than 2^32 lanes, the joint
+// launch of both gradient products among them.
+static int cross_entropy_shapes() {
+    const int64_t rows[] = {1, 15, 16, 255, 256, 257, 2048, 2049, 8191, 16384, 65536, 1 << 20, (1 << 22) - 1, 1 << 22, 1 << 24};
+    const int64_t hiddens[] = {8, 64, 256, 264, 4096, 16128, 16136, 16384, 32768, 65280, 65536};
+    const int64_t vocabs[] = {1, 255, 256, 257, 8192, 65535, 65536, 128256, 1 << 20, (1 << 22) - 256, (1 << 22) - 1};
+    const auto tiles = [](int64_t v) { return (v + 255) / 256; };
+    long taken = 0;
+    for (int64_t n : rows)
+        for (int64_t h : hiddens)
+            for (int64_t v : vocabs) {
+                const bool within = tiles(n) * tiles(v) < (1 << 22) && tiles(n) * tiles(h) < (1 << 22);
+                for (int grads = 0; grads < 2; ++grads) {
+                    const size_t bytes = linear_cross_entropy_workspace_bytes(n, h, v, grads);
+                    CHECK((bytes > 0) == within);
+                    if (!within) continue;
+                    if (grads) {           // what the header says that it holds: dz, planes, column sums
+                        CHECK(bytes >= size_t(n) * 2 * size_t(v < 8192 ? v : 8192) + size_t(n) * 4 * size_t(h));
+                        CHECK(bytes >= size_t(tiles(n)) * size_t(v) * 4);
+                    }
+                    g_lanes = 0;
+                    const auto targets = static_cast<int64_t*>(at(A));
+                    const auto loss = static_cast<float*>(at(A));
+                    CHECK((grads ? linear_cross_entropy(at(A), at(A), at(A), targets, n, h, v, RLPL_BF16, -100, 0.0f, 0, loss,
+                                                        at(A), at(A), at(A), RLPL_BF16, 0, at(A), bytes, nullptr)
+                                 : linear_cross_entropy_fwd(at(A), at(A), at(A), targets, n, h, v, RLPL_BF16, -100, 0.0f, 0,
+                                                            loss, at(A), bytes, nullptr)) == RLPL_OK);
+                    CHECK(g_lanes > 0 && g_lanes < (uint64_t(1) << 32));
+                    ++taken;
+                }
+            }
+    CHECK(taken > 1000);
+    CHECK(linear_cross_entropy_workspace_bytes(int64_t(1) << 24, 16384, 100, 1) == 0);   // 2^22 tiles of rows by hidden values
+    CHECK(linear_cross_entropy_workspace_bytes(int64_t(1) << 24, 16128, 100, 1) > 0);
+    return 0;
+}
+
 int main() {
-    if (device_failures()) return 1;
+    if (device_failures() || cross_entropy_shapes()) return 1;
     std::printf("ok %ld checks\n", g_checks);
     return 0;
 }

@@ -443,7 +443,10 @@ int layer_norm_bwd(const void* grad_y, const void* x, const void* weight, const 
  * rounded up with the probability of the part that rounding down would drop,
  * by 16 random bits hashed from (seed, t, the tensor's place in the list, the
  * element), so that the same call on the same state gives the same bits; a
- * root above zero is never rounded to zero.  An element that is not finite
+ * root above zero is never rounded to zero.  The first moment and the root are
+ * right on average; the root's square, the second moment, is held higher by the
+ * roundings' variance: by 5 % with Gaussian gradients and beta2 = 0.999, an
+ * eighth at most in e4m3's normal range.  An element that is not finite
  * becomes NaN and leaves its block's others as they would be.
  *
  * A plan holds what does not change between steps.  rlpl_adamw_plan_build

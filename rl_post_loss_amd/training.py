@@ -308,7 +308,8 @@ def adamw_plan(params: Sequence[torch.Tensor], *, state_dtype=torch.float32, wei
     """A plan of AdamW steps over ``params`` (contiguous, of one device and dtype: float32, float16 or bfloat16).
 
     state_dtype: torch.float32, or torch.float8_e4m3fn for moments in 8 bits (one float32 scale per 256 consecutive
-    elements; ``exp_avg_sq`` then holds the second moment's root).  The moments are made, filled with zeros, unless
+    elements; ``exp_avg_sq`` then holds the second moment's root, which is right on average, and so its square a little
+    high: 5 % with Gaussian gradients and beta2 = 0.999, an eighth at most in the normal range).  The moments are made, filled with zeros, unless
     they are given (``exp_avg``, ``exp_avg_sq``, and the scales with 8-bit ones), as when a run is resumed.
     weight_decay: a number, or one per tensor.  copies: float16 or bfloat16 tensors, one per float32 parameter, that
     every step writes with the new values."""

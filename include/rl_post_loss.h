@@ -333,9 +333,9 @@ enum rlpl_reduction { RLPL_REDUCE_MEAN = 0, RLPL_REDUCE_SUM = 1 };
  *
  * The products run on the matrix cores with `dtype` operands (RLPL_F16 or
  * RLPL_BF16) and float32 accumulation.  dz is rounded to `dtype` (without s,
- * in fp16 at 256 times its value, so that |1 + 2 z_loss lse_i| must stay below
- * 255 there), the operand of the gradients' products; every output is rounded
- * once.  Each call enqueues several kernels on `stream`; sums have a fixed
+ * in fp16 at 256 times its value, or 128 or 64 with a z_loss over 0.254 or 0.51;
+ * |lse_i| up to 500 stays in fp16's range), the operand of the gradients'
+ * products; every output is rounded once.  Each call enqueues several kernels on `stream`; sums have a fixed
  * order (no atomics), so repeated calls give equal bits.
  *
  * hidden      : (n, hidden_size) `dtype`, dense row-major, 16-byte aligned

@@ -60,7 +60,7 @@ const void* ce_gather_kernel();
 
 // One of the step's four products (the kernel's template argument):
 //   kCeLogits   per row and tile of columns (max, sum exp(z - max)), and the target's logit
-//   kCeDlogits  dz of a piece of the vocabulary, in the operand dtype, scaled by kDzScale
+//   kCeDlogits  dz of a piece of the vocabulary, in the operand dtype, scaled by dz_scale
 //   kCeHidden   dz . weight of a piece, into (or added to) float32 planes, one a split of K
 //   kCeWeight   dz^T . hidden of a piece, scaled, in the gradient's dtype
 // with z = hidden . weight^T + bias.  A (M x K) and B (K x N) as in GemmArgs.
@@ -83,6 +83,7 @@ struct CeGemmArgs {
     int32_t first;             // vocabulary index of column 0
     const float* lse;          // (kept rows) (kCeDlogits)
     float z_loss2;             // 2 z_loss (kCeDlogits)
+    float dz_scale;            // (kCeDlogits)
     float* part;               // (kept rows, tiles_n, 2) (kCeLogits)
     float* target_logit;       // (kept rows) (kCeLogits)
     float* col_part;           // (tiles_m, col_ld) from column 0 on: sums of dz over a tile's rows, or NULL (kCeDlogits)
@@ -104,8 +105,15 @@ struct CeGradArgs {
 const void* pick_ce_grads(int dtype, bool small);
 
 // dz is held at this scale (the onehot's 1), so that small probabilities stay
-// above fp16's subnormals; bf16 has float32's range.
-inline float ce_dz_scale(int dtype) { return dtype == 1 ? 256.0f : 1.0f; }
+// above fp16's subnormals; bf16 has float32's range.  A penalty's factor
+// 1 + 2 z_loss lse takes room above: the scale is the largest of 256, 128 and
+// 64 (z_loss <= 1) that holds it for |lse| up to 500.
+inline float ce_dz_scale(int dtype, float z_loss) {
+    if (dtype != 1) return 1.0f;
+    float scale = 256.0f;
+    while (scale * (1.0f + 1000.0f * z_loss) > 65504.0f) scale *= 0.5f;
+    return scale;
+}
 
 // A kept row's log-sum-exp and loss; the workgroup that is done last sums the rows' losses.
 struct CeRowArgs {

@@ -19,9 +19,10 @@
 // it from there.  The weight's gradient of a piece comes out whole, so it is rounded once and written once;
 // the hidden states' is summed over the pieces in float32.
 //
-// dz is formed without s and held at a fixed scale (its largest value is
-// about 1): s would push a long batch's small probabilities under fp16's
-// range.  The factor is applied to the float32 results.
+// dz is formed without s and, in fp16, held at a scale that z_loss alone decides
+// (ce_kernels.h; without a penalty its largest value is about 1): s would push a
+// long batch's small probabilities under fp16's range.  Both factors are applied
+// to the float32 results.
 //
 // What bounds it: the products, 6 n H V operations (8 where logits are formed again), where n is large, and
 // there the port of LDS.  A step of 64 of K over a 256 x 256 tile has 2048 cycles of matrix instructions;
@@ -44,9 +45,6 @@
 namespace rlpl {
 
 namespace {
-
-template <typename T> constexpr float kDzScale = 1.0f;
-template <> constexpr float kDzScale<_Float16> = 256.0f;
 
 // A wavefront's 128 x 64 block as 8 x 4 tiles of v_mfma_f32_16x16x32: at random operands, which hold the
 // chip to its power, it reaches 2.04 PFLOP/s from registers against 1.82 for 32x32x16 (a loop of
@@ -620,7 +618,7 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
             const float lse = row < M ? g.lse[row] : 0.0f;
             const int t = row < M ? g.target[row] - g.first - n0 : -1;
             row_lse[threadIdx.x] = lse;
-            row_f[threadIdx.x] = row < M ? kDzScale<T> * (1.0f + g.z_loss2 * lse) : 0.0f;
+            row_f[threadIdx.x] = row < M ? g.dz_scale * (1.0f + g.z_loss2 * lse) : 0.0f;
             tgt_col[threadIdx.x] = t >= 0 && t < S::BN && n0 + t < g.N ? t : -1;
         }
         __syncthreads();
@@ -635,7 +633,7 @@ __device__ __forceinline__ void ce_tile(const CeGemmArgs& g, const uint32_t bloc
 #pragma unroll
                 for (int j = 0; j < S::kColTiles; ++j) {
                     const float p = __builtin_amdgcn_exp2f((acc[i][j][e] - l) * kLog2eG);
-                    acc[i][j][e] = (f != 0.0f ? f * p : 0.0f) - (col_of(j) == tc ? kDzScale<T> : 0.0f);
+                    acc[i][j][e] = (f != 0.0f ? f * p : 0.0f) - (col_of(j) == tc ? g.dz_scale : 0.0f);
                 }
             }
         if (g.col_part) {
@@ -745,13 +743,13 @@ __global__ void __launch_bounds__(S::kThreads) ce_dz(const CeGemmArgs g) {
         for (int e = 0; e < 4; ++e) {
             const int row = row0 + 4 * (lane >> 4) + e;
             const float lse = row < M ? g.lse[row] : 0.0f;
-            const float f = row < M ? kDzScale<T> * (1.0f + g.z_loss2 * lse) : 0.0f;
+            const float f = row < M ? g.dz_scale * (1.0f + g.z_loss2 * lse) : 0.0f;
             const int target = row < M ? g.target[row] - g.first : -1;
 #pragma unroll
             for (int j = 0; j < S::kColTiles; ++j) {
                 const int col = n0 + wn * S::kWaveN + j * 16 + (lane & 15);
                 const float p = __builtin_amdgcn_exp2f((z[j][e] - lse) * kLog2eG);
-                z[j][e] = (f != 0.0f ? f * p : 0.0f) - (col == target && col < g.N ? kDzScale<T> : 0.0f);
+                z[j][e] = (f != 0.0f ? f * p : 0.0f) - (col == target && col < g.N ? g.dz_scale : 0.0f);
                 sum[j] += z[j][e];
             }
         }

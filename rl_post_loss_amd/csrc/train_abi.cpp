@@ -248,6 +248,7 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     z.target = ints(L.target);
     z.part = floats(L.part);
     z.target_logit = floats(L.target_logit);
+    z.dz_scale = ce_dz_scale(c.dtype, c.z_loss);
     const auto product = [&](const void* kernel, const CeShape& shape, const auto& args, uint32_t blocks) {
         return enqueue(kernel, args, dim3(blocks), shape.threads, stream, size_t(shape.lds));
     };
@@ -263,7 +264,7 @@ int ce_run(const CeCall& c, bool grads, hipStream_t stream) {
     if (st != RLPL_OK) return st;
     const uint32_t tiles_h = uint32_t(div_up(c.h, L.g.tile));
     const CeRowArgs rows{floats(L.part), floats(L.target_logit), ints(L.target), state, floats(L.lse), floats(L.row_loss),
-                         c.loss, c.z_loss, 1.0f / ce_dz_scale(c.dtype), int32_t(L.tiles_n),
+                         c.loss, c.z_loss, 1.0f / z.dz_scale, int32_t(L.tiles_n),
                          c.reduction == RLPL_REDUCE_MEAN ? 1 : 0, int32_t(L.piece), grads ? int32_t(L.splits) : 1,
                          uint32_t(L.plane_rows), tiles_h,
                          c.grad_weight ? uint32_t(div_up(L.piece < c.vocab ? L.piece : c.vocab, L.g.tile)) * tiles_h : 0,

@@ -119,7 +119,8 @@ def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_
 
     hidden (*, H) and weight (V, H) float16 or bfloat16, H a multiple of 8; bias (V,) or None; targets int64, of hidden's
     leading shape.  Rows whose target is ``ignore_index`` do not count.  loss is the mean (or sum) over the others of
-    lse - z[target] + z_loss * lse^2, a 0-d float32 tensor, and 0 where no row counts.
+    lse - z[target] + z_loss * lse^2, a 0-d float32 tensor, and 0 where no row counts.  0 <= z_loss <= 1; with fp16 operands
+    the penalty's factor 1 + 2 z_loss lse fits where |lse| <= 500 (beyond, gradients may overflow to NaN).
 
     weight_grad_dtype: the operands' dtype (the default) or torch.float32, of grad_weight and grad_bias;
     hidden_grad_dtype: likewise, of grad_hidden.  Passing ``grad_weight`` / ``grad_bias`` (contiguous float32) adds to

@@ -158,6 +158,8 @@ def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_
     with _on(dev):
         _check("linear_cross_entropy",
                lib.rlpl_linear_cross_entropy(CE_HIDDEN_F32, *args) if wide else lib.linear_cross_entropy(*args))
+    if accumulate:
+        increment_version([t for t in (dw, db) if t is not None])   # a graph that saved an old value says so
     return loss, dh if dh is None or hidden.dim() == 2 else dh.view(hidden.shape), dw, db
 
 

@@ -315,8 +315,9 @@ enum rlpl_reduction { RLPL_REDUCE_MEAN = 0, RLPL_REDUCE_SUM = 1 };
 /*
  * Softmax cross entropy of an output projection over a large vocabulary, with
  * its gradients, in pieces of the vocabulary (the supervised sibling of the
- * selective log-probabilities: no more than one piece's logits are held).  Over the rows i
- * whose target y_i is not ignore_index, N of them,
+ * selective log-probabilities): up to 2^27 logits are held in float32, the
+ * others are formed twice.  Over the rows i whose target y_i is not
+ * ignore_index, N of them,
  *
  *   z_i  = hidden[i] . weight^T + bias,   lse_i = log sum_v exp(z_i[v])
  *   loss = s sum_i (lse_i - z_i[y_i] + z_loss lse_i^2)

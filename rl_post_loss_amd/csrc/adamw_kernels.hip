@@ -6,9 +6,10 @@
 // One launch covers up to 440 tensors: a workgroup takes one chunk of 4096
 // elements of one tensor, found through the plan's table.  Each element's
 // state is read and written once, which bounds it: 150 M parameters in 300
-// tensors with float32 moments, 16-bit gradients and copies take 0.90 ms (5.0
-// TB/s of 4.5 GB), 525 M with 8-bit moments 1.71 ms (4.9 TB/s of 8.4 GB; 1.84
-// ms while an element's rounding took 125 vector instructions instead of 100).
+// tensors with float32 moments, 16-bit gradients and copies take 0.81 to 0.92 ms
+// (kernel trace; 4.9 to 5.6 TB/s of 4.5 GB), 525 M with 8-bit moments 1.71 ms (4.9
+// TB/s of 8.4 GB; 1.84 ms while an element's rounding took 125 vector instructions
+// instead of 100).
 //
 // 8-bit moments: 256 consecutive elements of a tensor share a float32 scale,
 // their largest magnitude / 448, and are held as e4m3 values of x / scale.

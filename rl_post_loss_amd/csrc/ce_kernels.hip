@@ -1,6 +1,6 @@
 // Softmax cross entropy of an output projection over a large vocabulary on
-// gfx950, with its gradients, in pieces of the vocabulary: never more than one
-// piece's worth of logits is held.  For the rows i whose target y_i is not ignored (N of them),
+// gfx950, with its gradients, in pieces of the vocabulary: up to 2^27 logits are
+// held in float32, one piece's worth.  For the rows i whose target y_i is not ignored (N of them),
 //
 //   z_i = hidden_i . weight^T + bias,   lse_i = log sum_v exp(z_iv)
 //   loss = s sum_i (lse_i - z_i[y_i] + c lse_i^2),   s = 1 / max(N, 1) or 1
@@ -24,11 +24,17 @@
 // long batch's small probabilities under fp16's range.  Both factors are applied
 // to the float32 results.
 //
-// What bounds it: the products, 6 n H V operations (8 where logits are formed again), where n is large, and
-// there the port of LDS.  A step of 64 of K over a 256 x 256 tile has 2048 cycles of matrix instructions;
-// its fragment reads take 1573 alone and its copies 1863, both 2575 together, the step 2860 (8192^3,
-// 1.37 PFLOP/s; 1.22 at 1024 x 4096 x 128256).  Few rows are bound by the weight's bytes: 16 rows of 4096 x 128256
-// read it at 4.4 to 5.5 TB/s (logits 190 to 237 us), and write its gradient beside (483 to 525).
+// What bounds it: the products, 6 n H V operations (8 where logits are formed
+// again), where n is large.  In them a tile's ends: its ring leaves a compute
+// unit no second workgroup to cover its first copies and its epilogue, 13 us by
+// the fit of train_abi.cpp beside 1.1 a step of K (the weight's product over 1024
+// rows has 16 steps).  Within the steps the port of LDS: a step of 64 of K over a
+// 256 x 256 tile has 2048 cycles of matrix instructions; its fragment reads take
+// 1573 alone and its copies 1863, both 2575 together, the step 2860 (8192^3, 1.37
+// PFLOP/s, where the library's product by tiles of this size reaches 1.61; 1.22
+// at 1024 x 4096 x 128256).  Few rows are bound by the weight's bytes: 16 rows of
+// 4096 x 128256 read it at 4.4 to 5.5 TB/s (logits 190 to 237 us), and write its
+// gradient beside (483 to 525).
 //
 // The contraction and its tiles are those of mfma_tile.h.
 #include <hip/hip_runtime.h>

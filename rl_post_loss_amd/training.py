@@ -113,9 +113,10 @@ def linear_cross_entropy_fwd(hidden, weight, bias, targets, *, ignore_index=-100
 def linear_cross_entropy(hidden, weight, bias, targets, *, ignore_index=-100, z_loss=0.0, reduction="mean",
                          need_hidden=True, need_weight=True, need_bias=True, weight_grad_dtype=None, grad_weight=None,
                          grad_bias=None, workspace=None, hidden_grad_dtype=None):
-    """Softmax cross entropy of the logits hidden . weight^T + bias, with its gradients, in pieces of the vocabulary
-    (no more than one piece's logits are held): (loss, grad_hidden, grad_weight, grad_bias), None for gradients not
-    wanted and for a bias that is not there (unless its gradient is passed to be added to).
+    """Softmax cross entropy of the logits hidden . weight^T + bias, with its gradients, in pieces of the vocabulary:
+    (loss, grad_hidden, grad_weight, grad_bias), None for gradients not wanted and for a bias that is not there (unless
+    its gradient is passed to be added to).  Up to 2^27 logits are held in float32 (all of 1024 x 128256, in a
+    workspace of 0.93 GB), the others are formed twice.
 
     hidden (*, H) and weight (V, H) float16 or bfloat16, H a multiple of 8; bias (V,) or None; targets int64, of hidden's
     leading shape.  Rows whose target is ``ignore_index`` do not count.  loss is the mean (or sum) over the others of
@@ -312,8 +313,9 @@ def adamw_plan(params: Sequence[torch.Tensor], *, state_dtype=torch.float32, wei
 
     state_dtype: torch.float32, or torch.float8_e4m3fn for moments in 8 bits (one float32 scale per 256 consecutive
     elements; ``exp_avg_sq`` then holds the second moment's root, which is right on average, and so its square a little
-    high: 5 % with Gaussian gradients and beta2 = 0.999, an eighth at most in the normal range).  The moments are made, filled with zeros, unless
-    they are given (``exp_avg``, ``exp_avg_sq``, and the scales with 8-bit ones), as when a run is resumed.
+    high: 5 % with Gaussian gradients and beta2 = 0.999, an eighth at most in the normal range).  The moments are made,
+    filled with zeros, unless they are given (``exp_avg``, ``exp_avg_sq``, and the scales with 8-bit ones), as when a
+    run is resumed.
     weight_decay: a number, or one per tensor.  copies: float16 or bfloat16 tensors, one per float32 parameter, that
     every step writes with the new values."""
     params = list(params)

@@ -6,7 +6,7 @@ import rl_post_loss_amd as rl
 from test_adamw import DEV, F8, HYPER, same, tensors
 
 pytestmark = pytest.mark.gpu
-SIZES = [70000, 300, 1 << 20]
+SIZES = [70000, 0, 300, 1 << 20]
 
 
 @pytest.mark.parametrize("state", [torch.float32, F8])
@@ -27,7 +27,7 @@ def test_moments_outlive_a_dropped_plan(state):
         rl.adamw_step(plan, grads, step=1, seed=4, **HYPER)
     dt = torch.float32 if state == torch.float32 else torch.uint8
     del plan
-    taken = [torch.full((n,), 3, dtype=d, device=DEV) for n in SIZES for d in (dt, dt, torch.float32)]
+    taken = [torch.full((n,), 3, dtype=d, device=DEV) for n in SIZES if n for d in (dt, dt, torch.float32)]
     taken += [torch.full(((n + 255) // 256,), 3.0, device=DEV) for n in SIZES for _ in range(2)]
     torch.cuda.synchronize()
     assert all((t == 3).all() for t in taken)

@@ -82,3 +82,43 @@ def test_refusals_of_the_binding():
     for bad in (torch.float16, torch.float64):
         with pytest.raises(TypeError, match="hidden_grad_dtype"):
             rl.linear_cross_entropy(*args, hidden_grad_dtype=bad)
+
+
+@gpu
+def test_float32_hidden_gradients_of_no_rows_and_in_a_replayed_graph():
+    args = on_device(make(40, 64, 300, "fp16", ignored=1.1))
+    out = rl.linear_cross_entropy(*args, hidden_grad_dtype=torch.float32)
+    assert out[0] == 0 and out[1].dtype == torch.float32 and not out[1].any()
+    sets = [on_device(make(40, 64, 300, "fp16", ignored=0.3, seed=s)) for s in range(4)]
+    static = [t.clone() for t in sets[0]]
+    call = lambda a: rl.linear_cross_entropy(*a, hidden_grad_dtype=torch.float32)  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(static)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(static)
+    for c in sets[1:]:
+        for t, new in zip(static, c):
+            t.copy_(new)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, call(c)))
+
+
+@gpu
+@pytest.mark.parametrize("wanted", [(0,), (1,), (2,), (0, 2), (1, 2)])
+def test_fp16_gradients_of_some_inputs(wanted):
+    args = on_device(make(90, 64, 500, "fp16", ignored=0.2))
+    leaves = [t.clone().requires_grad_(i in wanted) for i, t in enumerate(args[:3])]
+    (256.0 * rl.linear_cross_entropy_autograd(*leaves, args[3], reduction="sum")).backward()
+    need = dict(need_hidden=0 in wanted, need_weight=1 in wanted, need_bias=2 in wanted)
+    direct = rl.linear_cross_entropy(*args, reduction="sum", weight_grad_dtype=torch.float32,
+                                     hidden_grad_dtype=torch.float32, **need)
+    for i, (t, g) in enumerate(zip(leaves, direct[1:])):
+        assert (t.grad is None) == (i not in wanted)
+        assert g is None or torch.equal(t.grad, (g * 256.0).half())

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import rl_post_loss_amd as rl
-from test_linear_cross_entropy import DEV, E, IGNORE, make, on_device
+from test_linear_cross_entropy import DEV, IGNORE, make, on_device
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")

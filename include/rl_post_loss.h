@@ -480,6 +480,168 @@ int rlpl_adamw_step(const void* plan, const void* plan_device, const void* const
                     const float* lr_device, double beta1, double beta2, double eps, int64_t step,
                     const int64_t* step_device, const float* grad_scale, uint32_t seed, hipStream_t stream);
 
+/*
+ * RMS norm of rows, with the addition of a residual:
+ *
+ *   h_ij    = x_ij + residual_ij (rounded to `stream_dtype`), or x_ij without a residual
+ *   rstd_i  = 1 / sqrt(avg_j h_ij^2 + eps),   y_ij = h_ij rstd_i weight_j
+ *
+ * The norm is that of h as it is stored.  rms_norm_fp8 writes y in 8 bits
+ * instead: e4m3 values q with one float32 scale for every 128 columns (the
+ * last group may be shorter), y ~ q scale, scale = the group's largest finite
+ * magnitude / 448 (0 for a group below 2^-118), y 448 / largest rounded to
+ * nearest even; a value that is not finite becomes NaN and leaves its group's
+ * others as they are.  Backward, for grad_y = d L / d y, grad_stream = d L / d h
+ * from elsewhere, xhat_ij = h_ij rstd_i and g_ij = grad_y_ij weight_j:
+ *
+ *   grad_h_ij     = rstd_i (g_ij - xhat_ij avg_j (g_ij xhat_ij)) + grad_stream_ij
+ *   grad_weight_j = sum_i grad_y_ij xhat_ij
+ *
+ * grad_h is the gradient of x and of the residual alike.  Statistics and sums
+ * are float32, every output is rounded once, and the reduction over the rows
+ * has a fixed order (no atomics).
+ *
+ * x, y, grad_y                      : (rows, cols) `dtype`, dense row-major
+ * residual, stream_out              : (rows, cols) `stream_dtype` (`dtype` or RLPL_F32), or both NULL;
+ *                                     stream_out receives h, and may be the residual or, with the same type, x
+ * h, grad_stream, grad_h            : (rows, cols) `stream_dtype`; grad_stream NULL for zeros, grad_h NULL if not wanted
+ * weight, grad_weight               : (cols,) `weight_dtype` (`dtype` or RLPL_F32); weight NULL for ones,
+ *                                     grad_weight NULL if not wanted
+ * q, scale                          : (rows, cols) bytes, (rows, (cols + 127) / 128) float32
+ * rstd                              : (rows,) float32; the forward's may be NULL (not wanted)
+ * workspace                         : rms_norm_workspace_bytes(rows, cols) bytes, 256-byte aligned, no initial
+ *                                     contents needed; one call in flight per workspace
+ *
+ * 1 <= rows < 2^31, 1 <= cols <= 16384.  Pointers aligned to their elements.  Apart from what is said above, outputs
+ * overlap neither each other nor an input.
+ */
+int rms_norm_fwd(const void* x, const void* weight, const void* residual, int64_t rows, int64_t cols, int dtype,
+                 int weight_dtype, int stream_dtype, float eps, void* y, float* rstd_out, void* stream_out,
+                 hipStream_t stream);
+
+int rms_norm_fp8(const void* x, const void* weight, const void* residual, int64_t rows, int64_t cols, int dtype,
+                 int weight_dtype, int stream_dtype, float eps, void* q, float* scale, float* rstd_out, void* stream_out,
+                 hipStream_t stream);
+
+size_t rms_norm_workspace_bytes(int64_t rows, int64_t cols);
+
+int rms_norm_bwd(const void* grad_y, const void* h, const void* weight, const float* rstd, const void* grad_stream,
+                 int64_t rows, int64_t cols, int dtype, int weight_dtype, int stream_dtype, void* grad_h, void* grad_weight,
+                 void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* How rlpl_grad_norm joins the gradients. */
+enum rlpl_norm_kind { RLPL_NORM_2 = 0, RLPL_NORM_INF = 1 };
+
+/*
+ * The norm over a list of gradients, and the factor that clips it:
+ *
+ *   norm  = |s| (sum g^2)^(1/2)  or  |s| max |g|,   scale = s min(1, max_norm / (norm + eps))
+ *
+ * with s = *grad_scale (1 where that is NULL; 1 / a loss scale, for instance):
+ * scale is what rlpl_adamw_step takes as its grad_scale.  Squares are summed in
+ * float64 in a fixed order (no atomics).  A NaN among the gradients makes both
+ * NaN; an infinite norm gives a scale of +-0.
+ *
+ * rlpl_grad_scale multiplies the tensors by *scale in place, each element
+ * rounded once; a factor of exactly 1 writes nothing.
+ *
+ * grads, sizes, dtypes : device pointers, elements (0 <= size <= 2^40) and types (RLPL_F32, RLPL_F16, RLPL_BF16), one
+ *                        per tensor (host arrays, read during the call only); pointers aligned to their elements.
+ *                        Tensors of rlpl_grad_scale must not overlap (RLPL_ERR_PARAM)
+ * norm_out, scale_out  : 1 float each (device memory, written); scale_out NULL: not wanted, max_norm and eps ignored
+ * grad_scale, scale    : 1 float (device memory)
+ * max_norm, eps        : >= 0
+ * workspace            : rlpl_grad_norm_workspace_bytes(sizes, count) bytes, 256-byte aligned, no initial contents
+ *                        needed; one call in flight per workspace
+ *
+ * A call enqueues one launch per 190 tensors and one more; a list of up to 65,536 elements (in chunks of 4096 of one
+ * tensor, 16 of them) takes one launch.
+ */
+size_t rlpl_grad_norm_workspace_bytes(const int64_t* sizes, int64_t count);
+
+int rlpl_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int64_t count, int norm_kind,
+                   const float* grad_scale, float max_norm, float eps, float* norm_out, float* scale_out, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream);
+
+int rlpl_grad_scale(void* const* grads, const int64_t* sizes, const int32_t* dtypes, int64_t count, const float* scale,
+                    hipStream_t stream);
+
+/*
+ * Log-probabilities of given tokens over rows of logits, with each row's
+ * entropy and its most likely tokens.  For a row z at temperature T,
+ *
+ *   lse  = log sum_v exp(z_v / T),   logp = z_y / T - lse,   p_v = exp(z_v / T - lse)
+ *   entropy = -sum_v p_v log p_v (a term with p_v = 0 adds nothing)
+ *   top_logp, top_index: the top_k largest z_v / T - lse in falling order, the lowest index first among equal ones
+ *
+ * and, for gradients g of logp and h of the entropy,
+ *
+ *   grad_logits_v = (g ((v == y) - p_v) - h p_v (log p_v + entropy)) / T
+ *
+ * A row whose mask byte is zero is not read: its outputs are 0, its indices -1, its gradients +0.  A target outside
+ * [0, vocab) gives logp = NaN and no one-hot term.  A logit of -inf has probability 0; a row of them
+ * alone, or with a NaN or +inf, gives NaN (and indices of -1 but for the row of -inf).  One pass over the logits, sums in
+ * float32 in a fixed order.
+ *
+ * logits      : `dtype`, row r's vocab elements side by side from group_stride (r / inner) + row_stride (r % inner)
+ *               elements on: inner = rows and row_stride = vocab for a dense (rows, vocab), group_stride =
+ *               (T + 1) vocab and inner = T for the first T of T + 1 positions of each sequence.  Aligned to its
+ *               elements; rows of 16-byte alignment go faster
+ * targets     : (rows,) int64
+ * mask        : (rows,) bytes, or NULL (every row counts)
+ * logp_out, lse_out, entropy_out : (rows,) float32; entropy_out may be NULL (not wanted)
+ * top_logp_out, top_index_out    : (rows, top_k) float32 and int64, written if top_k > 0
+ * lse, entropy                   : the forward's; entropy is read with grad_entropy only
+ * grad_logp, grad_entropy        : (rows,) float32, or NULL (zeros)
+ * grad_logits : (rows, vocab) `dtype`, dense, written; must not overlap the logits
+ * workspace   : token_logprobs_workspace_bytes(rows, vocab, top_k) bytes, 256-byte aligned, no initial contents needed;
+ *               one call in flight per workspace
+ *
+ * 1 <= rows < 2^31, 1 <= vocab <= 2^31 - 65536, 0 <= top_k <= min(64, vocab), 1 <= inner <= rows, strides >= 0;
+ * T finite and above 0.
+ */
+size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top_k);
+
+int token_logprobs_fwd(const void* logits, const int64_t* targets, const void* mask, int64_t rows, int64_t vocab,
+                       int64_t inner, int64_t group_stride, int64_t row_stride, int dtype, float temperature, int64_t top_k,
+                       float* logp_out, float* lse_out, float* entropy_out, float* top_logp_out, int64_t* top_index_out,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+int token_logprobs_bwd(const void* logits, const int64_t* targets, const void* mask, const float* lse, const float* entropy,
+                       const float* grad_logp, const float* grad_entropy, int64_t rows, int64_t vocab, int64_t inner,
+                       int64_t group_stride, int64_t row_stride, int dtype, float temperature, void* grad_logits,
+                       hipStream_t stream);
+
+/*
+ * Products of 8-bit operands, e4m3 values with a float32 scale for each block
+ * of 128: a scoring pass's output projection,
+ *
+ *   out[i][v] = sum_b x_scale[i][b] weight_scale[v / 128][b] sum_{k in block b} x[i][k] weight[v][k]  (+ bias[v])
+ *
+ * with K cut into blocks of 128 (the last may be shorter).  rms_norm_fp8 gives x and x_scale; rlpl_fp8_quantize makes
+ * both operands from (rows, cols) float32, float16 or bfloat16: block_rows 1 (scales (rows, blocks)) or 128 (scales
+ * ((rows + 127) / 128, blocks), for the weight), rounded as rms_norm_fp8 does.  The products run on the matrix cores,
+ * sums are float32 in a fixed order, the output is rounded once.
+ *
+ * x, weight    : (n, hidden_size), (vocab, hidden_size) bytes, dense, 16-byte aligned
+ * bias         : (vocab,) `out_dtype`, or NULL
+ * out          : (n, vocab) `out_dtype` (RLPL_F32, RLPL_F16, RLPL_BF16), dense
+ * q            : (rows, cols) bytes, dense; row_stride is x's, in elements
+ * workspace    : fp8_linear_workspace_bytes(n, hidden_size, vocab) bytes, 256-byte aligned, no initial contents needed;
+ *                one call in flight per workspace
+ *
+ * 1 <= n <= 2^20, hidden_size a multiple of 16 in [16, 65536], 1 <= vocab < 2^22; for rlpl_fp8_quantize 1 <= rows < 2^31,
+ * 1 <= cols <= 2^31 - 65536.
+ */
+int rlpl_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t row_stride, int dtype, int block_rows, void* q,
+                      float* scale, hipStream_t stream);
+
+size_t fp8_linear_workspace_bytes(int64_t n, int64_t hidden_size, int64_t vocab);
+
+int fp8_linear(const void* x, const float* x_scale, const void* weight, const float* weight_scale, const void* bias, int64_t n,
+               int64_t hidden_size, int64_t vocab, int out_dtype, void* out, void* workspace, size_t workspace_bytes,
+               hipStream_t stream);
+
 /* bnpo_loss for callers that cannot allocate (code under HIP graph capture,
  * tight serving loops, harnesses that forbid hipMalloc): the same kernels,
  * results bit-identical to bnpo_loss, with no workspace argument.  The

@@ -27,6 +27,14 @@ Entry points (model card "Geometric-AI Kernels": sections "BNPO Loss",
   ``linear_cross_entropy_fwd(...)`` -> loss: the supervised loss of the same projection, in pieces of the vocabulary
 * ``layer_norm_fwd(x, weight, bias)`` -> (y, mean, rstd) and ``layer_norm_bwd(grad_y, x, weight, mean, rstd)`` ->
   (grad_x, grad_weight, grad_bias): the norm in front of the output projection
+* ``rms_norm_fwd(x, weight, residual)`` -> (y, rstd, stream), ``rms_norm_fp8(...)`` -> (q, scale, rstd, stream) in 8 bits,
+  and ``rms_norm_bwd(grad_y, h, weight, rstd, grad_stream)`` -> (grad_h, grad_weight): the norm with the residual's addition
+* ``token_logprobs_fwd(logits, targets, mask)`` -> (logp, lse, entropy, top_logp, top_index) over (*, V) logit rows, and
+  ``token_logprobs_bwd(...)`` -> grad_logits
+* ``fp8_linear(x, x_scale, weight, weight_scale)`` -> the logits of an 8-bit output projection with a scale for each
+  block of 128, and ``fp8_quantize(x)`` -> (q, scale)
+* ``grad_norm(grads)`` -> the norm over many gradients (and the factor that clips it, which ``adamw_step`` takes),
+  ``scale_grads(grads, scale)`` and ``clip_grads(grads, max_norm)`` in place
 * ``adamw_plan(params, ...)`` and ``adamw_step(plan, grads, step=, lr=)``: the update of many tensors at once, with
   moments in float32 or in 8 bits
 
@@ -64,7 +72,9 @@ __all__ = ["bnpo_loss", "bnpo_loss_fwd", "grpo_loss", "grpo_loss_fwd", "reverse_
            "grpo_loss_autograd", "reverse_kl_autograd", "reverse_kl_logits_autograd",
            "selective_logprob_fwd", "selective_logprob_bwd", "selective_logprob_autograd",
            "linear_cross_entropy", "linear_cross_entropy_fwd", "linear_cross_entropy_autograd",
-           "layer_norm_fwd", "layer_norm_bwd", "layer_norm_autograd", "adamw_plan", "adamw_step", "AdamWPlan"]
+           "layer_norm_fwd", "layer_norm_bwd", "layer_norm_autograd", "adamw_plan", "adamw_step", "AdamWPlan",
+           "rms_norm_fwd", "rms_norm_fp8", "rms_norm_bwd", "rms_norm_autograd", "grad_norm", "scale_grads", "clip_grads",
+           "token_logprobs_fwd", "token_logprobs_bwd", "token_logprobs_autograd", "fp8_quantize", "fp8_linear"]
 
 STATUS = {0: "RLPL_OK", 1: "RLPL_ERR_NULL", 2: "RLPL_ERR_SHAPE", 3: "RLPL_ERR_ALIGN",
           4: "RLPL_ERR_DTYPE", 5: "RLPL_ERR_PARAM", 6: "RLPL_ERR_WORKSPACE", 7: "RLPL_ERR_DEVICE",
@@ -144,8 +154,23 @@ def _declare(lib):
     lib.rlpl_adamw_plan_bytes.argtypes, lib.rlpl_adamw_plan_bytes.restype = [vp, i64], sz
     lib.rlpl_adamw_plan_build.argtypes = [vp, sz, vp, i64, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp]
     lib.rlpl_adamw_step.argtypes = [vp, vp, vp, i32, f64, vp, f64, f64, f64, i64, vp, vp, ctypes.c_uint32, vp]
+    lib.rms_norm_fwd.argtypes = [vp, vp, vp, i64, i64, i32, i32, i32, f32, vp, vp, vp, vp]
+    lib.rms_norm_fp8.argtypes = [vp, vp, vp, i64, i64, i32, i32, i32, f32, vp, vp, vp, vp, vp]
+    lib.rms_norm_workspace_bytes.argtypes, lib.rms_norm_workspace_bytes.restype = [i64, i64], sz
+    lib.rms_norm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, vp, vp, vp, sz, vp]
+    lib.rlpl_grad_norm_workspace_bytes.argtypes, lib.rlpl_grad_norm_workspace_bytes.restype = [vp, i64], sz
+    lib.rlpl_grad_norm.argtypes = [vp, vp, vp, i64, i32, vp, f32, f32, vp, vp, vp, sz, vp]
+    lib.rlpl_grad_scale.argtypes = [vp, vp, vp, i64, vp, vp]
+    lib.token_logprobs_workspace_bytes.argtypes, lib.token_logprobs_workspace_bytes.restype = [i64, i64, i64], sz
+    lib.token_logprobs_fwd.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i32, f32, i64, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.token_logprobs_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i32, f32, vp, vp]
+    lib.rlpl_fp8_quantize.argtypes = [vp, i64, i64, i64, i32, i32, vp, vp, vp]
+    lib.fp8_linear_workspace_bytes.argtypes, lib.fp8_linear_workspace_bytes.restype = [i64, i64, i64], sz
+    lib.fp8_linear.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, vp, sz, vp]
     for name in ("linear_cross_entropy_fwd", "linear_cross_entropy", "rlpl_linear_cross_entropy", "layer_norm_fwd",
-                 "layer_norm_bwd", "rlpl_adamw_plan_build", "rlpl_adamw_step"):
+                 "layer_norm_bwd", "rlpl_adamw_plan_build", "rlpl_adamw_step", "rms_norm_fwd", "rms_norm_fp8", "rms_norm_bwd",
+                 "rlpl_grad_norm", "rlpl_grad_scale", "token_logprobs_fwd", "token_logprobs_bwd", "rlpl_fp8_quantize",
+                 "fp8_linear"):
         getattr(lib, name).restype = ctypes.c_int
     lib.rlpl_policy_loss.argtypes = [i32, ctypes.c_uint32] + policy
     lib.rlpl_policy_loss.restype = ctypes.c_int
@@ -521,7 +546,9 @@ def selective_logprob_bwd(hidden, weight, bias, targets, lse, grad_logp, *, need
     return dh, dw, db
 
 
-from .training import (AdamWPlan, adamw_plan, adamw_step, layer_norm_bwd, layer_norm_fwd,  # noqa: E402
-                       linear_cross_entropy, linear_cross_entropy_fwd)
+from .training import (AdamWPlan, adamw_plan, adamw_step, clip_grads, grad_norm, layer_norm_bwd, layer_norm_fwd,  # noqa: E402
+                       linear_cross_entropy, linear_cross_entropy_fwd, rms_norm_bwd, rms_norm_fp8, rms_norm_fwd, scale_grads)
+from .scoring import fp8_linear, fp8_quantize, token_logprobs_bwd, token_logprobs_fwd  # noqa: E402
 from .autograd import (bnpo_loss_autograd, grpo_loss_autograd, layer_norm_autograd,  # noqa: E402
-                       linear_cross_entropy_autograd, reverse_kl_autograd, reverse_kl_logits_autograd, selective_logprob_autograd)
+                       linear_cross_entropy_autograd, reverse_kl_autograd, reverse_kl_logits_autograd, rms_norm_autograd,
+                       selective_logprob_autograd, token_logprobs_autograd)

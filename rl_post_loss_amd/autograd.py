@@ -28,11 +28,13 @@ import torch
 from torch.autograd.forward_ad import unpack_dual
 
 from . import _policy, _rkl, _rkl_logits, selective_logprob_bwd, selective_logprob_fwd
-from .training import layer_norm_bwd, layer_norm_fwd, linear_cross_entropy, linear_cross_entropy_fwd
+from .scoring import token_logprobs_bwd, token_logprobs_fwd
+from .training import (layer_norm_bwd, layer_norm_fwd, linear_cross_entropy, linear_cross_entropy_fwd, rms_norm_bwd,
+                       rms_norm_fwd)
 
 __all__ = ["bnpo_loss_autograd", "grpo_loss_autograd", "reverse_kl_autograd",
            "reverse_kl_logits_autograd", "selective_logprob_autograd", "layer_norm_autograd",
-           "linear_cross_entropy_autograd"]
+           "linear_cross_entropy_autograd", "rms_norm_autograd", "token_logprobs_autograd"]
 
 _LIB = "rlpl"
 
@@ -272,6 +274,116 @@ def layer_norm_autograd(x, weight=None, bias=None, *, eps=1e-5):
     weight and bias; the saved statistics are float32)."""
     _no_tangents(x, weight, bias)
     return _norm(x, weight, bias, float(eps))[0]
+
+
+@torch.library.custom_op(f"{_LIB}::rms_norm", mutates_args=())
+def _rms(x: torch.Tensor, weight: Optional[torch.Tensor], residual: Optional[torch.Tensor],
+         eps: float) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    y, rstd, h = rms_norm_fwd(x, weight, residual, eps=eps)
+    return y, rstd, x.new_empty((0,)) if h is None else h
+
+
+@_rms.register_fake
+def _(x, weight, residual, eps):
+    return (x.new_empty(x.shape), x.new_empty(x.shape[:-1], dtype=torch.float32),
+            x.new_empty((0,)) if residual is None else residual.new_empty(residual.shape))
+
+
+@torch.library.custom_op(f"{_LIB}::rms_norm_backward", mutates_args=())
+def _rms_bwd(grad_y: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor], rstd: torch.Tensor,
+             grad_stream: Optional[torch.Tensor], need_h: bool, need_weight: bool) -> Tuple[torch.Tensor, torch.Tensor]:
+    out = rms_norm_bwd(grad_y, h, weight, rstd, grad_stream, need_h=need_h, need_weight=need_weight)
+    return tuple(h.new_empty((0,)) if t is None else t for t in out)
+
+
+@_rms_bwd.register_fake
+def _(grad_y, h, weight, rstd, grad_stream, need_h, need_weight):
+    return (h.new_empty(h.shape) if need_h else h.new_empty((0,)),
+            weight.new_empty(weight.shape) if need_weight and weight is not None else h.new_empty((0,)))
+
+
+def _rms_setup(ctx, inputs, output):
+    x, weight, residual, _ = inputs
+    ctx.set_materialize_grads(False)
+    ctx.dtypes = x.dtype, None if residual is None else residual.dtype
+    ctx.save_for_backward(x if residual is None else output[2], weight, output[1])
+
+
+def _rms_backward(ctx, grad_y, grad_rstd, grad_h):
+    _first_only("rms_norm_autograd", grad_rstd)
+    h, weight, rstd = ctx.saved_tensors
+    x_dtype, r_dtype = ctx.dtypes
+    need_x, need_w, need_r = ctx.needs_input_grad[0], weight is not None and ctx.needs_input_grad[1], ctx.needs_input_grad[2]
+    if r_dtype is None:
+        grad_h = None
+    dh = grad_h
+    dw = None
+    if grad_y is not None and (need_x or need_r or need_w):
+        dh, dw = _rms_bwd(grad_y, h, weight, rstd, grad_h, need_x or need_r, need_w)
+    elif dh is None:
+        return None, None, None, None
+    return dh.to(x_dtype) if need_x else None, dw if need_w else None, dh.to(r_dtype) if need_r else None, None
+
+
+_rms.register_autograd(_rms_backward, setup_context=_rms_setup)
+
+
+def rms_norm_autograd(x, weight=None, residual=None, *, eps=1e-6):
+    """RMS norm over the last dimension as a differentiable tensor of x's shape and dtype, or with a residual (y, h), h =
+    x + residual in the residual's dtype.  Gradients flow to x, weight and residual."""
+    _no_tangents(x, weight, residual)
+    y, _, h = _rms(x, weight, residual, float(eps))
+    return y if residual is None else (y, h)
+
+
+@torch.library.custom_op(f"{_LIB}::token_logprobs", mutates_args=())
+def _token(logits: torch.Tensor, targets: torch.Tensor, mask: Optional[torch.Tensor],
+           temperature: float) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    logp, lse, entropy, _, _ = token_logprobs_fwd(logits, targets, mask, temperature=temperature)
+    return logp, entropy, lse
+
+
+@_token.register_fake
+def _(logits, targets, mask, temperature):
+    out = logits.new_empty(logits.shape[:-1], dtype=torch.float32)
+    return out, torch.empty_like(out), torch.empty_like(out)
+
+
+@torch.library.custom_op(f"{_LIB}::token_logprobs_backward", mutates_args=())
+def _token_bwd(logits: torch.Tensor, targets: torch.Tensor, mask: Optional[torch.Tensor], lse: torch.Tensor,
+               entropy: torch.Tensor, grad_logp: Optional[torch.Tensor], grad_entropy: Optional[torch.Tensor],
+               temperature: float) -> torch.Tensor:
+    return token_logprobs_bwd(logits, targets, mask, lse, entropy, grad_logp, grad_entropy, temperature=temperature)
+
+
+@_token_bwd.register_fake
+def _(logits, targets, mask, lse, entropy, grad_logp, grad_entropy, temperature):
+    return logits.new_empty(logits.shape)
+
+
+def _token_setup(ctx, inputs, output):
+    logits, targets, mask, temperature = inputs
+    ctx.set_materialize_grads(False)
+    ctx.temperature = temperature
+    ctx.save_for_backward(logits, targets, mask, output[2], output[1])
+
+
+def _token_backward(ctx, grad_logp, grad_entropy, grad_lse):
+    _first_only("token_logprobs_autograd", grad_lse)
+    if (grad_logp is None and grad_entropy is None) or not ctx.needs_input_grad[0]:
+        return None, None, None, None
+    logits, targets, mask, lse, entropy = ctx.saved_tensors
+    return _token_bwd(logits, targets, mask, lse, entropy, grad_logp, grad_entropy, ctx.temperature), None, None, None
+
+
+_token.register_autograd(_token_backward, setup_context=_token_setup)
+
+
+def token_logprobs_autograd(logits, targets, mask=None, *, temperature=1.0):
+    """(logp, entropy) of ``token_logprobs_fwd`` as differentiable float32 tensors of the logits' leading shape: gradients
+    of both flow to the logits, in one pass that writes them."""
+    _no_tangents(logits)
+    return _token(logits, targets, mask, float(temperature))[:2]
 
 
 def _ce_held(dtype: torch.dtype) -> torch.dtype:

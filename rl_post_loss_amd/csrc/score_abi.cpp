@@ -1,0 +1,178 @@
+// C ABI of the operators that score tokens (declared in
+// include/rl_post_loss.h): log-probabilities over logit rows, and products of
+// 8-bit operands with the quantisation of those.
+//
+// As in abi.cpp, arguments are validated on the host before any HIP call,
+// nothing is allocated and nothing synchronises; kernels go to the caller's
+// stream.
+#include "train_abi.h"
+
+#include <cmath>
+
+#include "fp8_kernels.h"
+#include "token_kernels.h"
+
+namespace {
+
+using namespace rlpl;
+
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr int64_t kMaxVocab = (int64_t(1) << 31) - 65536;   // columns are counted in 32 bits, a step of lanes past the end
+constexpr int64_t kMaxElements = int64_t(1) << 62;
+
+Devices<is_gfx950> g_devices;
+int device() { return g_devices.current(); }
+
+unsigned capped(int64_t grid, int64_t cap) { return unsigned(grid < cap ? grid : cap); }
+
+// ----------------------------------------------------------------------------- token log-probabilities
+
+bool token_shape_ok(int64_t rows, int64_t vocab, int64_t top_k) {
+    return rows >= 1 && rows < kMaxRows && vocab >= 1 && vocab <= kMaxVocab && top_k >= 0 && top_k <= kTokenMaxTop &&
+           top_k <= vocab;
+}
+// Rows r at group_stride (r / inner) + row_stride (r % inner), all of them within 2^62 elements.
+bool token_strides_ok(int64_t rows, int64_t inner, int64_t group_stride, int64_t row_stride) {
+    if (inner < 1 || inner > rows || group_stride < 0 || row_stride < 0) return false;
+    const __int128 last = __int128((rows - 1) / inner) * group_stride + __int128(inner - 1) * row_stride;
+    return last < kMaxElements;
+}
+int64_t token_vectors(int64_t vocab, int dtype) { return vocab / (16 / int64_t(dtype_bytes(dtype))); }
+
+// The pieces depend on the elements' size through their vectors: workspaces are sized for the most of them.
+size_t token_bytes(int64_t rows, int64_t vocab, int64_t top_k) {
+    const int64_t pieces = token_fwd_pieces(rows, token_vectors(vocab, RLPL_F32), int(top_k));
+    if (pieces == 1) return 256;
+    return up256(size_t(rows) * size_t(pieces) * sizeof(TokenPart)) +
+           up256(size_t(rows) * size_t(pieces) * size_t(top_k) * sizeof(uint64_t));
+}
+
+// ----------------------------------------------------------------------------- 8-bit products
+
+constexpr int64_t kFp8MaxRows = int64_t(1) << 20;
+constexpr int64_t kFp8MaxHidden = 65536;
+constexpr int64_t kFp8MaxVocab = int64_t(1) << 22;
+
+bool fp8_shape_ok(int64_t n, int64_t h, int64_t vocab) {
+    return n >= 1 && n <= kFp8MaxRows && h >= 16 && h <= kFp8MaxHidden && h % 16 == 0 && vocab >= 1 && vocab < kFp8MaxVocab;
+}
+
+size_t fp8_bytes(int64_t, int64_t, int64_t) { return 256; }
+
+}  // namespace
+
+extern "C" {
+
+size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top_k) {
+    return token_shape_ok(rows, vocab, top_k) ? token_bytes(rows, vocab, top_k) : 0;
+}
+
+int token_logprobs_fwd(const void* logits, const int64_t* targets, const void* mask, int64_t rows, int64_t vocab,
+                       int64_t inner, int64_t group_stride, int64_t row_stride, int dtype, float temperature, int64_t top_k,
+                       float* logp_out, float* lse_out, float* entropy_out, float* top_logp_out, int64_t* top_index_out,
+                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!logits || !targets || !logp_out || !lse_out || (top_k > 0 && (!top_logp_out || !top_index_out))) return RLPL_ERR_NULL;
+    if (!token_shape_ok(rows, vocab, top_k) || !token_strides_ok(rows, inner, group_stride, row_stride)) return RLPL_ERR_SHAPE;
+    if (!known_dtype(dtype)) return RLPL_ERR_DTYPE;
+    if (!std::isfinite(temperature) || !(temperature > 0.0f)) return RLPL_ERR_PARAM;
+    if (!is_aligned(logits, dtype_bytes(dtype)) || !is_aligned(targets, 8) || !is_aligned(logp_out, 4) ||
+        !is_aligned(lse_out, 4) || !is_aligned(entropy_out, 4) || !is_aligned(top_logp_out, 4) || !is_aligned(top_index_out, 8))
+        return RLPL_ERR_ALIGN;
+    if (!workspace || workspace_bytes < token_bytes(rows, vocab, top_k)) return RLPL_ERR_WORKSPACE;
+    if (!is_aligned(workspace, 256)) return RLPL_ERR_ALIGN;
+    int st = device();
+    if (st != RLPL_OK) return st;
+    const int64_t vectors = token_vectors(vocab, dtype);
+    TokenFwdArgs a{};
+    a.in = TokenRows{logits, static_cast<const uint8_t*>(mask), rows, inner, group_stride, row_stride, vocab};
+    a.targets = targets;
+    a.logp = logp_out;
+    a.lse = lse_out;
+    a.entropy = entropy_out;
+    a.top_logp = top_logp_out;
+    a.top_index = top_index_out;
+    a.pieces = int32_t(token_fwd_pieces(rows, vectors, int(top_k)));
+    a.piece_vectors = div_up(vectors > 0 ? vectors : 1, a.pieces);
+    a.top_k = int32_t(top_k);
+    a.scale = float(1.4426950408889634 / double(temperature));
+    a.part = static_cast<TokenPart*>(workspace);
+    a.part_top = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) +
+                                             up256(size_t(rows) * size_t(a.pieces) * sizeof(TokenPart)));
+    st = enqueue(pick_token_fwd(dtype, top_k > 0), a, dim3(capped(rows * a.pieces, kTokenMaxGrid)), kTokenThreads, stream);
+    if (st != RLPL_OK || a.pieces == 1) return st;
+    return enqueue(pick_token_join(dtype), a, dim3(capped(rows, kTokenMaxGrid)), kTokenThreads, stream);
+}
+
+int token_logprobs_bwd(const void* logits, const int64_t* targets, const void* mask, const float* lse, const float* entropy,
+                       const float* grad_logp, const float* grad_entropy, int64_t rows, int64_t vocab, int64_t inner,
+                       int64_t group_stride, int64_t row_stride, int dtype, float temperature, void* grad_logits,
+                       hipStream_t stream) {
+    if (!logits || !targets || !lse || !grad_logits || (grad_entropy && !entropy)) return RLPL_ERR_NULL;
+    if (!token_shape_ok(rows, vocab, 0) || !token_strides_ok(rows, inner, group_stride, row_stride)) return RLPL_ERR_SHAPE;
+    if (!known_dtype(dtype)) return RLPL_ERR_DTYPE;
+    if (!std::isfinite(temperature) || !(temperature > 0.0f)) return RLPL_ERR_PARAM;
+    const size_t e = dtype_bytes(dtype);
+    if (!is_aligned(logits, e) || !is_aligned(targets, 8) || !is_aligned(lse, 4) || !is_aligned(entropy, 4) ||
+        !is_aligned(grad_logp, 4) || !is_aligned(grad_entropy, 4) || !is_aligned(grad_logits, e))
+        return RLPL_ERR_ALIGN;
+    const int st = device();
+    if (st != RLPL_OK) return st;
+    const int64_t vectors = token_vectors(vocab, dtype);
+    TokenBwdArgs a{};
+    a.in = TokenRows{logits, static_cast<const uint8_t*>(mask), rows, inner, group_stride, row_stride, vocab};
+    a.targets = targets;
+    a.lse = lse;
+    a.entropy = entropy;
+    a.grad_logp = grad_logp;
+    a.grad_entropy = grad_entropy;
+    a.grad = grad_logits;
+    // pieces of 8 vectors a lane
+    a.pieces = int32_t(div_up(vectors > 0 ? vectors : 1, 8 * kTokenThreads));
+    a.piece_vectors = div_up(vectors > 0 ? vectors : 1, a.pieces);
+    a.inv_t = float(1.0 / double(temperature));
+    return enqueue(pick_token_bwd(dtype), a, dim3(capped(rows * a.pieces, kTokenMaxGrid)), kTokenThreads, stream);
+}
+
+int rlpl_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t row_stride, int dtype, int block_rows, void* q,
+                      float* scale, hipStream_t stream) {
+    if (!x || !q || !scale) return RLPL_ERR_NULL;
+    if (rows < 1 || rows >= kMaxRows || cols < 1 || cols > kMaxVocab || row_stride < 0 ||
+        __int128(rows - 1) * row_stride >= kMaxElements)
+        return RLPL_ERR_SHAPE;
+    if (!known_dtype(dtype)) return RLPL_ERR_DTYPE;
+    if (block_rows != 1 && block_rows != kFp8Group) return RLPL_ERR_PARAM;
+    if (!is_aligned(x, dtype_bytes(dtype)) || !is_aligned(scale, 4)) return RLPL_ERR_ALIGN;
+    const int st = device();
+    if (st != RLPL_OK) return st;
+    const int64_t groups = div_up(cols, kFp8Group);
+    const QuantiseArgs a{x, static_cast<uint8_t*>(q), scale, rows, row_stride, int32_t(cols), int32_t(groups)};
+    const int64_t work = block_rows == 1 ? div_up(rows * groups, 16) : div_up(rows, kFp8Group) * groups;
+    return enqueue(pick_quantise(dtype, block_rows != 1), a, dim3(capped(work, kFp8MaxGrid)), kFp8Threads, stream);
+}
+
+size_t fp8_linear_workspace_bytes(int64_t n, int64_t hidden_size, int64_t vocab) {
+    return fp8_shape_ok(n, hidden_size, vocab) ? fp8_bytes(n, hidden_size, vocab) : 0;
+}
+
+int fp8_linear(const void* x, const float* x_scale, const void* weight, const float* weight_scale, const void* bias, int64_t n,
+               int64_t hidden_size, int64_t vocab, int out_dtype, void* out, void* workspace, size_t workspace_bytes,
+               hipStream_t stream) {
+    if (!x || !x_scale || !weight || !weight_scale || !out) return RLPL_ERR_NULL;
+    if (!fp8_shape_ok(n, hidden_size, vocab)) return RLPL_ERR_SHAPE;
+    if (!known_dtype(out_dtype)) return RLPL_ERR_DTYPE;
+    const size_t e = dtype_bytes(out_dtype);
+    if (!is_aligned(x, 16) || !is_aligned(weight, 16) || !is_aligned(x_scale, 4) || !is_aligned(weight_scale, 4) ||
+        !is_aligned(bias, e) || !is_aligned(out, e))
+        return RLPL_ERR_ALIGN;
+    if (!workspace || workspace_bytes < fp8_bytes(n, hidden_size, vocab)) return RLPL_ERR_WORKSPACE;
+    if (!is_aligned(workspace, 256)) return RLPL_ERR_ALIGN;
+    const int st = device();
+    if (st != RLPL_OK) return st;
+    const Fp8LinearArgs a{static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(weight), weight_scale, bias, out,
+                          int32_t(n), int32_t(hidden_size), int32_t(vocab), int32_t(div_up(hidden_size, kFp8Group))};
+    const int tokens = n <= 16 ? 16 : n <= 32 ? 32 : 64;
+    return enqueue(pick_fp8_small(out_dtype, tokens), a,
+                   dim3(unsigned(div_up(vocab, kFp8SmallVocab)), unsigned(div_up(n, tokens))), kFp8Threads, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,73 @@
+// Internal interface between the C ABI layer (score_abi.cpp) and the kernels
+// of the token log-probabilities over logit rows (token_kernels.hip).  Not
+// part of the public ABI.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+namespace rlpl {
+
+constexpr int kTokenThreads = 256;
+constexpr int kTokenMaxTop = 64;           // alternatives a row can give: no more than a wavefront's lanes
+constexpr int kTokenMaxPieces = 64;        // pieces of a row
+constexpr int kTokenMaxKeys = 2048;        // pieces times alternatives
+constexpr int64_t kTokenMaxGrid = 1 << 20; // workgroups of a launch (they stride over the rest)
+
+// Where the rows lie: row r at group_stride (r / inner) + row_stride (r % inner) elements.
+struct TokenRows {
+    const void* logits;
+    const uint8_t* mask;       // (rows) bytes, zero: the row is not read; or NULL
+    int64_t rows, inner, group_stride, row_stride;
+    int64_t vocab;             // < 2^31
+};
+
+// What a piece of a row leaves: its largest logit, and the sums over its elements that count from it.
+struct TokenPart {
+    float top, sum, weighted, pad;
+};
+
+struct TokenFwdArgs {
+    TokenRows in;
+    const int64_t* targets;    // (rows)
+    float* logp;               // (rows)
+    float* lse;                // (rows)
+    float* entropy;            // (rows) or NULL
+    float* top_logp;           // (rows, top_k)
+    int64_t* top_index;        // (rows, top_k)
+    TokenPart* part;           // (rows, pieces), pieces > 1
+    uint64_t* part_top;        // (rows, pieces, top_k) keys, the largest first
+    int64_t piece_vectors;     // 16-byte vectors of a piece
+    int32_t pieces, top_k;
+    float scale;               // log2(e) / temperature
+};
+
+struct TokenBwdArgs {
+    TokenRows in;
+    const int64_t* targets;
+    const float* lse;
+    const float* entropy;      // (rows), read with grad_entropy only
+    const float* grad_logp;    // (rows) or NULL
+    const float* grad_entropy; // (rows) or NULL
+    void* grad;                // (rows, vocab), dense
+    int64_t piece_vectors;
+    int32_t pieces;
+    float inv_t;               // 1 / temperature
+};
+
+// Pieces a row is cut into by the forward, so that few rows still fill the chip: 1024 workgroups in all, each with a
+// vector for every lane at least.
+inline int64_t token_fwd_pieces(int64_t rows, int64_t vectors, int top_k) {
+    const int64_t most = (vectors + kTokenThreads - 1) / kTokenThreads;
+    int64_t p = 1024 / rows;
+    if (p > most) p = most;
+    if (p > kTokenMaxPieces) p = kTokenMaxPieces;
+    if (p * top_k > kTokenMaxKeys) p = kTokenMaxKeys / top_k;
+    return p < 1 ? 1 : p;
+}
+
+const void* pick_token_fwd(int dtype, bool top);
+const void* pick_token_join(int dtype);
+const void* pick_token_bwd(int dtype);
+
+}  // namespace rlpl

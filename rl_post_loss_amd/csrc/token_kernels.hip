@@ -1,0 +1,455 @@
+// Log-probabilities of given tokens over rows of logits on gfx950, with each
+// row's entropy and its most likely tokens, and the backward pass.
+//
+// For a row z at temperature T, with c = log2(e) / T and the running maximum b,
+//
+//   s = sum 2^(c z - c b),   t = sum (c z - c b) 2^(c z - c b)
+//   lse = ln 2 (c b + log2 s),   logp = ln 2 (c z_y - c b - log2 s),   H = ln 2 (log2 s - t / s)
+//
+// in one pass: a lane keeps (b, s, t) over its vectors of 16 bytes and counts
+// anew from a larger maximum once per 32 elements (s 2^d and (t + d s) 2^d for
+// a maximum further by -d), and lanes, wavefronts and pieces of a row are joined in a
+// fixed order by the same rule.  A logit of -inf adds nothing (its exponent is
+// held at -1000, which 2^x takes to zero, by a maximum that lets NaN through).
+//
+// The k largest elements, the lowest index first among equal ones, come from
+// the same pass without a list in its loop: each lane knows the block of
+// its own largest element.  The k-th of the lanes' largest is a bound that k
+// elements reach, so the row's k largest all do, and they lie in the k lanes
+// whose largest reach it: those lanes' elements (k / 256 of the row) are read
+// a second time, the ones that reach the bound collected and ranked.  The work
+// does not depend on the order of the logits.
+//
+// The loop takes about ten vector operations an element (2^x counts four).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+#include "loss_kernels.h"
+#include "row_io.h"
+#include "token_kernels.h"
+
+namespace rlpl {
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -1000.0f;          // an exponent that 2^x takes to zero
+constexpr int kTokenWaves = kTokenThreads / 64;
+
+__device__ __forceinline__ float hold(float d) { return __builtin_elementwise_maximum(d, kNone); }
+__device__ __forceinline__ float exp2_hw(float d) { return __builtin_amdgcn_exp2f(d); }
+// What a sum counts from: its largest element, or 0 where that is -inf.
+__device__ __forceinline__ float base_of(float top) { return top == -__builtin_inff() ? 0.0f : top; }
+
+// The largest of a wavefront's values in every lane (NaN passed over), by DPP lane moves; lanes without a source keep theirs.
+__device__ __forceinline__ float wave_top(float v) {
+    const auto more = [&v](auto move) { v = fmaxf(v, __int_as_float(move(__float_as_int(v)))); };
+    more([](int x) { return __builtin_amdgcn_update_dpp(x, x, 0xB1, 0xF, 0xF, false); });
+    more([](int x) { return __builtin_amdgcn_update_dpp(x, x, 0x4E, 0xF, 0xF, false); });
+    more([](int x) { return __builtin_amdgcn_update_dpp(x, x, 0x141, 0xF, 0xF, false); });
+    more([](int x) { return __builtin_amdgcn_update_dpp(x, x, 0x140, 0xF, 0xF, false); });
+    more([](int x) { return __builtin_amdgcn_update_dpp(x, x, 0x142, 0xA, 0xF, false); });
+    more([](int x) { return __builtin_amdgcn_update_dpp(x, x, 0x143, 0xC, 0xF, false); });
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sums that count from `top`.
+struct Sums {
+    float top, s, t;
+    static __device__ __forceinline__ Sums none() { return Sums{-__builtin_inff(), 0.0f, 0.0f}; }
+    // Counts from a larger maximum.
+    __device__ __forceinline__ void rise(float to, float c) {
+        const float d = hold(c * (base_of(top) - base_of(to)));
+        const float f = top == -__builtin_inff() ? 0.0f : exp2_hw(d);
+        t = fmaf(d, s, t) * f;
+        s *= f;
+        top = to;
+    }
+    __device__ __forceinline__ void add(float d) {
+        d = hold(d);
+        const float e = exp2_hw(d);
+        s += e;
+        t = fmaf(e, d, t);
+    }
+};
+
+// A logit's place among others: larger keys are larger logits, of equal ones the one of the lower index.  Never 0.
+__device__ __forceinline__ uint64_t key_of(float z, uint32_t index) {
+    const uint32_t bits = __float_as_uint(z + 0.0f);           // -0 and 0 are equal
+    return uint64_t(bits ^ (int32_t(bits) < 0 ? 0xFFFFFFFFu : 0x80000000u)) << 32 | uint32_t(~index);
+}
+__device__ __forceinline__ float key_logit(uint64_t key) {
+    const uint32_t o = uint32_t(key >> 32);
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~uint32_t(key); }
+
+// A row: elements [0, head) and [head + V vectors, n) one by one, those between in 16-byte vectors of V.
+template <typename T>
+struct Row {
+    static constexpr int V = kVec16<T>;
+    const T* p;
+    int32_t n, head, vectors;
+    __device__ __forceinline__ Row(const TokenRows& in, int64_t row) {
+        p = static_cast<const T*>(in.logits) + (row / in.inner) * in.group_stride + (row % in.inner) * in.row_stride;
+        n = int32_t(in.vocab);
+        head = int32_t((-reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+        if (head > n) head = n;
+        vectors = (n - head) / V;
+    }
+    __device__ __forceinline__ u32x4 vector(int32_t i) const {
+        return load_word<u32x4, true>(p + head + int64_t(i) * V);
+    }
+    __device__ __forceinline__ int32_t edges() const { return n - vectors * V; }
+    // The place of edge element e.
+    __device__ __forceinline__ int32_t edge(int32_t e) const { return e < head ? e : e + vectors * V; }
+};
+
+// The row's results from its joined sums.
+struct Finish {
+    float bc, l2;              // c b, log2 s
+    __device__ __forceinline__ Finish(const Sums& a, float c) : bc(c * base_of(a.top)), l2(__log2f(a.s)) {}
+    __device__ __forceinline__ float logp(float z, float c) const { return kLn2 * (fmaf(z, c, -bc) - l2); }
+};
+
+template <typename T>
+__device__ __forceinline__ void write_row(const TokenFwdArgs& a, const Row<T>& r, int64_t row, const Sums& j, const Finish& f) {
+    const int64_t y = a.targets[row];
+    a.logp[row] = y >= 0 && y < r.n ? f.logp(widen(r.p[y]), a.scale) : __builtin_nanf("");
+    a.lse[row] = kLn2 * (f.bc + f.l2);
+    if (a.entropy) a.entropy[row] = kLn2 * (f.l2 - j.t / j.s);
+}
+__device__ __forceinline__ void write_masked(const TokenFwdArgs& a, int64_t row) {
+    if (threadIdx.x == 0) {
+        a.logp[row] = 0.0f;
+        a.lse[row] = 0.0f;
+        if (a.entropy) a.entropy[row] = 0.0f;
+    }
+    for (int i = threadIdx.x; i < a.top_k; i += kTokenThreads) {
+        a.top_logp[row * a.top_k + i] = 0.0f;
+        a.top_index[row * a.top_k + i] = -1;
+    }
+}
+__device__ __forceinline__ void write_top(const TokenFwdArgs& a, int64_t row, int rank, uint64_t key, const Finish& f) {
+    const bool bad = !(f.l2 < __builtin_inff());               // a NaN or +inf among the logits
+    a.top_logp[row * a.top_k + rank] = bad ? __builtin_nanf("") : f.logp(key_logit(key), a.scale);
+    a.top_index[row * a.top_k + rank] = bad ? -1 : int64_t(key_index(key));
+}
+
+// How many of n keys in LDS are larger than `mine`.
+__device__ __forceinline__ int rank_of(uint64_t mine, const uint64_t* keys, int n) {
+    int rank = 0;
+    for (int i = 0; i < n; ++i) rank += keys[i] > mine ? 1 : 0;
+    return rank;
+}
+
+constexpr int kTokenKeep = 192;            // candidates past which a step's are cut to the k largest
+template <typename T> constexpr int kTokenStep = kTokenThreads * kVec16<T>;   // a step adds so many at most
+
+// One workgroup a row, or a piece of it.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a) {
+    constexpr int V = kVec16<T>, U = 32 / V;                   // 32 elements a lane at a time
+    __shared__ Sums joined[kTokenWaves];
+    __shared__ uint64_t found[TOP ? kTokenKeep + kTokenStep<T> : 1];
+    __shared__ uint64_t kept[TOP ? kTokenMaxTop : 1];
+    __shared__ int lanes[TOP ? kTokenMaxTop : 1];
+    __shared__ int count;
+    const int tid = threadIdx.x;
+    const float c = a.scale;
+    for (int64_t item = blockIdx.x; item < a.in.rows * a.pieces; item += gridDim.x) {
+        const int64_t row = a.pieces == 1 ? item : item / a.pieces;
+        const int piece = a.pieces == 1 ? 0 : int(item % a.pieces);
+        if (a.in.mask && !a.in.mask[row]) {
+            if (piece == 0) write_masked(a, row);
+            continue;
+        }
+        const Row<T> r(a.in, row);
+        const int32_t first = int32_t(piece * a.piece_vectors) < r.vectors ? int32_t(piece * a.piece_vectors) : r.vectors;
+        const int32_t last = piece == a.pieces - 1 || r.vectors - first < a.piece_vectors ? r.vectors : first + int32_t(a.piece_vectors);
+        Sums mine = Sums::none();
+        int32_t at = first + tid;          // the first vector of the block with the lane's largest element
+        const auto block = [&](const u32x4 (&raw)[U], int live, int32_t i) {
+            float z[U][V];
+            float top = -__builtin_inff();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                widen_raw<T>(raw[u], z[u]);
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    if (u >= live) z[u][k] = -__builtin_inff();
+                    top = fmaxf(top, z[u][k]);
+                }
+            }
+            if (top > mine.top) {
+                mine.rise(top, c);
+                at = i;
+            }
+            const float bc = c * base_of(mine.top);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < V; ++k) mine.add(fmaf(z[u][k], c, -bc));
+        };
+        int32_t i = first + tid;
+        for (; i + (U - 1) * kTokenThreads < last; i += U * kTokenThreads) {
+            u32x4 raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) raw[u] = r.vector(i + u * kTokenThreads);
+            block(raw, U, i);
+        }
+        if (i < last) {
+            u32x4 raw[U];
+            int live = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                raw[u] = u32x4{0, 0, 0, 0};
+                if (i + u * kTokenThreads < last) {
+                    raw[u] = r.vector(i + u * kTokenThreads);
+                    live = u + 1;
+                }
+            }
+            block(raw, live, i);
+        }
+        Sums all = mine;
+        if (piece == 0 && tid < r.edges()) {                   // at most 2 (V - 1) elements outside the vectors
+            const float z = widen(r.p[r.edge(tid)]);
+            if (z > all.top) all.rise(z, c);
+            all.add(fmaf(z, c, -c * base_of(all.top)));
+        }
+        // lanes to wavefronts to the workgroup
+        const float top = wave_top(all.top);
+        all.rise(top, c);
+        all.s = wave_sum(all.s);
+        all.t = wave_sum(all.t);
+        __syncthreads();                   // the last row's LDS may still be read
+        if ((tid & 63) == 0) joined[tid >> 6] = all;
+        if (tid == 0) count = 0;
+        uint64_t best = 0;
+        if constexpr (TOP) {
+            if (tid < kTokenMaxTop) {      // places that no lane of a row of NaN fills
+                lanes[tid] = tid;
+                kept[tid] = 1;
+            }
+            if (first + tid < last) {
+                // the lane's largest element's first place
+#pragma unroll
+                for (int u = U - 1; u >= 0; --u) {
+                    if (at + u * kTokenThreads >= last) continue;
+                    float z[V];
+                    widen_raw<T>(r.vector(at + u * kTokenThreads), z);
+#pragma unroll
+                    for (int k = V - 1; k >= 0; --k)
+                        if (z[k] == mine.top) best = key_of(z[k], r.head + (at + u * kTokenThreads) * V + k);
+                }
+            }
+            found[tid] = best;
+        }
+        __syncthreads();
+        all = joined[0];
+#pragma unroll
+        for (int w = 1; w < kTokenWaves; ++w) {
+            Sums o = joined[w];
+            const float higher = fmaxf(all.top, o.top);
+            all.rise(higher, c);
+            o.rise(higher, c);
+            all.s += o.s;
+            all.t += o.t;
+        }
+        const Finish f(all, c);
+        if (tid == 0) {
+            if (a.pieces == 1) write_row(a, r, row, all, f);
+            else a.part[item] = TokenPart{all.top, all.s, all.t, 0.0f};
+        }
+        if constexpr (TOP) {
+            const int rank = rank_of(best, found, kTokenThreads);
+            if (rank < a.top_k && best) {
+                lanes[rank] = tid;
+                kept[rank] = best;
+            }
+            const int some = last - first < a.top_k ? int(last - first) : a.top_k;     // lanes that have elements
+            __syncthreads();
+            // k lanes' largest reach this bound; with fewer lanes every element is taken
+            uint64_t bound = some == a.top_k ? kept[a.top_k - 1] : 1;
+            const int32_t each = (last - first + kTokenThreads - 1) / kTokenThreads;
+            const int32_t all_vectors = some * each;
+            int n = 0;
+            const auto take = [&](float z, uint32_t index) {
+                const uint64_t key = key_of(z, index);
+                if (key >= bound) found[atomicAdd(&count, 1)] = key;
+            };
+            if (piece == 0 && tid < r.edges()) take(widen(r.p[r.edge(tid)]), uint32_t(r.edge(tid)));
+            for (int32_t v0 = 0; v0 < all_vectors; v0 += kTokenThreads) {
+                const int32_t v = v0 + tid;
+                const int32_t i = v < all_vectors ? first + lanes[v / each] + v % each * kTokenThreads : last;
+                if (i < last) {
+                    float z[V];
+                    widen_raw<T>(r.vector(i), z);
+#pragma unroll
+                    for (int k = 0; k < V; ++k) take(z[k], uint32_t(r.head + i * V + k));
+                }
+                __syncthreads();
+                n = count;
+                __syncthreads();           // every lane has read it
+                if (n > kTokenKeep) {                          // uniform: cut to the k largest
+                    for (int j = tid; j < n; j += kTokenThreads) {
+                        const uint64_t key = found[j];
+                        const int rank = rank_of(key, found, n);
+                        if (rank < a.top_k) kept[rank] = key;
+                    }
+                    __syncthreads();
+                    if (tid < a.top_k) found[tid] = kept[tid];
+                    if (tid == 0) count = a.top_k;
+                    bound = kept[a.top_k - 1];
+                    __syncthreads();
+                }
+            }
+            __syncthreads();
+            n = count;
+            for (int j = tid; j < n || j < a.top_k; j += kTokenThreads) {
+                // a piece of fewer than k elements gives keys of 0 past them
+                const uint64_t key = j < n ? found[j] : 0;
+                const int rank = j < n ? rank_of(key, found, n) : j;
+                if (rank >= a.top_k) continue;
+                if (a.pieces == 1) write_top(a, row, rank, key, f);
+                else a.part_top[item * a.top_k + rank] = key;
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// A row's pieces joined: the sums in piece order, and the k largest of the pieces' k largest by the rule of the lanes.
+template <typename T>
+__global__ void __launch_bounds__(kTokenThreads) token_join(const TokenFwdArgs a) {
+    __shared__ Sums sums[kTokenMaxPieces];
+    __shared__ uint64_t keys[kTokenMaxKeys], found[kTokenMaxKeys];
+    __shared__ uint64_t bound;
+    __shared__ int count;
+    const int tid = threadIdx.x;
+    const float c = a.scale;
+    for (int64_t row = blockIdx.x; row < a.in.rows; row += gridDim.x) {
+        if (a.in.mask && !a.in.mask[row]) continue;            // written by its first piece
+        __syncthreads();
+        if (tid < a.pieces) {
+            const TokenPart p = a.part[row * a.pieces + tid];
+            sums[tid] = Sums{p.top, p.sum, p.weighted};
+        }
+        if (tid == 0) {
+            count = 0;
+            bound = 1;
+        }
+        for (int i = tid; i < a.pieces * a.top_k; i += kTokenThreads) keys[i] = a.part_top[row * a.pieces * a.top_k + i];
+        __syncthreads();
+        float top = sums[0].top;
+        for (int p = 1; p < a.pieces; ++p) top = fmaxf(top, sums[p].top);
+        Sums all = sums[0];
+        all.rise(top, c);
+        for (int p = 1; p < a.pieces; ++p) {
+            Sums o = sums[p];
+            o.rise(all.top, c);
+            all.s += o.s;
+            all.t += o.t;
+        }
+        const Finish f(all, c);
+        if (tid == 0) write_row(a, Row<T>(a.in, row), row, all, f);
+        if (a.top_k == 0) continue;
+        // the k-th of the pieces' largest
+        if (tid < a.pieces) {
+            const uint64_t mine = keys[tid * a.top_k];
+            int rank = 0;
+            for (int p = 0; p < a.pieces; ++p) rank += keys[p * a.top_k] > mine ? 1 : 0;
+            if (rank == a.top_k - 1 && mine) bound = mine;
+        }
+        __syncthreads();
+        for (int i = tid; i < a.pieces * a.top_k; i += kTokenThreads)
+            if (keys[i] >= bound) found[atomicAdd(&count, 1)] = keys[i];
+        __syncthreads();
+        for (int j = tid; j < count; j += kTokenThreads) {
+            const int rank = rank_of(found[j], found, count);
+            if (rank < a.top_k) write_top(a, row, rank, found[j], f);
+        }
+    }
+}
+
+// The gradient of sum(grad_logp logp + grad_entropy H): with p = exp(z / T - lse),
+//   dz_v = (grad_logp ((v == y) - p_v) - grad_entropy p_v (log p_v + H)) / T.
+// Vectors are cut where the gradient's row is aligned.
+template <typename T>
+__global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a) {
+    constexpr int V = kVec16<T>;
+    const int tid = threadIdx.x;
+    for (int64_t item = blockIdx.x; item < a.in.rows * a.pieces; item += gridDim.x) {
+        const int64_t row = a.pieces == 1 ? item : item / a.pieces;
+        const int piece = a.pieces == 1 ? 0 : int(item % a.pieces);
+        const int32_t n = int32_t(a.in.vocab);
+        const T* x = static_cast<const T*>(a.in.logits) + (row / a.in.inner) * a.in.group_stride + (row % a.in.inner) * a.in.row_stride;
+        T* out = static_cast<T*>(a.grad) + row * a.in.vocab;
+        int32_t head = int32_t((-reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T));
+        if (head > n) head = n;
+        const int32_t vectors = (n - head) / V, edges = n - vectors * V;
+        const int32_t first = int32_t(piece * a.piece_vectors) < vectors ? int32_t(piece * a.piece_vectors) : vectors;
+        const int32_t last = piece == a.pieces - 1 || vectors - first < a.piece_vectors ? vectors : first + int32_t(a.piece_vectors);
+        const int32_t edge = tid < head ? tid : tid + vectors * V;
+        if (a.in.mask && !a.in.mask[row]) {
+            if (piece == 0 && tid < edges) out[edge] = T(0.0f);
+            for (int32_t i = first + tid; i < last; i += kTokenThreads)
+                store_word<true>(out + head + int64_t(i) * V, u32x4{0, 0, 0, 0});
+            continue;
+        }
+        const float lse = a.lse[row], g = a.grad_logp ? a.grad_logp[row] : 0.0f;
+        const float h = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
+        const float k0 = a.grad_entropy ? fmaf(h, a.entropy[row], g) : g;      // g + h H
+        const int64_t target = a.targets[row];
+        const int32_t y = target >= 0 && target < n ? int32_t(target) : -1;
+        const auto value = [&](float z, int32_t v) {
+            const float l = hold(fmaf(z, a.inv_t, -lse));
+            const float p = exp2_hw(l * kLog2e);
+            return a.inv_t * ((v == y ? g : 0.0f) - p * fmaf(h, l, k0));
+        };
+        if (piece == 0 && tid < edges) out[edge] = T(value(widen(x[edge]), edge));
+#pragma unroll 4
+        for (int32_t i = first + tid; i < last; i += kTokenThreads) {
+            const int32_t v = head + i * V;
+            float z[V];
+            widen_raw<T>(load_word<typename Unaligned16<T>::type, true>(x + v), z);
+#pragma unroll
+            for (int k = 0; k < V; ++k) z[k] = value(z[k], v + k);
+            store_word<true>(out + v, narrow_raw<T>(z));
+        }
+    }
+}
+
+template <bool TOP>
+const void* fwd_of(int dtype) {
+    switch (dtype) {
+    case kF32: return reinterpret_cast<const void*>(&token_fwd<float, TOP>);
+    case kF16: return reinterpret_cast<const void*>(&token_fwd<_Float16, TOP>);
+    case kBF16: return reinterpret_cast<const void*>(&token_fwd<__bf16, TOP>);
+    }
+    return nullptr;
+}
+
+}  // namespace
+
+const void* pick_token_fwd(int dtype, bool top) { return top ? fwd_of<true>(dtype) : fwd_of<false>(dtype); }
+const void* pick_token_join(int dtype) {
+    switch (dtype) {
+    case kF32: return reinterpret_cast<const void*>(&token_join<float>);
+    case kF16: return reinterpret_cast<const void*>(&token_join<_Float16>);
+    case kBF16: return reinterpret_cast<const void*>(&token_join<__bf16>);
+    }
+    return nullptr;
+}
+const void* pick_token_bwd(int dtype) {
+    switch (dtype) {
+    case kF32: return reinterpret_cast<const void*>(&token_bwd<float>);
+    case kF16: return reinterpret_cast<const void*>(&token_bwd<_Float16>);
+    case kBF16: return reinterpret_cast<const void*>(&token_bwd<__bf16>);
+    }
+    return nullptr;
+}
+
+}  // namespace rlpl

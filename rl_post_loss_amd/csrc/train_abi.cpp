@@ -1,40 +1,34 @@
 // C ABI of the operators around the losses (declared in
 // include/rl_post_loss.h): the vocabulary cross
-// entropy, layer norm and the AdamW step.
+// entropy, layer norm, RMS norm, the AdamW step and the gradients' norm.
 //
 // As in abi.cpp, arguments are validated on the host before any HIP call,
 // nothing is allocated and nothing synchronises; kernels go to the caller's
 // stream.
 #include "train_abi.h"
 
-#include <atomic>
+#include <algorithm>
 #include <cmath>
 #include <cstring>
-#include <mutex>
+#include <memory>
+#include <new>
+#include <numeric>
 
 #include "adamw_kernels.h"
 #include "ce_kernels.h"
+#include "grad_kernels.h"
 #include "norm_kernels.h"
+#include "rms_kernels.h"
 
 namespace {
 
 using namespace rlpl;
 
-constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxRows = int64_t(1) << 31;
 
-struct Device {
-    std::mutex lock;
-    std::atomic<bool> ready{false};
-};
-Device g_devices[kMaxDevices];
-
-// Whether device dev is a gfx950 with a known number of compute units, set up for the kernels.
+// Whether device dev is set up for the kernels.
 bool set_up(int dev) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess || std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return false;
-    int cus = 0;
-    if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 1) return false;
+    if (!is_gfx950(dev)) return false;
     // the contractions take their LDS ring beyond the default limit
     for (int dt : {RLPL_F16, RLPL_BF16})
         for (bool small : {false, true})
@@ -49,24 +43,8 @@ bool set_up(int dev) {
     return true;
 }
 
-// The current device, set up once.  A failure is not kept: the next call tries again.
-int device() {
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
-        (void)hipGetLastError();
-        return RLPL_ERR_DEVICE;
-    }
-    Device& d = g_devices[dev];
-    if (d.ready.load(std::memory_order_acquire)) return RLPL_OK;
-    const std::lock_guard<std::mutex> hold(d.lock);
-    if (d.ready.load(std::memory_order_relaxed)) return RLPL_OK;
-    if (!set_up(dev)) {
-        (void)hipGetLastError();
-        return RLPL_ERR_DEVICE;
-    }
-    d.ready.store(true, std::memory_order_release);
-    return RLPL_OK;
-}
+Devices<set_up> g_devices;
+int device() { return g_devices.current(); }
 
 // ----------------------------------------------------------------------------- vocabulary cross entropy
 
@@ -391,6 +369,135 @@ NormLayout norm_layout(int64_t rows, int64_t cols) {
     return L;
 }
 
+// ----------------------------------------------------------------------------- RMS norm
+
+bool rms_shape_ok(int64_t rows, int64_t cols) {
+    return rows >= 1 && rows < kMaxRows && cols >= 1 && cols <= kRmsMaxCols;
+}
+
+// Room for one plane of column sums of each workgroup (and of a second one, as the joining kernel counts them).
+size_t rms_bytes(int64_t rows, int64_t cols) {
+    return up256(size_t(norm_held_grid(rows, cols, 1)) * 2 * size_t(cols) * sizeof(float));
+}
+
+struct RmsCall {
+    const void *x, *weight, *residual;
+    int64_t rows, cols;
+    int dtype, weight_dtype, stream_dtype;
+    float eps;
+    void* y;
+    float* scale;
+    float* rstd;
+    void* stream_out;
+};
+
+int rms_forward(const RmsCall& c, bool fp8, hipStream_t stream) {
+    if (!c.x || !c.y || (fp8 && !c.scale) || (c.residual && !c.stream_out)) return RLPL_ERR_NULL;
+    if (!rms_shape_ok(c.rows, c.cols)) return RLPL_ERR_SHAPE;
+    if (!norm_types_ok(c.dtype, c.weight_dtype) || !norm_types_ok(c.dtype, c.stream_dtype)) return RLPL_ERR_DTYPE;
+    if (!std::isfinite(c.eps) || c.eps < 0.0f) return RLPL_ERR_PARAM;
+    const size_t e = dtype_bytes(c.dtype), re = dtype_bytes(c.stream_dtype);
+    if (!is_aligned(c.x, e) || !is_aligned(c.y, fp8 ? 1 : e) || !is_aligned(c.weight, dtype_bytes(c.weight_dtype)) ||
+        !is_aligned(c.residual, re) || !is_aligned(c.stream_out, re) || !is_aligned(c.rstd, 4) || !is_aligned(c.scale, 4))
+        return RLPL_ERR_ALIGN;
+    const int st = device();
+    if (st != RLPL_OK) return st;
+    const NormRowKernel k = pick_rms_fwd(c.dtype, c.residual ? c.stream_dtype : c.dtype, fp8, c.cols);
+    if (!k.kernel) return RLPL_ERR_DTYPE;
+    const RmsFwdArgs a{c.x, c.residual, c.weight, c.residual ? c.stream_out : nullptr, c.y, c.scale, c.rstd, c.rows,
+                       int32_t(c.cols), int32_t(div_up(c.cols, kFp8Group)), c.weight_dtype == RLPL_F32 ? 1 : 0, c.eps};
+    return enqueue(k.kernel, a, dim3(row_grid(c.rows, k.rows_per_group)), k.threads, stream);
+}
+
+// ----------------------------------------------------------------------------- gradients' norm
+
+constexpr int64_t kGradMaxTensors = int64_t(1) << 24;
+constexpr int64_t kGradMaxElements = int64_t(1) << 40;
+constexpr int64_t kGradMaxChunks = int64_t(1) << 31;        // of a launch
+
+int grad_check(void* const* grads, const int64_t* sizes, const int32_t* dtypes, int64_t count) {
+    if (!grads || !sizes || !dtypes) return RLPL_ERR_NULL;
+    if (count < 1 || count > kGradMaxTensors) return RLPL_ERR_SHAPE;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] < 0 || sizes[i] > kGradMaxElements) return RLPL_ERR_SHAPE;
+        if (!known_dtype(dtypes[i])) return RLPL_ERR_DTYPE;
+        if (sizes[i] == 0) continue;
+        if (!grads[i]) return RLPL_ERR_NULL;
+        if (!is_aligned(grads[i], dtype_bytes(dtypes[i]))) return RLPL_ERR_ALIGN;
+    }
+    return RLPL_OK;
+}
+
+// Windows of the list that fit a launch's arguments: calls f(chunks) with each in `list`, until one fails.
+template <typename F>
+int grad_windows(GradList& list, void* const* grads, const int64_t* sizes, const int32_t* dtypes, int64_t count, F f) {
+    list.count = 0;
+    int64_t chunks = 0;
+    const auto close = [&]() {
+        list.first[list.count] = uint32_t(chunks);
+        const int st = list.count ? f(chunks) : int(RLPL_OK);
+        list.count = 0;
+        chunks = 0;
+        return st;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        const int64_t here = div_up(sizes[i], kGradChunk);
+        if (list.count == kGradWindow || chunks + here >= kGradMaxChunks) {
+            const int st = close();
+            if (st != RLPL_OK) return st;
+        }
+        list.p[list.count] = grads[i];
+        list.n[list.count] = sizes[i] * 4 + dtypes[i];
+        list.first[list.count++] = uint32_t(chunks);
+        chunks += here;
+    }
+    return close();
+}
+
+// The launches that grad_windows makes of a list, or -1 where its sizes cannot be taken.
+int64_t grad_launches(const int64_t* sizes, int64_t count) {
+    if (!sizes || count < 1 || count > kGradMaxTensors) return -1;
+    int64_t launches = 0, tensors = 0, chunks = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] < 0 || sizes[i] > kGradMaxElements) return -1;
+        if (sizes[i] == 0) continue;
+        const int64_t here = div_up(sizes[i], kGradChunk);
+        if (tensors == kGradWindow || chunks + here >= kGradMaxChunks) {
+            ++launches;
+            tensors = chunks = 0;
+        }
+        ++tensors;
+        chunks += here;
+    }
+    return launches + (tensors > 0);
+}
+size_t grad_bytes(int64_t launches) { return up256(size_t(launches > 0 ? launches : 1) * kGradGrid * sizeof(double)); }
+
+// Whether two of the tensors share memory; false too where there is no host memory to find out.
+bool grads_apart(void* const* grads, const int64_t* sizes, const int32_t* dtypes, int64_t count) {
+    const auto begin = [&](int64_t i) { return reinterpret_cast<uintptr_t>(grads[i]); };
+    const auto end = [&](int64_t i) { return begin(i) + uintptr_t(sizes[i]) * dtype_bytes(dtypes[i]); };
+    const auto ordered = [&](auto at) {
+        int64_t before = -1;
+        for (int64_t k = 0; k < count; ++k) {
+            const int64_t i = at(k);
+            if (sizes[i] == 0) continue;
+            if (before >= 0 && begin(i) < end(before)) return false;
+            before = i;
+        }
+        return true;
+    };
+    if (ordered([](int64_t k) { return k; })) return true;
+    const std::unique_ptr<int64_t[]> order(new (std::nothrow) int64_t[size_t(count)]);
+    if (!order) return false;
+    std::iota(order.get(), order.get() + count, int64_t(0));
+    std::sort(order.get(), order.get() + count, [&](int64_t a, int64_t b) { return begin(a) < begin(b); });
+    return ordered([&](int64_t k) { return order[size_t(k)]; });
+}
+
+unsigned grad_grid(int64_t chunks) { return unsigned(chunks < kGradGrid ? chunks : kGradGrid); }
+
 // ----------------------------------------------------------------------------- AdamW
 
 constexpr int64_t kAdamMaxTensors = int64_t(1) << 24;
@@ -655,6 +762,104 @@ int layer_norm_bwd(const void* grad_y, const void* x, const void* weight, const 
     const NormReduceArgs r{a.part, grad_weight, grad_bias, int32_t(slabs), int32_t(cols)};
     return enqueue(pick_norm_reduce(weight_dtype), r, dim3(unsigned(div_up(cols, kNormReduceCols)), 2), kNormReduceThreads,
                    stream);
+}
+
+int rms_norm_fwd(const void* x, const void* weight, const void* residual, int64_t rows, int64_t cols, int dtype,
+                 int weight_dtype, int stream_dtype, float eps, void* y, float* rstd_out, void* stream_out,
+                 hipStream_t stream) {
+    return rms_forward({x, weight, residual, rows, cols, dtype, weight_dtype, stream_dtype, eps, y, nullptr, rstd_out,
+                        stream_out}, false, stream);
+}
+
+int rms_norm_fp8(const void* x, const void* weight, const void* residual, int64_t rows, int64_t cols, int dtype,
+                 int weight_dtype, int stream_dtype, float eps, void* q, float* scale, float* rstd_out, void* stream_out,
+                 hipStream_t stream) {
+    return rms_forward({x, weight, residual, rows, cols, dtype, weight_dtype, stream_dtype, eps, q, scale, rstd_out,
+                        stream_out}, true, stream);
+}
+
+size_t rms_norm_workspace_bytes(int64_t rows, int64_t cols) { return rms_shape_ok(rows, cols) ? rms_bytes(rows, cols) : 0; }
+
+int rms_norm_bwd(const void* grad_y, const void* h, const void* weight, const float* rstd, const void* grad_stream,
+                 int64_t rows, int64_t cols, int dtype, int weight_dtype, int stream_dtype, void* grad_h, void* grad_weight,
+                 void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!grad_y || !h || !rstd) return RLPL_ERR_NULL;
+    if (!rms_shape_ok(rows, cols)) return RLPL_ERR_SHAPE;
+    if (!norm_types_ok(dtype, weight_dtype) || !norm_types_ok(dtype, stream_dtype)) return RLPL_ERR_DTYPE;
+    const size_t re = dtype_bytes(stream_dtype), we = dtype_bytes(weight_dtype);
+    if (!is_aligned(grad_y, dtype_bytes(dtype)) || !is_aligned(h, re) || !is_aligned(weight, we) || !is_aligned(rstd, 4) ||
+        !is_aligned(grad_stream, re) || !is_aligned(grad_h, re) || !is_aligned(grad_weight, we))
+        return RLPL_ERR_ALIGN;
+    if (!workspace || workspace_bytes < rms_bytes(rows, cols)) return RLPL_ERR_WORKSPACE;
+    if (!is_aligned(workspace, 256)) return RLPL_ERR_ALIGN;
+    int st = device();
+    if (st != RLPL_OK) return st;
+    if (!grad_h && !grad_weight) return RLPL_OK;
+    const NormRowKernel k = pick_rms_bwd(dtype, stream_dtype, cols);
+    if (!k.kernel) return RLPL_ERR_DTYPE;
+    const int64_t groups = norm_held_grid(rows, cols, k.rows_per_group);
+    const RmsBwdArgs a{grad_y, h, weight, rstd, grad_stream, grad_h, grad_weight ? static_cast<float*>(workspace) : nullptr,
+                       rows, int32_t(cols), weight_dtype == RLPL_F32 ? 1 : 0};
+    st = enqueue(k.kernel, a, dim3(unsigned(groups)), k.threads, stream);
+    if (st != RLPL_OK || !grad_weight) return st;
+    const NormReduceArgs r{a.part, grad_weight, nullptr, int32_t(groups), int32_t(cols)};
+    return enqueue(pick_norm_reduce(weight_dtype), r, dim3(unsigned(div_up(cols, kNormReduceCols)), 1), kNormReduceThreads,
+                   stream);
+}
+
+size_t rlpl_grad_norm_workspace_bytes(const int64_t* sizes, int64_t count) {
+    const int64_t launches = grad_launches(sizes, count);
+    return launches < 0 ? 0 : grad_bytes(launches);
+}
+
+int rlpl_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int64_t count, int norm_kind,
+                   const float* grad_scale, float max_norm, float eps, float* norm_out, float* scale_out, void* workspace,
+                   size_t workspace_bytes, hipStream_t stream) {
+    void* const* list = const_cast<void* const*>(grads);
+    int st = grad_check(list, sizes, dtypes, count);
+    if (st != RLPL_OK) return st;
+    if (!norm_out) return RLPL_ERR_NULL;
+    if (norm_kind != RLPL_NORM_2 && norm_kind != RLPL_NORM_INF) return RLPL_ERR_PARAM;
+    if (scale_out && (!std::isfinite(max_norm) || max_norm < 0.0f || !std::isfinite(eps) || eps < 0.0f)) return RLPL_ERR_PARAM;
+    if (!is_aligned(grad_scale, 4) || !is_aligned(norm_out, 4) || !is_aligned(scale_out, 4)) return RLPL_ERR_ALIGN;
+    if (!workspace || workspace_bytes < grad_bytes(grad_launches(sizes, count))) return RLPL_ERR_WORKSPACE;
+    if (!is_aligned(workspace, 256)) return RLPL_ERR_ALIGN;
+    if ((st = device()) != RLPL_OK) return st;
+    const bool inf = norm_kind == RLPL_NORM_INF;
+    int64_t chunks = 0, tensors = 0;
+    for (int64_t i = 0; i < count && chunks <= kGradAloneChunks; ++i) {
+        chunks += div_up(sizes[i], kGradChunk);
+        tensors += sizes[i] > 0;
+    }
+    GradNormArgs a;
+    a.part = static_cast<double*>(workspace);
+    a.finish = GradFinish{a.part, norm_out, scale_out, grad_scale, max_norm, eps, 0, inf ? 1 : 0};
+    if (chunks <= kGradAloneChunks && tensors <= kGradWindow && tensors > 0)
+        return grad_windows(a.list, list, sizes, dtypes, count,
+                            [&](int64_t) { return enqueue(pick_grad_alone(inf), a, dim3(1), kGradAloneThreads, stream); });
+    st = grad_windows(a.list, list, sizes, dtypes, count, [&](int64_t here) {
+        const unsigned grid = grad_grid(here);
+        const int s = enqueue(pick_grad_norm(inf), a, dim3(grid), kGradThreads, stream);
+        a.part += grid;
+        a.finish.parts += int32_t(grid);
+        return s;
+    });
+    return st != RLPL_OK ? st : enqueue(grad_finish_kernel(), a.finish, dim3(1), kGradAloneThreads, stream);
+}
+
+int rlpl_grad_scale(void* const* grads, const int64_t* sizes, const int32_t* dtypes, int64_t count, const float* scale,
+                    hipStream_t stream) {
+    int st = grad_check(grads, sizes, dtypes, count);
+    if (st != RLPL_OK) return st;
+    if (!scale) return RLPL_ERR_NULL;
+    if (!is_aligned(scale, 4)) return RLPL_ERR_ALIGN;
+    if (!grads_apart(grads, sizes, dtypes, count)) return RLPL_ERR_PARAM;
+    if ((st = device()) != RLPL_OK) return st;
+    GradScaleArgs a;
+    a.scale = scale;
+    return grad_windows(a.list, grads, sizes, dtypes, count, [&](int64_t here) {
+        return enqueue(grad_scale_kernel(), a, dim3(grad_grid(here)), kGradThreads, stream);
+    });
 }
 
 }  // extern "C"

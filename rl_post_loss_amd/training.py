@@ -4,7 +4,10 @@
   large vocabulary, with the gradients of the hidden states, the projection and its bias;
 * ``layer_norm_fwd`` / ``layer_norm_bwd``: the norm of the hidden states that the output projection reads,
   with the reduction of its weight's and bias's gradients;
-* ``adamw_plan`` / ``adamw_step``: one AdamW step over a list of tensors, moments in float32 or in 8 bits.
+* ``rms_norm_fwd`` / ``rms_norm_fp8`` / ``rms_norm_bwd``: the norm by the root mean square, with the residual's addition,
+  in the input's type or in 8 bits with scales;
+* ``adamw_plan`` / ``adamw_step``: one AdamW step over a list of tensors, moments in float32 or in 8 bits;
+* ``grad_norm`` / ``scale_grads`` / ``clip_grads``: the norm over a list of gradients, and clipping.
 
 As in the package's other entry points, this module marshals arguments only: every step runs in the library's HIP
 kernels on the current stream of the tensors' device, without synchronising.
@@ -12,6 +15,7 @@ kernels on the current stream of the tensors' device, without synchronising.
 from __future__ import annotations
 
 import ctypes
+import math
 from contextlib import nullcontext
 from typing import Optional, Sequence
 
@@ -22,7 +26,8 @@ from torch.autograd.graph import increment_version
 
 from . import DTYPE, _aligned, _check, _ws_ptr, library
 
-__all__ = ["linear_cross_entropy", "linear_cross_entropy_fwd", "layer_norm_fwd", "layer_norm_bwd", "adamw_plan", "adamw_step", "AdamWPlan"]
+__all__ = ["linear_cross_entropy", "linear_cross_entropy_fwd", "layer_norm_fwd", "layer_norm_bwd", "adamw_plan", "adamw_step", "AdamWPlan",
+           "rms_norm_fwd", "rms_norm_fp8", "rms_norm_bwd", "grad_norm", "scale_grads", "clip_grads"]
 
 REDUCTION = {"mean": 0, "sum": 1}
 CE_HIDDEN_F32 = 1    # rlpl_linear_cross_entropy flags (RLPL_CE_HIDDEN_F32)
@@ -240,6 +245,85 @@ def layer_norm_bwd(grad_y, x, weight, mean, rstd, *, need_x=True, need_weight=Tr
     return dx, dw, db
 
 
+# ------------------------------------------------------------------------------------------------------- RMS norm
+
+GROUP = 128   # columns of an 8-bit row that share one scale
+
+
+def _rms_operands(x, weight, residual):
+    x = _norm_rows(x, "x")
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor) or residual.dtype not in (x.dtype, torch.float32):
+            raise TypeError("residual must be a tensor of x's dtype or float32")
+        if residual.shape != x.shape or residual.device != x.device:
+            raise ValueError("residual must match x in shape and device")
+        residual = _dense(residual)
+    return x, _norm_vector(weight, "weight", x), residual
+
+
+def _rms_call(fn, x, w, residual, eps, outputs):
+    H = x.shape[-1]
+    stream = None if residual is None else torch.empty_like(residual)
+    rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    with _on(x.device):
+        _check(fn, getattr(library(), fn)(
+            x.data_ptr(), _ptr(w), _ptr(residual), x.numel() // H, H, DTYPE[x.dtype], DTYPE[x.dtype if w is None else w.dtype],
+            DTYPE[x.dtype if residual is None else residual.dtype], float(eps), *(t.data_ptr() for t in outputs),
+            rstd.data_ptr(), _ptr(stream), _stream(x.device)))
+    return rstd, stream
+
+
+def rms_norm_fwd(x, weight=None, residual=None, *, eps=1e-6):
+    """RMS norm over the last dimension of h = x + residual (x itself without a residual): (y, rstd, h), None for the
+    last without a residual.
+
+    x (*, H) float32, float16 or bfloat16, H up to 16384; weight (H,) of x's dtype or float32, or None (ones); residual of
+    x's shape, of its dtype or float32.  y = h / sqrt(avg h^2 + eps) * weight has x's dtype; h, the new residual stream,
+    has the residual's, and the norm is that of h as it is stored; rstd is float32 of x's leading shape."""
+    x, w, residual = _rms_operands(x, weight, residual)
+    y = torch.empty_like(x)
+    return y, *_rms_call("rms_norm_fwd", x, w, residual, eps, (y,))
+
+
+def rms_norm_fp8(x, weight=None, residual=None, *, eps=1e-6):
+    """``rms_norm_fwd`` with y in 8 bits: (q, scale, rstd, h).  q has x's shape and dtype float8_e4m3fn; scale is float32
+    (*, ceil(H / 128)), one for every 128 columns: y is about q * scale, as ``fp8_linear`` takes it."""
+    x, w, residual = _rms_operands(x, weight, residual)
+    q = x.new_empty(x.shape, dtype=torch.float8_e4m3fn)
+    scale = x.new_empty((*x.shape[:-1], (x.shape[-1] + GROUP - 1) // GROUP), dtype=torch.float32)
+    return q, scale, *_rms_call("rms_norm_fp8", x, w, residual, eps, (q, scale))
+
+
+def rms_norm_bwd(grad_y, h, weight, rstd, grad_stream=None, *, need_h=True, need_weight=True, workspace=None):
+    """Gradients of sum(grad_y * y) + sum(grad_stream * h): (grad_h, grad_weight), None where not wanted.  h and rstd are
+    the forward's (h is x without a residual).  grad_h, the gradient of x and of the residual alike, has h's dtype;
+    grad_weight the weight's (float32 sums over the rows, rounded once)."""
+    gy = _norm_rows(grad_y, "grad_y")
+    h = _norm_rows(h, "h")
+    if h.shape != gy.shape or h.device != gy.device or h.dtype not in (gy.dtype, torch.float32):
+        raise ValueError("h must match grad_y in shape and device, and have its dtype or float32")
+    w = _norm_vector(weight, "weight", gy)
+    if not isinstance(rstd, torch.Tensor) or rstd.dtype != torch.float32 or rstd.shape != h.shape[:-1] or rstd.device != h.device:
+        raise ValueError(f"rstd must be the forward's float32 tensor of shape {tuple(h.shape[:-1])}")
+    if grad_stream is not None:
+        if not isinstance(grad_stream, torch.Tensor) or grad_stream.dtype != h.dtype or grad_stream.shape != h.shape \
+                or grad_stream.device != h.device:
+            raise ValueError("grad_stream must match h in shape, dtype and device")
+        grad_stream = _dense(grad_stream)
+    rstd, H = _dense(rstd), h.shape[-1]
+    rows = h.numel() // H
+    dh = torch.empty_like(h) if need_h else None
+    dw = torch.empty_like(w) if need_weight and w is not None else None
+    lib = library()
+    ws = _scratch(lib.rms_norm_workspace_bytes(rows, H), workspace, h.device, "rms_norm_workspace_bytes")
+    wp, wn = _ws_ptr(ws)
+    with _on(h.device):
+        _check("rms_norm_bwd", lib.rms_norm_bwd(
+            gy.data_ptr(), h.data_ptr(), _ptr(w), rstd.data_ptr(), _ptr(grad_stream), rows, H, DTYPE[gy.dtype],
+            DTYPE[gy.dtype if w is None else w.dtype], DTYPE[h.dtype], _ptr(dh), _ptr(dw), wp, wn, _stream(h.device)))
+    return dh, dw
+
+
 # ------------------------------------------------------------------------------------------------------- AdamW
 
 def _pointers(tensors) -> ctypes.Array:
@@ -426,3 +510,101 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], *, step
     if any(g is None for g in grads):
         written = [p for p, g in zip(written, grads + grads) if g is not None]
     increment_version(written)   # a graph that saved an old value says so in its backward pass
+
+
+# ------------------------------------------------------------------------------------------------------- gradients' norm
+
+NORM = {2.0: 0, math.inf: 1}
+
+
+def _without_gaps(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one run of memory, each once, in any order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    at = 1
+    for stride, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != at:
+            return False
+        at *= n
+    return True
+
+
+def _grad_list(grads, in_place):
+    """(tensors to keep until the call returns, pointers, sizes, dtypes, device) of the gradients that are there."""
+    kept, dev = [], None
+    for i, g in enumerate(grads):
+        if g is None:
+            continue
+        if not isinstance(g, torch.Tensor) or not g.is_cuda or g.dtype not in DTYPE:
+            raise TypeError(f"gradient {i} must be a float32, float16 or bfloat16 CUDA (HIP) tensor")
+        if dev is None:
+            dev = g.device
+        elif g.device != dev:
+            raise ValueError(f"gradient {i} must be on {dev}, as the first one")
+        if not _without_gaps(g):
+            if in_place:
+                raise ValueError(f"gradient {i} must fill its memory without gaps to be scaled in place")
+            g = g.contiguous()
+        kept.append(g)
+    if not kept:
+        raise ValueError("grads holds no tensor")
+    n = len(kept)
+    return (kept, (ctypes.c_void_p * n)(*[g.data_ptr() or None for g in kept]), (ctypes.c_int64 * n)(*[g.numel() for g in kept]),
+            (ctypes.c_int32 * n)(*[DTYPE[g.dtype] for g in kept]), dev)
+
+
+def _norm_of(listed, max_norm, norm_type, eps, grad_scale, workspace):
+    kept, pointers, sizes, dtypes, dev = listed
+    if norm_type not in NORM:
+        raise ValueError("norm_type must be 2 or inf")
+    scale_at = None if grad_scale is None else _device_scalar(grad_scale, "grad_scale", torch.float32, dev)
+    lib = library()
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    scale = None if max_norm is None else torch.empty((), dtype=torch.float32, device=dev)
+    ws = _scratch(lib.rlpl_grad_norm_workspace_bytes(sizes, len(kept)), workspace, dev, "rlpl_grad_norm_workspace_bytes")
+    wp, wn = _ws_ptr(ws)
+    with _on(dev):
+        _check("rlpl_grad_norm", lib.rlpl_grad_norm(
+            pointers, sizes, dtypes, len(kept), NORM[norm_type], scale_at, 0.0 if max_norm is None else float(max_norm),
+            float(eps), norm.data_ptr(), _ptr(scale), wp, wn, _stream(dev)))
+    return norm, scale
+
+
+def grad_norm(grads: Sequence[Optional[torch.Tensor]], *, max_norm=None, norm_type=2.0, eps=1e-6,
+              grad_scale: Optional[torch.Tensor] = None, workspace=None):
+    """The norm over all gradients (a 0-d float32 tensor), or with ``max_norm`` (norm, scale): scale =
+    min(1, max_norm / (norm + eps)), the factor that clips the gradients, which ``adamw_step`` takes as its grad_scale.
+
+    grads: float32, float16 or bfloat16 tensors of one device, of any strides, in any mixture, or None (passed over).
+    norm_type: 2 or math.inf.  grad_scale: a one-element float32 device tensor that the gradients are meant to be
+    multiplied by (1 / a loss scale): the norm is of the products, and scale includes it.  Squares are summed in float64.
+    A NaN makes both NaN, an infinite norm a scale of 0."""
+    norm, scale = _norm_of(_grad_list(grads, False), max_norm, norm_type, eps, grad_scale, workspace)
+    return norm if max_norm is None else (norm, scale)
+
+
+def _scale_listed(listed, scale):
+    kept, pointers, sizes, dtypes, dev = listed
+    at = _device_scalar(scale, "scale", torch.float32, dev)
+    with _on(dev):
+        _check("rlpl_grad_scale", library().rlpl_grad_scale(pointers, sizes, dtypes, len(kept), at, _stream(dev)))
+    increment_version(kept)   # a graph that saved an old value says so in its backward pass
+
+
+def scale_grads(grads: Sequence[Optional[torch.Tensor]], scale: torch.Tensor) -> None:
+    """Multiplies the gradients by ``scale``, a one-element float32 device tensor, in place (each element rounded once).
+    grads as for ``grad_norm``; each fills its memory without gaps (a transposed one may), and no two overlap.
+    A scale of exactly 1 writes nothing."""
+    _scale_listed(_grad_list(grads, True), scale)
+
+
+def clip_grads(grads: Sequence[Optional[torch.Tensor]], max_norm, *, norm_type=2.0, eps=1e-6, workspace=None) -> torch.Tensor:
+    """Scales the gradients in place by min(1, max_norm / (norm + eps)) and returns their norm before that, a 0-d float32
+    tensor.  Nothing is written where the norm is within max_norm.  Where ``adamw_step`` follows, ``grad_norm``'s scale
+    saves this second pass over the gradients."""
+    if max_norm is None:
+        raise ValueError("max_norm must be a number")
+    listed = _grad_list(grads, True)
+    norm, scale = _norm_of(listed, max_norm, norm_type, eps, None, workspace)
+    _scale_listed(listed, scale)
+    return norm

@@ -14,7 +14,7 @@ LIB = os.path.join(PKG, "librl_post_loss.so")
 SOURCES = ["loss_kernels_bf16.hip", "loss_kernels_f16.hip", "loss_kernels_f32.hip", "loss_kernels.hip",
            "vocab_kernels.hip", "logprob_kernels.hip", "abi.cpp", "ce_kernels.hip", "norm_kernels.hip",
            "adamw_kernels.hip", "rms_kernels.hip", "grad_kernels.hip", "train_abi.cpp", "token_kernels.hip",
-           "fp8_kernels.hip", "score_abi.cpp"]
+           "fp8_kernels.hip", "fp8_gemm.hip", "score_abi.cpp"]
 # Measurement helpers for bench.py (timing loops over the public entry points,
 # reference kernels); linked against the loss library, found beside it.
 BENCH_LIB = os.path.join(PKG, "librlpl_bench.so")

@@ -29,10 +29,28 @@ struct Fp8LinearArgs {
     const void* bias;          // (vocab) of the output's type, or NULL
     void* out;                 // (n, vocab)
     int32_t n, K, vocab, blocks;
+    uint32_t tiles_v, tiles_t; // of fp8_tile
+    int32_t scale_ld;          // kFp8Large: x_scale is (blocks, scale_ld)
 };
+// (rows, cols) to (cols, ld).
+struct TurnArgs {
+    const float* from;
+    float* to;
+    int32_t rows, cols, ld;
+};
+const void* turn_kernel();
+constexpr int kTurnTile = 64;  // rows and columns of a workgroup
 
-// Few rows: a workgroup takes 64 vocabulary entries and `tokens` rows, its four wavefronts every fourth block of K each.
-constexpr int kFp8SmallVocab = 64;
-const void* pick_fp8_small(int out_dtype, int tokens);   // 16, 32 or 64 rows
+// Tiles of entries by tokens (fp8_gemm.hip).
+struct Fp8TileShape {
+    int vocab, tokens, threads, lds;
+};
+enum { kFp8Small = 0, kFp8Middle = 1, kFp8Large = 2 };     // float32 outputs take the small one
+constexpr Fp8TileShape kFp8Shapes[] = {{64, 64, 256, 32 * 1024}, {128, 128, 256, 64 * 1024}, {256, 256, 512, 160 * 1024}};
+const void* pick_fp8_tile(int out_dtype, int kind);
+
+// Up to 16 rows: a workgroup takes 64 vocabulary entries, or 32 or 16, its four wavefronts every fourth block of K each.
+constexpr int kFp8FewRows = 16;
+const void* pick_fp8_few(int out_dtype, int entries);
 
 }  // namespace rlpl

@@ -3,10 +3,9 @@
 //
 //   out[i][v] = sum_b sx[i][b] sw[v / 128][b] sum_{k in block b} x[i][k] w[v][k]  (+ bias[v])
 //
-// A block of K is one matrix instruction deep (v_mfma_f32_16x16x128_f8f6f4):
-// each starts from zero and its result is added to the accumulators times the
-// block's two scales.  The projection takes the instruction's rows and the
-// tokens its columns, so that a lane's four results share both scales and
+// A block of K starts from zero on the matrix cores (fp8_mfma.h), and its result is added to the
+// accumulators times the block's two scales.  The projection takes the instructions' rows and the
+// tokens their columns, so that a lane's four results share both scales and
 // lie side by side in the output.  Sums are float32; the output is rounded once.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -14,6 +13,7 @@
 #include "device_common.h"
 #include "fp8_convert.h"
 #include "fp8_kernels.h"
+#include "fp8_mfma.h"
 #include "loss_kernels.h"
 #include "row_io.h"
 
@@ -21,83 +21,88 @@ namespace rlpl {
 
 namespace {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-// A 16 x 16 tile of one block of K: element (i, j) = sum_k a[i][k] b[j][k].  Lane l holds 32 consecutive K bytes from
-// 32 (l / 16) of row l % 16 of each operand, and rows 4 (l / 16) .. + 3 of column l % 16 of the result.
-__device__ __forceinline__ f32x4 product(v8i a, v8i b) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+// The rows of an operand from `first` on as a buffer: what lies past the last one reads as zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const uint8_t* x, int32_t first, int32_t rows, int32_t K) {
+    const int64_t bytes = int64_t(rows - first) * K;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(x) + int64_t(first) * K, 0,
+                                             int(bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0), 0x00020000);
+}
+// 32 bytes from `offset` (32 bytes of one row, `left` of them, or fewer, before its end; a multiple of 16), zeros past that.
+__device__ __forceinline__ v8i load32(__amdgpu_buffer_rsrc_t from, uint32_t offset, int32_t left) {
+    constexpr uint32_t kPast = 0xFFFFFFF0u;
+    const auto lo = __builtin_amdgcn_raw_buffer_load_b128(from, int(left > 0 ? offset : kPast), 0, 0);
+    const auto hi = __builtin_amdgcn_raw_buffer_load_b128(from, int(left > 16 ? offset + 16u : kPast), 0, 0);
+    return __builtin_bit_cast(v8i, __builtin_shufflevector(__builtin_bit_cast(u32x4, lo), __builtin_bit_cast(u32x4, hi), 0, 1, 2, 3,
+                                                           4, 5, 6, 7));
 }
 
-// 32 bytes of a row from byte k on, zeros past K (a multiple of 16).
-__device__ __forceinline__ v8i load32(const uint8_t* row, int32_t k, int32_t K) {
-    u32x4 lo{0, 0, 0, 0}, hi{0, 0, 0, 0};
-    if (k < K) lo = *reinterpret_cast<const u32x4*>(row + k);
-    if (k + 16 < K) hi = *reinterpret_cast<const u32x4*>(row + k + 16);
-    return v8i{int(lo.x), int(lo.y), int(lo.z), int(lo.w), int(hi.x), int(hi.y), int(hi.z), int(hi.w)};
-}
-
-template <typename T, int NT>
-__global__ void __launch_bounds__(kFp8Threads) fp8_small(const Fp8LinearArgs a) {
-    constexpr int F = kFp8SmallVocab / 16;
-    __shared__ f32x4 part[3][F * NT][64];
+// Up to 16 rows: the projection goes from memory to registers, each byte once; the next block's 64 x 128 bytes are on
+// their way while a block's are multiplied.
+template <typename T, int F>
+__global__ void __launch_bounds__(kFp8Threads) fp8_few(const Fp8LinearArgs a) {
+    constexpr int kStep = kFp8Threads / 64;
+    using Frag = Fragment<sizeof(T) == 4>;
+    __shared__ f32x4 part[kStep - 1][F][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quarter = lane >> 4;
-    const int32_t v0 = int32_t(blockIdx.x) * kFp8SmallVocab, t0 = int32_t(blockIdx.y) * (16 * NT);
-    f32x4 acc[F][NT] = {};
-    const uint8_t* w[F];
-    const uint8_t* x[NT];
-    const float* sx[NT];
-#pragma unroll
-    for (int f = 0; f < F; ++f) {          // rows past the end read the last one: their results are not stored
-        const int32_t v = v0 + 16 * f + row < a.vocab ? v0 + 16 * f + row : a.vocab - 1;
-        w[f] = a.w + int64_t(v) * a.K;
-    }
-#pragma unroll
-    for (int g = 0; g < NT; ++g) {
-        const int32_t t = t0 + 16 * g + row < a.n ? t0 + 16 * g + row : a.n - 1;
-        x[g] = a.x + int64_t(t) * a.K;
-        sx[g] = a.x_scale + int64_t(t) * a.blocks;
-    }
+    const int32_t v0 = int32_t(blockIdx.x) * (16 * F);
+    f32x4 acc[F] = {};
+    const __amdgpu_buffer_rsrc_t from_w = rows_from(a.w, v0, a.vocab, a.K), from_x = rows_from(a.x, 0, a.n, a.K);
+    const float* sx = a.x_scale + int64_t(row < a.n ? row : a.n - 1) * a.blocks;
     const float* sw = a.w_scale + int64_t(v0 / kFp8Group) * a.blocks;
-    for (int32_t b = wave; b < a.blocks; b += kFp8Threads / 64) {
+    v8i wf[F], xf;
+    float s_x = 0.0f, s_w = 0.0f;
+    const auto load = [&](int32_t b) {
         const int32_t k = b * kFp8Group + 32 * quarter;
-        v8i wf[F], xf[NT];
 #pragma unroll
-        for (int f = 0; f < F; ++f) wf[f] = load32(w[f], k, a.K);
+        for (int f = 0; f < F; ++f) wf[f] = load32(from_w, uint32_t(16 * f + row) * uint32_t(a.K) + uint32_t(k), a.K - k);
+        xf = load32(from_x, uint32_t(row) * uint32_t(a.K) + uint32_t(k), a.K - k);
+        s_x = sx[b];
+        s_w = sw[b];
+    };
+    if (wave < a.blocks) load(wave);
+    for (int32_t b = wave; b < a.blocks; b += kStep) {
+        Frag wb[F];
+        const Frag xb(xf);
+        const float sb = s_x * s_w;
 #pragma unroll
-        for (int g = 0; g < NT; ++g) xf[g] = load32(x[g], k, a.K);
+        for (int f = 0; f < F; ++f) wb[f] = Frag(wf[f]);
+        if (b + kStep < a.blocks) load(b + kStep);
 #pragma unroll
-        for (int g = 0; g < NT; ++g) {
-            const float s = sx[g][b] * sw[b];
-#pragma unroll
-            for (int f = 0; f < F; ++f) acc[f][g] += s * product(wf[f], xf[g]);
-        }
+        for (int f = 0; f < F; ++f) acc[f] += sb * block_product(wb[f], xb);
     }
     // the wavefronts' shares, in their order
     if (wave > 0) {
 #pragma unroll
-        for (int f = 0; f < F; ++f)
-#pragma unroll
-            for (int g = 0; g < NT; ++g) part[wave - 1][f * NT + g][lane] = acc[f][g];
+        for (int f = 0; f < F; ++f) part[wave - 1][f][lane] = acc[f];
     }
     __syncthreads();
-    if (wave > 0) return;
-    T* out = static_cast<T*>(a.out);
+    if (wave > 0 || row >= a.n) return;
+    T* out = static_cast<T*>(a.out) + int64_t(row) * a.vocab;
     const T* bias = static_cast<const T*>(a.bias);
 #pragma unroll
-    for (int f = 0; f < F; ++f)
+    for (int f = 0; f < F; ++f) {
+        f32x4 sum = acc[f];
 #pragma unroll
-        for (int g = 0; g < NT; ++g) {
-            f32x4 s = acc[f][g];
+        for (int i = 0; i < kStep - 1; ++i) sum += part[i][f][lane];
+        const int32_t v = v0 + 16 * f + 4 * quarter;
 #pragma unroll
-            for (int i = 0; i < 3; ++i) s += part[i][f * NT + g][lane];
-            const int32_t t = t0 + 16 * g + row, v = v0 + 16 * f + 4 * quarter;
-            if (t >= a.n) continue;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (v + i < a.vocab) out[int64_t(t) * a.vocab + v + i] = T(bias ? s[i] + widen(bias[v + i]) : s[i]);
-        }
+        for (int i = 0; i < 4; ++i)
+            if (v + i < a.vocab) out[v + i] = T(bias ? sum[i] + widen(bias[v + i]) : sum[i]);
+    }
+}
+
+// A 64 x 64 tile of scales turned over, by a wavefront a row at a time.
+__global__ void __launch_bounds__(kFp8Threads) turn(const TurnArgs a) {
+    __shared__ float tile[kTurnTile][kTurnTile + 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t r0 = int64_t(blockIdx.x) * kTurnTile, c0 = int64_t(blockIdx.y) * kTurnTile;
+#pragma unroll 4
+    for (int i = wave; i < kTurnTile; i += kFp8Threads / 64)
+        if (r0 + i < a.rows && c0 + lane < a.cols) tile[i][lane] = a.from[(r0 + i) * a.cols + c0 + lane];
+    __syncthreads();
+#pragma unroll 4
+    for (int i = wave; i < kTurnTile; i += kFp8Threads / 64)
+        if (c0 + i < a.cols && r0 + lane < a.rows) a.to[(c0 + i) * a.ld + r0 + lane] = tile[lane][i];
 }
 
 // A lane's piece of 8 columns: where it lies and how many are there.
@@ -192,15 +197,6 @@ __global__ void __launch_bounds__(kFp8Threads) quantise(const QuantiseArgs a) {
     }
 }
 
-template <typename T>
-const void* small_of(int tokens) {
-    switch (tokens) {
-    case 16: return reinterpret_cast<const void*>(&fp8_small<T, 1>);
-    case 32: return reinterpret_cast<const void*>(&fp8_small<T, 2>);
-    case 64: return reinterpret_cast<const void*>(&fp8_small<T, 4>);
-    }
-    return nullptr;
-}
 template <bool SQUARE>
 const void* quantise_of(int dtype) {
     switch (dtype) {
@@ -213,14 +209,24 @@ const void* quantise_of(int dtype) {
 
 }  // namespace
 
-const void* pick_fp8_small(int out_dtype, int tokens) {
+template <int F>
+const void* few_of(int out_dtype) {
     switch (out_dtype) {
-    case kF32: return small_of<float>(tokens);
-    case kF16: return small_of<_Float16>(tokens);
-    case kBF16: return small_of<__bf16>(tokens);
+    case kF32: return reinterpret_cast<const void*>(&fp8_few<float, F>);
+    case kF16: return reinterpret_cast<const void*>(&fp8_few<_Float16, F>);
+    case kBF16: return reinterpret_cast<const void*>(&fp8_few<__bf16, F>);
     }
     return nullptr;
 }
+const void* pick_fp8_few(int out_dtype, int entries) {
+    switch (entries) {
+    case 16: return few_of<1>(out_dtype);
+    case 32: return few_of<2>(out_dtype);
+    case 64: return few_of<4>(out_dtype);
+    }
+    return nullptr;
+}
+const void* turn_kernel() { return reinterpret_cast<const void*>(&turn); }
 const void* pick_quantise(int dtype, bool square) { return square ? quantise_of<true>(dtype) : quantise_of<false>(dtype); }
 
 }  // namespace rlpl

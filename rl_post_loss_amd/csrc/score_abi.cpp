@@ -20,7 +20,19 @@ constexpr int64_t kMaxRows = int64_t(1) << 31;
 constexpr int64_t kMaxVocab = (int64_t(1) << 31) - 65536;   // columns are counted in 32 bits, a step of lanes past the end
 constexpr int64_t kMaxElements = int64_t(1) << 62;
 
-Devices<is_gfx950> g_devices;
+// The tiles' ring is beyond the default limit of LDS.
+bool set_up(int dev) {
+    if (!is_gfx950(dev)) return false;
+    for (int dt : {RLPL_F32, RLPL_F16, RLPL_BF16})
+        for (int kind = kFp8Small; kind <= kFp8Large; ++kind) {
+            const void* k = pick_fp8_tile(dt, kind);
+            if (k && hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kFp8Shapes[kind].lds) != hipSuccess)
+                return false;
+        }
+    return true;
+}
+
+Devices<set_up> g_devices;
 int device() { return g_devices.current(); }
 
 unsigned capped(int64_t grid, int64_t cap) { return unsigned(grid < cap ? grid : cap); }
@@ -57,7 +69,39 @@ bool fp8_shape_ok(int64_t n, int64_t h, int64_t vocab) {
     return n >= 1 && n <= kFp8MaxRows && h >= 16 && h <= kFp8MaxHidden && h % 16 == 0 && vocab >= 1 && vocab < kFp8MaxVocab;
 }
 
-size_t fp8_bytes(int64_t, int64_t, int64_t) { return 256; }
+// The time of a product's tiles in microseconds, to choose between their shapes: a tile of `steps` blocks of K takes
+// fixed + step * steps alone, and a chip full of them fill + pace * steps each on one of its 256 compute units (fitted to
+// 23 sizes between 1 x 1024 x 1000 and 8192^3: 333 x 2048 x 5003 takes 11 us with the small shape, 18 and 38 with the
+// others; 2048 x 4096 x 4096 68, 48 and 65; 2048 x 4096 x 128256 1969, 1533 and 1026).
+struct Fp8Pace {
+    double fixed, step, fill, pace;
+};
+constexpr Fp8Pace kFp8Paces[] = {{2.0, 0.40, 0.5, 0.215}, {3.2, 0.825, 2.0, 0.6}, {8.8, 1.47, 9.0, 1.7}};
+double fp8_time(int kind, int64_t n, int64_t blocks, int64_t vocab) {
+    const Fp8TileShape& s = kFp8Shapes[kind];
+    const Fp8Pace& p = kFp8Paces[kind];
+    const double tiles = double(div_up(vocab, s.vocab)) * double(div_up(n, s.tokens));
+    const double one = p.fixed + p.step * double(blocks), all = tiles * (p.fill + p.pace * double(blocks)) / 256.0;
+    return all > one ? all + 0.3 * one : one + 0.3 * all;
+}
+int fp8_kind(int64_t n, int64_t blocks, int64_t vocab, int out_dtype) {
+    if (out_dtype == RLPL_F32) return kFp8Small;
+    int best = kFp8Small;
+    for (int kind : {kFp8Middle, kFp8Large})
+        if (fp8_time(kind, n, blocks, vocab) < fp8_time(best, n, blocks, vocab)) best = kind;
+    return best;
+}
+
+// Entries a workgroup of few rows takes: fewer where there would be few workgroups (one compute unit streams 64 of 8192 in
+// 19 us), more where x is read often (1 x 8192 x 512 takes 11.2, 11.6 and 19.0 us with 16, 32 and 64; 1 x 4096 x 16384 12.8,
+// 12.5 and 14.8; 16 x 4096 x 128256 150, 117 and 105).
+int fp8_few_entries(int64_t vocab) { return vocab <= 8192 ? 16 : vocab <= 24576 ? 32 : 64; }
+
+// For the large shape, the scales of the rows, one block of K after the other: a lane's tokens are then neighbours
+// (2048 x 4096 x 128256: 1113 us with the scales where they lie, a cache line a token and step; 1026 with 3 us to turn
+// them).
+int64_t fp8_scale_ld(int64_t n) { return div_up(n, kTurnTile) * kTurnTile; }
+size_t fp8_bytes(int64_t n, int64_t h) { return up256(size_t(fp8_scale_ld(n)) * size_t(div_up(h, kFp8Group)) * sizeof(float)); }
 
 }  // namespace
 
@@ -151,7 +195,7 @@ int rlpl_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t row_str
 }
 
 size_t fp8_linear_workspace_bytes(int64_t n, int64_t hidden_size, int64_t vocab) {
-    return fp8_shape_ok(n, hidden_size, vocab) ? fp8_bytes(n, hidden_size, vocab) : 0;
+    return fp8_shape_ok(n, hidden_size, vocab) ? fp8_bytes(n, hidden_size) : 0;
 }
 
 int fp8_linear(const void* x, const float* x_scale, const void* weight, const float* weight_scale, const void* bias, int64_t n,
@@ -164,15 +208,29 @@ int fp8_linear(const void* x, const float* x_scale, const void* weight, const fl
     if (!is_aligned(x, 16) || !is_aligned(weight, 16) || !is_aligned(x_scale, 4) || !is_aligned(weight_scale, 4) ||
         !is_aligned(bias, e) || !is_aligned(out, e))
         return RLPL_ERR_ALIGN;
-    if (!workspace || workspace_bytes < fp8_bytes(n, hidden_size, vocab)) return RLPL_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < fp8_bytes(n, hidden_size)) return RLPL_ERR_WORKSPACE;
     if (!is_aligned(workspace, 256)) return RLPL_ERR_ALIGN;
     const int st = device();
     if (st != RLPL_OK) return st;
-    const Fp8LinearArgs a{static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(weight), weight_scale, bias, out,
-                          int32_t(n), int32_t(hidden_size), int32_t(vocab), int32_t(div_up(hidden_size, kFp8Group))};
-    const int tokens = n <= 16 ? 16 : n <= 32 ? 32 : 64;
-    return enqueue(pick_fp8_small(out_dtype, tokens), a,
-                   dim3(unsigned(div_up(vocab, kFp8SmallVocab)), unsigned(div_up(n, tokens))), kFp8Threads, stream);
+    Fp8LinearArgs a{static_cast<const uint8_t*>(x), x_scale, static_cast<const uint8_t*>(weight), weight_scale, bias, out,
+                    int32_t(n), int32_t(hidden_size), int32_t(vocab), int32_t(div_up(hidden_size, kFp8Group)), 0, 0};
+    if (n <= kFp8FewRows) {
+        const int entries = fp8_few_entries(vocab);
+        return enqueue(pick_fp8_few(out_dtype, entries), a, dim3(unsigned(div_up(vocab, entries))), kFp8Threads, stream);
+    }
+    const int kind = fp8_kind(n, a.blocks, vocab, out_dtype);
+    const Fp8TileShape& s = kFp8Shapes[kind];
+    a.tiles_v = uint32_t(div_up(vocab, s.vocab));
+    a.tiles_t = uint32_t(div_up(n, s.tokens));
+    if (kind == kFp8Large) {
+        a.scale_ld = int32_t(fp8_scale_ld(n));
+        const TurnArgs t{x_scale, static_cast<float*>(workspace), a.n, a.blocks, a.scale_ld};
+        const int turned = enqueue(turn_kernel(), t, dim3(unsigned(div_up(n, kTurnTile)), unsigned(div_up(a.blocks, kTurnTile))),
+                                   kFp8Threads, stream);
+        if (turned != RLPL_OK) return turned;
+        a.x_scale = t.to;
+    }
+    return enqueue(pick_fp8_tile(out_dtype, kind), a, dim3(a.tiles_v * a.tiles_t), s.threads, stream, size_t(s.lds));
 }
 
 }  // extern "C"

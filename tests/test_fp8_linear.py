@@ -1,9 +1,12 @@
 """Products of 8-bit operands with scales, against float64, and the quantisation of those operands.
 
-Tolerances (eps = 2^-24): a block's product of 128 terms, exact in themselves, is summed in float32 by the matrix core in an
-order and with an intermediate rounding of its own, which may be towards zero: 128 * 2 eps of the terms' magnitudes; the blocks
-are scaled (3 eps) and added one after the other or in shares, and the bias: (2 * 128 + H / 128 + 8) eps sum |x w| s
-+ eps |bias|, and half a step of the output.  Quantisation is a few IEEE float32 operations: equal to torch's, bit for bit.
+Tolerances (eps = 2^-24): products of two e4m3 values are exact.  float32 outputs sum them in float32 in an order and with an
+intermediate rounding of the matrix core's own, which may be towards zero: 128 * 2 eps of a block's magnitudes.  16-bit
+outputs sum each aligned eight of them after dropping what lies below 2^-13 of the largest, so each of the other seven
+is off by 2^-13 of it at most (products of 256 * 256 and 1 * 4, 12 and 30 in one group of eight give 65536 + 0, 8 and 24;
+in two groups all of it), and the groups in float32 as above.  Blocks are scaled (3 eps) and added one after the other or in
+shares, and the bias: (2 * 128 + H / 128 + 8) eps sum |x w| s + eps |out|, with 16 bits 7 * 2^-13 sum over the groups of
+max |x w| s more, and half a step of the output.  Quantisation is a few IEEE float32 operations: equal to torch's, bit for bit.
 """
 import ctypes
 import math
@@ -28,7 +31,7 @@ def quantised(x, rows):
     top = torch.where(finite, a.abs(), 0.0).amax(dim=(1, 3))
     live = top >= 2.0 ** -118
     scale = torch.where(live, top * torch.tensor(1 / 448.0), 0.0)
-    inv = torch.where(live, 448.0 / top, 0.0)
+    inv = torch.where(live, torch.full_like(top, 448.0) / top, 0.0)   # a number over a tensor would be a reciprocal times it
     q = (a * inv[:, None, :, None])
     q = torch.where(finite, q.clamp(-448, 448), math.nan).view(r * rows, c * 128)[:R, :C]
     return q.to(torch.float8_e4m3fn), scale
@@ -45,10 +48,24 @@ def make(n, H, V, seed=0):
     return *quantised(x, 1), *quantised(w, 128), torch.randn(V, generator=g)
 
 
-def product_case(x, xs, w, ws, bias, out):
-    a, b = wide(x, xs, 1), wide(w, ws, 128)
+def dropped(a, b):
+    """7 * 2^-13 of the largest product of each aligned eight, summed over them."""
+    total = torch.zeros(a.shape[0], b.shape[0])
+    for k in range(0, a.shape[1], 8):
+        x, y = a[:, k:k + 8].abs().float(), b[:, k:k + 8].abs().float()
+        top = torch.zeros_like(total)
+        for i in range(x.shape[1]):
+            top = torch.maximum(top, x[:, i:i + 1] * y[:, i])
+        total += top
+    return 7.01 * 2.0 ** -13 * total.double()
+
+
+def product_case(x, xs, w, ws, bias, out, block_rows=128):
+    a, b = wide(x, xs, 1), wide(w, ws, block_rows)
     want = a @ b.t()
     tol = (256 + x.shape[1] / 128 + 8) * E32 * (a.abs() @ b.abs().t())
+    if out.dtype != torch.float32:
+        tol = tol + dropped(a, b)
     if bias is not None:
         want = want + bias.double()
         tol = tol + E32 * want.abs()
@@ -76,16 +93,35 @@ def test_against_float64(n, H, V):
 
 
 @gpu
+@pytest.mark.parametrize("n,H,V", [(700, 2064, 40001), (1100, 144, 12001), (1500, 400, 30011), (257, 8192, 33000)])
+def test_larger_tiles_by_some_of_their_results(n, H, V):
+    """Sizes that take the tiles of 256 and of 128, at rows and columns around the tiles' ends and some others."""
+    x, xs, w, ws, b = make(n, H, V)
+    rows = torch.tensor(sorted({r for r in (0, 1, 15, 16, 63, 64, 127, 128, 255, 256, 257, n // 2, n - 65, n - 2, n - 1) if r < n}))
+    g = torch.Generator().manual_seed(0)
+    cols = torch.unique(torch.cat([torch.arange(300), torch.arange(V - 300, V), torch.randint(0, V, (500,), generator=g)]))
+    scales = ws.repeat_interleave(128, 0)[cols]
+    for dtype in (torch.bfloat16, torch.float16, torch.float32):
+        bias = b.to(dtype)
+        out = rl.fp8_linear(x.to(DEV), xs.to(DEV), w.to(DEV), ws.to(DEV), bias.to(DEV), out_dtype=dtype).cpu()
+        pick = w.view(torch.uint8)[cols].view(torch.float8_e4m3fn)
+        product_case(x.view(torch.uint8)[rows].view(torch.float8_e4m3fn), xs[rows], pick, scales, bias[cols], out[rows][:, cols], 1)
+
+
+@gpu
 def test_small_integers_are_exact():
     """Which element meets which: products of small integers with scales of powers of two have no rounding."""
     g = torch.Generator().manual_seed(1)
-    for n, H, V in ((5, 272, 200), (300, 528, 300)):
+    for n, H, V in ((5, 272, 200), (300, 528, 300), (1100, 144, 12001), (700, 2064, 40001)):
         x, w = (torch.randint(-3, 4, s, generator=g).float() for s in ((n, H), (V, H)))
-        xs = torch.exp2(torch.randint(-3, 4, (n, -(-H // 128)), generator=g).float())
-        ws = torch.exp2(torch.randint(-3, 4, (-(-V // 128), -(-H // 128)), generator=g).float())
+        xs = torch.exp2(torch.randint(-2, 2, (n, -(-H // 128)), generator=g).float())
+        ws = torch.exp2(torch.randint(-2, 2, (-(-V // 128), -(-H // 128)), generator=g).float())
         q, p = x.to(torch.float8_e4m3fn), w.to(torch.float8_e4m3fn)
-        out = rl.fp8_linear(q.to(DEV), xs.to(DEV), p.to(DEV), ws.to(DEV), out_dtype=torch.float32)
-        assert torch.equal(out.cpu().double(), wide(q, xs, 1) @ wide(p, ws, 128).t())
+        d = [t.to(DEV) for t in (q, xs, p, ws)]
+        want = wide(d[0], d[1], 1) @ wide(d[2], d[3], 128).t()
+        assert torch.equal(rl.fp8_linear(*d, out_dtype=torch.float32).double(), want)
+        for dtype in (torch.bfloat16, torch.float16):      # |sums| stay in fp16's range; one rounding
+            assert torch.equal(rl.fp8_linear(*d, out_dtype=dtype), want.to(dtype))
 
 
 @gpu

@@ -597,8 +597,8 @@ int rlpl_grad_scale(void* const* grads, const int64_t* sizes, const int32_t* dty
  * workspace   : token_logprobs_workspace_bytes(rows, vocab, top_k) bytes, 256-byte aligned, no initial contents needed;
  *               one call in flight per workspace
  *
- * 1 <= rows < 2^31, 1 <= vocab <= 2^31 - 65536, 0 <= top_k <= min(64, vocab), 1 <= inner <= rows, strides >= 0;
- * T finite and above 0.
+ * 1 <= rows < 2^31, 1 <= vocab <= 2^31 - 65536 (2^22 with top_k > 0), 0 <= top_k <= min(64, vocab), 1 <= inner <= rows,
+ * strides >= 0; T finite and above 0.
  */
 size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top_k);
 

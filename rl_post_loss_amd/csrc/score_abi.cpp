@@ -18,6 +18,7 @@ using namespace rlpl;
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
 constexpr int64_t kMaxVocab = (int64_t(1) << 31) - 65536;   // columns are counted in 32 bits, a step of lanes past the end
+constexpr int64_t kMaxTopVocab = int64_t(1) << 22;          // 32 pieces of 131,072 with 64 alternatives
 constexpr int64_t kMaxElements = int64_t(1) << 62;
 
 // The tiles' ring is beyond the default limit of LDS.
@@ -40,8 +41,8 @@ unsigned capped(int64_t grid, int64_t cap) { return unsigned(grid < cap ? grid :
 // ----------------------------------------------------------------------------- token log-probabilities
 
 bool token_shape_ok(int64_t rows, int64_t vocab, int64_t top_k) {
-    return rows >= 1 && rows < kMaxRows && vocab >= 1 && vocab <= kMaxVocab && top_k >= 0 && top_k <= kTokenMaxTop &&
-           top_k <= vocab;
+    return rows >= 1 && rows < kMaxRows && vocab >= 1 && vocab <= (top_k > 0 ? kMaxTopVocab : kMaxVocab) && top_k >= 0 &&
+           top_k <= kTokenMaxTop && top_k <= vocab;
 }
 // Rows r at group_stride (r / inner) + row_stride (r % inner), all of them within 2^62 elements.
 bool token_strides_ok(int64_t rows, int64_t inner, int64_t group_stride, int64_t row_stride) {
@@ -49,11 +50,12 @@ bool token_strides_ok(int64_t rows, int64_t inner, int64_t group_stride, int64_t
     const __int128 last = __int128((rows - 1) / inner) * group_stride + __int128(inner - 1) * row_stride;
     return last < kMaxElements;
 }
-int64_t token_vectors(int64_t vocab, int dtype) { return vocab / (16 / int64_t(dtype_bytes(dtype))); }
+int token_vector(int dtype) { return 16 / int(dtype_bytes(dtype)); }
+int64_t token_vectors(int64_t vocab, int dtype) { return vocab / token_vector(dtype); }
 
 // The pieces depend on the elements' size through their vectors: workspaces are sized for the most of them.
 size_t token_bytes(int64_t rows, int64_t vocab, int64_t top_k) {
-    const int64_t pieces = token_fwd_pieces(rows, token_vectors(vocab, RLPL_F32), int(top_k));
+    const int64_t pieces = token_fwd_pieces(rows, token_vectors(vocab, RLPL_F32), token_vector(RLPL_F32), int(top_k));
     if (pieces == 1) return 256;
     return up256(size_t(rows) * size_t(pieces) * sizeof(TokenPart)) +
            up256(size_t(rows) * size_t(pieces) * size_t(top_k) * sizeof(uint64_t));
@@ -135,7 +137,7 @@ int token_logprobs_fwd(const void* logits, const int64_t* targets, const void* m
     a.entropy = entropy_out;
     a.top_logp = top_logp_out;
     a.top_index = top_index_out;
-    a.pieces = int32_t(token_fwd_pieces(rows, vectors, int(top_k)));
+    a.pieces = int32_t(token_fwd_pieces(rows, vectors, token_vector(dtype), int(top_k)));
     a.piece_vectors = div_up(vectors > 0 ? vectors : 1, a.pieces);
     a.top_k = int32_t(top_k);
     a.scale = float(1.4426950408889634 / double(temperature));

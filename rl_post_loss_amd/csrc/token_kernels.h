@@ -12,6 +12,7 @@ constexpr int kTokenThreads = 256;
 constexpr int kTokenMaxTop = 64;           // alternatives a row can give: no more than a wavefront's lanes
 constexpr int kTokenMaxPieces = 64;        // pieces of a row
 constexpr int kTokenMaxKeys = 2048;        // pieces times alternatives
+constexpr int kTokenBlocks = 16;           // blocks of 32 elements that a lane has of a piece with alternatives, at most
 constexpr int64_t kTokenMaxGrid = 1 << 20; // workgroups of a launch (they stride over the rest)
 
 // Where the rows lie: row r at group_stride (r / inner) + row_stride (r % inner) elements.
@@ -56,13 +57,18 @@ struct TokenBwdArgs {
 };
 
 // Pieces a row is cut into by the forward, so that few rows still fill the chip: 1024 workgroups in all, each with a
-// vector for every lane at least.
-inline int64_t token_fwd_pieces(int64_t rows, int64_t vectors, int top_k) {
+// vector for every lane at least; with alternatives pieces of 131,072 elements at most (32 of them take 2^22 elements).
+inline int64_t token_fwd_pieces(int64_t rows, int64_t vectors, int vector, int top_k) {
     const int64_t most = (vectors + kTokenThreads - 1) / kTokenThreads;
     int64_t p = 1024 / rows;
     if (p > most) p = most;
     if (p > kTokenMaxPieces) p = kTokenMaxPieces;
-    if (p * top_k > kTokenMaxKeys) p = kTokenMaxKeys / top_k;
+    if (top_k > 0) {
+        if (p > kTokenMaxKeys / top_k) p = kTokenMaxKeys / top_k;
+        const int64_t room = int64_t(kTokenBlocks) * 32 / vector * kTokenThreads;   // vectors
+        const int64_t least = (vectors + room - 1) / room;
+        if (p < least) p = least;
+    }
     return p < 1 ? 1 : p;
 }
 

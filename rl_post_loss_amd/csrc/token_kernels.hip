@@ -13,12 +13,14 @@
 // held at -1000, which 2^x takes to zero, by a maximum that lets NaN through).
 //
 // The k largest elements, the lowest index first among equal ones, come from
-// the same pass without a list in its loop: each lane knows the block of
-// its own largest element.  The k-th of the lanes' largest is a bound that k
-// elements reach, so the row's k largest all do, and they lie in the k lanes
-// whose largest reach it: those lanes' elements (k / 256 of the row) are read
-// a second time, the ones that reach the bound collected and ranked.  The work
-// does not depend on the order of the logits.
+// the same pass without a list in its loop: each lane leaves the largest of
+// every 32 of its elements in LDS.  The k-th of the largest of groups of lanes is a
+// bound that k elements reach, so the row's k largest all do, and they lie in
+// blocks of 32 whose own largest reaches it, little more than k of them: those are read a
+// second time, their elements that reach the bound collected and ranked.  Where
+// equal logits or their order make that many blocks or elements, the bound is
+// taken by (logit, index), which no two elements share, and from the lanes that reach it,
+// in steps if need be.
 //
 // The loop takes about ten vector operations an element (2^x counts four).
 #include <hip/hip_runtime.h>
@@ -141,22 +143,77 @@ __device__ __forceinline__ void write_top(const TokenFwdArgs& a, int64_t row, in
 // How many of n keys in LDS are larger than `mine`.
 __device__ __forceinline__ int rank_of(uint64_t mine, const uint64_t* keys, int n) {
     int rank = 0;
+#pragma unroll 8
     for (int i = 0; i < n; ++i) rank += keys[i] > mine ? 1 : 0;
     return rank;
 }
+// The larger of two lanes' keys.
+template <int CTRL>
+__device__ __forceinline__ uint64_t larger_of(uint64_t key) {
+    const uint64_t other = uint64_t(dpp_move<CTRL>(uint32_t(key >> 32))) << 32 | dpp_move<CTRL>(uint32_t(key));
+    return other > key ? other : key;
+}
+// The k-th largest of 64 G keys in LDS (none of them equal, but for zeros), or 1 where fewer than k are not zero; in every
+// lane.
+template <int G>
+__device__ __forceinline__ uint64_t bound_of(const uint64_t* keys, int k) {
+    uint64_t mine[G];
+    int rank[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        mine[g] = keys[64 * g + (threadIdx.x & 63)];
+        rank[g] = 0;
+    }
+#pragma unroll 16
+    for (int i = 0; i < 64 * G; ++i) {
+        const uint64_t other = keys[i];
+#pragma unroll
+        for (int g = 0; g < G; ++g) rank[g] += other > mine[g] ? 1 : 0;
+    }
+    uint64_t bound = 1;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const uint64_t at = __ballot(mine[g] != 0 && rank[g] == k - 1);
+        if (!at) continue;
+        const int lane = int(__builtin_ctzll(at));
+        bound = uint64_t(uint32_t(__builtin_amdgcn_readlane(int(uint32_t(mine[g] >> 32)), lane))) << 32 |
+                uint32_t(__builtin_amdgcn_readlane(int(uint32_t(mine[g])), lane));
+    }
+    return bound;
+}
+// The lanes' largest keys to LDS: the quads', where there are twice as many of them as alternatives (so that the k-th of
+// them is near the k-th of all), else every lane's.
+__device__ __forceinline__ bool by_quads(int32_t vectors, int k) { return min(vectors, int32_t(kTokenThreads)) >= 8 * k; }
+__device__ __forceinline__ void leave_heads(uint64_t* heads, uint64_t key, int32_t vectors, int k) {
+    const uint64_t quad = larger_of<0x4E>(larger_of<0xB1>(key));
+    if (!by_quads(vectors, k)) heads[threadIdx.x] = key;
+    else if ((threadIdx.x & 3) == 0) heads[threadIdx.x >> 2] = quad;
+}
+// After the workgroup's barrier, the k-th of those; `found` is a word of LDS that holds 1.
+__device__ __forceinline__ uint64_t bound_of_heads(const uint64_t* heads, int32_t vectors, int k, uint64_t* found) {
+    if (by_quads(vectors, k)) return bound_of<1>(heads, k);
+    const int n = min(vectors, int32_t(kTokenThreads));        // the lanes that have elements are the first ones
+    const uint64_t mine = heads[threadIdx.x];
+    if (mine != 0 && rank_of(mine, heads, n) == k - 1) *found = mine;
+    __syncthreads();
+    return *found;
+}
 
-constexpr int kTokenKeep = 192;            // candidates past which a step's are cut to the k largest
-template <typename T> constexpr int kTokenStep = kTokenThreads * kVec16<T>;   // a step adds so many at most
+constexpr int kTokenFound = 1024;          // candidates that there is room for
+constexpr int kTokenList = 256;            // blocks, and lanes, likewise
+static_assert(kTokenList >= kTokenThreads, "every lane may be listed");
 
 // One workgroup a row, or a piece of it.
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a) {
     constexpr int V = kVec16<T>, U = 32 / V;                   // 32 elements a lane at a time
     __shared__ Sums joined[kTokenWaves];
-    __shared__ uint64_t found[TOP ? kTokenKeep + kTokenStep<T> : 1];
-    __shared__ uint64_t kept[TOP ? kTokenMaxTop : 1];
-    __shared__ int lanes[TOP ? kTokenMaxTop : 1];
-    __shared__ int count;
+    __shared__ __attribute__((aligned(16))) uint64_t found[TOP ? kTokenFound : 2];
+    __shared__ __attribute__((aligned(16))) uint64_t heads[TOP ? kTokenThreads : 2];
+    __shared__ float tops[TOP ? kTokenBlocks : 1][TOP ? kTokenThreads : 1];
+    __shared__ int listed[TOP ? kTokenList : 1];
+    __shared__ uint64_t bounds[2];
+    __shared__ int count, some;
     const int tid = threadIdx.x;
     const float c = a.scale;
     for (int64_t item = blockIdx.x; item < a.in.rows * a.pieces; item += gridDim.x) {
@@ -170,8 +227,8 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
         const int32_t first = int32_t(piece * a.piece_vectors) < r.vectors ? int32_t(piece * a.piece_vectors) : r.vectors;
         const int32_t last = piece == a.pieces - 1 || r.vectors - first < a.piece_vectors ? r.vectors : first + int32_t(a.piece_vectors);
         Sums mine = Sums::none();
-        int32_t at = first + tid;          // the first vector of the block with the lane's largest element
-        const auto block = [&](const u32x4 (&raw)[U], int live, int32_t i) {
+        int blocks = 0;                    // the lane's, of U vectors each
+        const auto block = [&](const u32x4 (&raw)[U], int live) {
             float z[U][V];
             float top = -__builtin_inff();
 #pragma unroll
@@ -183,10 +240,9 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
                     top = fmaxf(top, z[u][k]);
                 }
             }
-            if (top > mine.top) {
-                mine.rise(top, c);
-                at = i;
-            }
+            if constexpr (TOP) tops[blocks][tid] = top;
+            ++blocks;
+            if (top > mine.top) mine.rise(top, c);
             const float bc = c * base_of(mine.top);
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -198,7 +254,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
             u32x4 raw[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) raw[u] = r.vector(i + u * kTokenThreads);
-            block(raw, U, i);
+            block(raw, U);
         }
         if (i < last) {
             u32x4 raw[U];
@@ -211,7 +267,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
                     live = u + 1;
                 }
             }
-            block(raw, live, i);
+            block(raw, live);
         }
         Sums all = mine;
         if (piece == 0 && tid < r.edges()) {                   // at most 2 (V - 1) elements outside the vectors
@@ -226,27 +282,11 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
         all.t = wave_sum(all.t);
         __syncthreads();                   // the last row's LDS may still be read
         if ((tid & 63) == 0) joined[tid >> 6] = all;
-        if (tid == 0) count = 0;
-        uint64_t best = 0;
-        if constexpr (TOP) {
-            if (tid < kTokenMaxTop) {      // places that no lane of a row of NaN fills
-                lanes[tid] = tid;
-                kept[tid] = 1;
-            }
-            if (first + tid < last) {
-                // the lane's largest element's first place
-#pragma unroll
-                for (int u = U - 1; u >= 0; --u) {
-                    if (at + u * kTokenThreads >= last) continue;
-                    float z[V];
-                    widen_raw<T>(r.vector(at + u * kTokenThreads), z);
-#pragma unroll
-                    for (int k = V - 1; k >= 0; --k)
-                        if (z[k] == mine.top) best = key_of(z[k], r.head + (at + u * kTokenThreads) * V + k);
-                }
-            }
-            found[tid] = best;
+        if (tid == 0) {
+            count = some = 0;
+            if constexpr (TOP) bounds[0] = bounds[1] = 1;
         }
+        if constexpr (TOP) leave_heads(heads, blocks > 0 ? key_of(mine.top, uint32_t(tid)) : 0, last - first, a.top_k);
         __syncthreads();
         all = joined[0];
 #pragma unroll
@@ -264,50 +304,87 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
             else a.part[item] = TokenPart{all.top, all.s, all.t, 0.0f};
         }
         if constexpr (TOP) {
-            const int rank = rank_of(best, found, kTokenThreads);
-            if (rank < a.top_k && best) {
-                lanes[rank] = tid;
-                kept[rank] = best;
-            }
-            const int some = last - first < a.top_k ? int(last - first) : a.top_k;     // lanes that have elements
-            __syncthreads();
-            // k lanes' largest reach this bound; with fewer lanes every element is taken
-            uint64_t bound = some == a.top_k ? kept[a.top_k - 1] : 1;
-            const int32_t each = (last - first + kTokenThreads - 1) / kTokenThreads;
-            const int32_t all_vectors = some * each;
-            int n = 0;
+            uint64_t bound = bound_of_heads(heads, last - first, a.top_k, &bounds[0]);
             const auto take = [&](float z, uint32_t index) {
                 const uint64_t key = key_of(z, index);
-                if (key >= bound) found[atomicAdd(&count, 1)] = key;
+                if (key < bound) return;
+                const int place = atomicAdd(&count, 1);
+                if (place < kTokenFound) found[place] = key;
             };
-            if (piece == 0 && tid < r.edges()) take(widen(r.p[r.edge(tid)]), uint32_t(r.edge(tid)));
-            for (int32_t v0 = 0; v0 < all_vectors; v0 += kTokenThreads) {
-                const int32_t v = v0 + tid;
-                const int32_t i = v < all_vectors ? first + lanes[v / each] + v % each * kTokenThreads : last;
-                if (i < last) {
-                    float z[V];
-                    widen_raw<T>(r.vector(i), z);
+            const auto take_vector = [&](int32_t i) {
+                float z[V];
+                widen_raw<T>(r.vector(i), z);
 #pragma unroll
-                    for (int k = 0; k < V; ++k) take(z[k], uint32_t(r.head + i * V + k));
+                for (int k = 0; k < V; ++k) take(z[k], uint32_t(r.head + i * V + k));
+            };
+            const auto take_edges = [&]() {
+                if (piece == 0 && tid < r.edges()) take(widen(r.p[r.edge(tid)]), uint32_t(r.edge(tid)));
+            };
+            if (bound > 1) bound &= 0xFFFFFFFF00000000ull;     // any index
+            const float least = key_logit(bound);
+            for (int b = 0; b < blocks; ++b)
+                if (bound == 1 || tops[b][tid] >= least) {
+                    const int place = atomicAdd(&some, 1);
+                    if (place < kTokenList) listed[place] = first + tid + b * (U * kTokenThreads);
                 }
-                __syncthreads();
-                n = count;
-                __syncthreads();           // every lane has read it
-                if (n > kTokenKeep) {                          // uniform: cut to the k largest
-                    for (int j = tid; j < n; j += kTokenThreads) {
-                        const uint64_t key = found[j];
-                        const int rank = rank_of(key, found, n);
-                        if (rank < a.top_k) kept[rank] = key;
-                    }
-                    __syncthreads();
-                    if (tid < a.top_k) found[tid] = kept[tid];
-                    if (tid == 0) count = a.top_k;
-                    bound = kept[a.top_k - 1];
-                    __syncthreads();
+            take_edges();
+            __syncthreads();
+            if (some <= kTokenList) {
+                for (int j = tid; j < some * U; j += kTokenThreads) {
+                    const int32_t i = listed[j / U] + j % U * kTokenThreads;
+                    if (i < last) take_vector(i);
                 }
             }
             __syncthreads();
-            n = count;
+            if (some > kTokenList || count > kTokenFound) {    // uniform
+                uint64_t best = 0;         // the lane's largest element at its first place
+                for (int b = blocks - 1; b >= 0; --b)
+                    if (tops[b][tid] == mine.top)
+                        for (int u = U - 1; u >= 0; --u) {
+                            const int32_t i = first + tid + (b * U + u) * kTokenThreads;
+                            if (i >= last) continue;
+                            float z[V];
+                            widen_raw<T>(r.vector(i), z);
+#pragma unroll
+                            for (int k = V - 1; k >= 0; --k)
+                                if (z[k] == mine.top) best = key_of(z[k], uint32_t(r.head + i * V + k));
+                        }
+                __syncthreads();
+                leave_heads(heads, best, last - first, a.top_k);
+                if (tid == 0) count = some = 0;
+                __syncthreads();
+                bound = bound_of_heads(heads, last - first, a.top_k, &bounds[1]);
+                if (best >= bound) listed[atomicAdd(&some, 1)] = tid;
+                take_edges();
+                __syncthreads();
+                const int32_t each = (last - first + kTokenThreads - 1) / kTokenThreads, all_vectors = some * each;
+                constexpr int32_t kStep = (kTokenFound - kTokenMaxTop - 2 * V) / V;
+                for (int32_t from = 0; from < all_vectors; from += kStep) {
+                    const int32_t to = from + kStep < all_vectors ? from + kStep : all_vectors;
+                    for (int32_t v = from + tid; v < to; v += kTokenThreads) {
+                        const int32_t i = first + listed[v / each] + v % each * kTokenThreads;
+                        if (i < last) take_vector(i);
+                    }
+                    __syncthreads();
+                    const int n = count;
+                    uint64_t held[kTokenFound / kTokenThreads];
+                    int rank[kTokenFound / kTokenThreads];
+#pragma unroll
+                    for (int q = 0; q < kTokenFound / kTokenThreads; ++q) {
+                        const int j = q * kTokenThreads + tid;
+                        held[q] = j < n ? found[j] : 0;
+                        rank[q] = j < n ? rank_of(held[q], found, n) : kTokenFound;
+                    }
+                    __syncthreads();       // every lane has read them
+#pragma unroll
+                    for (int q = 0; q < kTokenFound / kTokenThreads; ++q)
+                        if (rank[q] < a.top_k) found[rank[q]] = held[q];
+                    if (tid == 0 && n > a.top_k) count = a.top_k;
+                    __syncthreads();
+                    if (n >= a.top_k) bound = found[a.top_k - 1];
+                }
+            }
+            const int n = count;
             for (int j = tid; j < n || j < a.top_k; j += kTokenThreads) {
                 // a piece of fewer than k elements gives keys of 0 past them
                 const uint64_t key = j < n ? found[j] : 0;
@@ -317,55 +394,44 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
                 else a.part_top[item * a.top_k + rank] = key;
             }
         }
-        __syncthreads();
     }
 }
 
-// A row's pieces joined: the sums in piece order, and the k largest of the pieces' k largest by the rule of the lanes.
+// A row's pieces joined: the sums in piece order, and the k largest of the pieces' k largest likewise.
 template <typename T>
 __global__ void __launch_bounds__(kTokenThreads) token_join(const TokenFwdArgs a) {
-    __shared__ Sums sums[kTokenMaxPieces];
-    __shared__ uint64_t keys[kTokenMaxKeys], found[kTokenMaxKeys];
-    __shared__ uint64_t bound;
+    __shared__ uint64_t heads[128];
+    __shared__ uint64_t found[kTokenMaxKeys];
     __shared__ int count;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
     const float c = a.scale;
+    static_assert(kTokenMaxPieces <= 64, "a lane a piece");
     for (int64_t row = blockIdx.x; row < a.in.rows; row += gridDim.x) {
         if (a.in.mask && !a.in.mask[row]) continue;            // written by its first piece
-        __syncthreads();
-        if (tid < a.pieces) {
-            const TokenPart p = a.part[row * a.pieces + tid];
-            sums[tid] = Sums{p.top, p.sum, p.weighted};
+        const uint64_t* keys = a.part_top + row * a.pieces * a.top_k;
+        __syncthreads();                   // the last row's LDS may still be read
+        Sums all = Sums::none();           // each wavefront joins the pieces, a lane a piece
+        if (lane < a.pieces) {
+            const TokenPart p = a.part[row * a.pieces + lane];
+            all = Sums{p.top, p.sum, p.weighted};
         }
-        if (tid == 0) {
-            count = 0;
-            bound = 1;
+        if (tid < 128 && a.top_k > 0) {    // the first few keys of each piece, k of them at least
+            const int few = min(a.top_k, 128 / a.pieces), p = tid / few;
+            heads[tid] = p < a.pieces ? keys[p * a.top_k + tid % few] : 0;
         }
-        for (int i = tid; i < a.pieces * a.top_k; i += kTokenThreads) keys[i] = a.part_top[row * a.pieces * a.top_k + i];
-        __syncthreads();
-        float top = sums[0].top;
-        for (int p = 1; p < a.pieces; ++p) top = fmaxf(top, sums[p].top);
-        Sums all = sums[0];
-        all.rise(top, c);
-        for (int p = 1; p < a.pieces; ++p) {
-            Sums o = sums[p];
-            o.rise(all.top, c);
-            all.s += o.s;
-            all.t += o.t;
-        }
+        if (tid == 0) count = 0;
+        all.rise(wave_top(all.top), c);
+        all.s = wave_sum(all.s);
+        all.t = wave_sum(all.t);
         const Finish f(all, c);
         if (tid == 0) write_row(a, Row<T>(a.in, row), row, all, f);
         if (a.top_k == 0) continue;
-        // the k-th of the pieces' largest
-        if (tid < a.pieces) {
-            const uint64_t mine = keys[tid * a.top_k];
-            int rank = 0;
-            for (int p = 0; p < a.pieces; ++p) rank += keys[p * a.top_k] > mine ? 1 : 0;
-            if (rank == a.top_k - 1 && mine) bound = mine;
-        }
         __syncthreads();
-        for (int i = tid; i < a.pieces * a.top_k; i += kTokenThreads)
-            if (keys[i] >= bound) found[atomicAdd(&count, 1)] = keys[i];
+        const uint64_t bound = bound_of<2>(heads, a.top_k);
+        for (int i = tid; i < a.pieces * a.top_k; i += kTokenThreads) {
+            const uint64_t key = keys[i];
+            if (key >= bound) found[atomicAdd(&count, 1)] = key;
+        }
         __syncthreads();
         for (int j = tid; j < count; j += kTokenThreads) {
             const int rank = rank_of(found[j], found, count);

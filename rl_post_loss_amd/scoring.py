@@ -25,6 +25,8 @@ def _rows_of(z: torch.Tensor):
     copied only where its rows do not lie so."""
     V, lead = z.shape[-1], z.shape[:-1]
     rows = z.numel() // V
+    if z.is_contiguous():
+        return z, rows, rows, 0, V
     if z.stride(-1) == 1 or V == 1:
         # the leading dimensions, from the innermost outwards, those of one row left out, neighbours joined
         dims = []
@@ -69,16 +71,16 @@ def token_logprobs_fwd(logits, targets, mask=None, *, temperature=1.0, top_k=0, 
     logits (*, V) float32, float16 or bfloat16, read where they lie as long as a row's elements are side by side and the
     rows take two strides at most (``logits[:, :-1]`` is not copied); targets int64 of the leading shape; mask bool, int8
     or uint8 of it, or None: rows of a zero are not read, and give 0 (indices -1).  logp, lse and entropy are float32 of
-    the leading shape; top_logp (float32) and top_index (int64) have top_k <= 64 more columns, in falling order, the lowest
-    index first among equal logits.  A target outside [0, V) gives logp = NaN; logits of -inf have probability 0."""
+    the leading shape; top_logp (float32) and top_index (int64) have top_k <= 64 more columns (V up to 2^22 then), in falling
+    order, the lowest index first among equal logits.  A target outside [0, V) gives logp = NaN; logits of -inf have probability 0."""
     z, y, m, (rows, inner, group, stride) = _token_operands(logits, targets, mask)
     V, lead, dev, lib = z.shape[-1], z.shape[:-1], z.device, library()
     top_k = int(top_k)
     ws = _scratch(lib.token_logprobs_workspace_bytes(rows, V, top_k), workspace, dev, "token_logprobs_workspace_bytes")
     wp, wn = _ws_ptr(ws)
-    logp, lse, entropy = (torch.empty(lead, dtype=torch.float32, device=dev) for _ in range(3))
-    top_logp = torch.empty((*lead, top_k), dtype=torch.float32, device=dev) if top_k else None
-    top_index = torch.empty((*lead, top_k), dtype=torch.int64, device=dev) if top_k else None
+    logp = torch.empty_like(y, dtype=torch.float32)
+    lse, entropy = torch.empty_like(logp), torch.empty_like(logp)
+    top_logp, top_index = (logp.new_empty((*lead, top_k)), y.new_empty((*lead, top_k))) if top_k else (None, None)
     with _on(dev):
         _check("token_logprobs_fwd", lib.token_logprobs_fwd(
             z.data_ptr(), y.data_ptr(), _ptr(m), rows, V, inner, group, stride, DTYPE[z.dtype], float(temperature), top_k,

@@ -39,7 +39,7 @@ struct TurnArgs {
     int32_t rows, cols, ld;
 };
 const void* turn_kernel();
-constexpr int kTurnTile = 64;  // rows and columns of a workgroup
+constexpr int kTurnRows = 64, kTurnCols = 4;   // of a workgroup
 
 // Tiles of entries by tokens (fp8_gemm.hip).
 struct Fp8TileShape {

@@ -91,18 +91,17 @@ __global__ void __launch_bounds__(kFp8Threads) fp8_few(const Fp8LinearArgs a) {
     }
 }
 
-// A 64 x 64 tile of scales turned over, by a wavefront a row at a time.
-__global__ void __launch_bounds__(kFp8Threads) turn(const TurnArgs a) {
-    __shared__ float tile[kTurnTile][kTurnTile + 1];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t r0 = int64_t(blockIdx.x) * kTurnTile, c0 = int64_t(blockIdx.y) * kTurnTile;
-#pragma unroll 4
-    for (int i = wave; i < kTurnTile; i += kFp8Threads / 64)
-        if (r0 + i < a.rows && c0 + lane < a.cols) tile[i][lane] = a.from[(r0 + i) * a.cols + c0 + lane];
-    __syncthreads();
-#pragma unroll 4
-    for (int i = wave; i < kTurnTile; i += kFp8Threads / 64)
-        if (c0 + i < a.cols && r0 + lane < a.rows) a.to[(c0 + i) * a.ld + r0 + lane] = tile[lane][i];
+// Scales turned over: a wavefront takes four columns of 64 rows, a lane a row.
+__global__ void __launch_bounds__(64) turn(const TurnArgs a) {
+    const int64_t r = int64_t(blockIdx.x) * kTurnRows + threadIdx.x;
+    const int32_t c0 = int32_t(blockIdx.y) * kTurnCols;
+    if (r >= a.rows) return;
+    float v[kTurnCols];
+#pragma unroll
+    for (int k = 0; k < kTurnCols; ++k) v[k] = a.from[r * a.cols + (c0 + k < a.cols ? c0 + k : c0)];
+#pragma unroll
+    for (int k = 0; k < kTurnCols; ++k)
+        if (c0 + k < a.cols) a.to[int64_t(c0 + k) * a.ld + r] = v[k];
 }
 
 // A lane's piece of 8 columns: where it lies and how many are there.

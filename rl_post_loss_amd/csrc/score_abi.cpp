@@ -102,7 +102,7 @@ int fp8_few_entries(int64_t vocab) { return vocab <= 8192 ? 16 : vocab <= 24576 
 // For the large shape, the scales of the rows, one block of K after the other: a lane's tokens are then neighbours
 // (2048 x 4096 x 128256: 1113 us with the scales where they lie, a cache line a token and step; 1026 with 3 us to turn
 // them).
-int64_t fp8_scale_ld(int64_t n) { return div_up(n, kTurnTile) * kTurnTile; }
+int64_t fp8_scale_ld(int64_t n) { return div_up(n, kTurnRows) * kTurnRows; }
 size_t fp8_bytes(int64_t n, int64_t h) { return up256(size_t(fp8_scale_ld(n)) * size_t(div_up(h, kFp8Group)) * sizeof(float)); }
 
 }  // namespace
@@ -227,8 +227,8 @@ int fp8_linear(const void* x, const float* x_scale, const void* weight, const fl
     if (kind == kFp8Large) {
         a.scale_ld = int32_t(fp8_scale_ld(n));
         const TurnArgs t{x_scale, static_cast<float*>(workspace), a.n, a.blocks, a.scale_ld};
-        const int turned = enqueue(turn_kernel(), t, dim3(unsigned(div_up(n, kTurnTile)), unsigned(div_up(a.blocks, kTurnTile))),
-                                   kFp8Threads, stream);
+        const int turned = enqueue(turn_kernel(), t, dim3(unsigned(div_up(n, kTurnRows)), unsigned(div_up(a.blocks, kTurnCols))),
+                                   kTurnRows, stream);
         if (turned != RLPL_OK) return turned;
         a.x_scale = t.to;
     }

@@ -22,7 +22,11 @@
 // taken by (logit, index), which no two elements share, and from the lanes that reach it,
 // in steps if need be.
 //
-// The loop takes about ten vector operations an element (2^x counts four).
+// The loop takes about ten vector operations an element (2^x counts four), a
+// little less time than its reading: 3072 x 128256 bf16 142 to 149 us (5.3 to 5.6
+// TB/s of 0.79 GB), with 5 alternatives 147, with 20 151, with 64 163 (225 with 20, while
+// the elements of the lanes that reach the bound were read again, each vector a cache line
+// of its own).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -442,7 +446,8 @@ __global__ void __launch_bounds__(kTokenThreads) token_join(const TokenFwdArgs a
 
 // The gradient of sum(grad_logp logp + grad_entropy H): with p = exp(z / T - lse),
 //   dz_v = (grad_logp ((v == y) - p_v) - grad_entropy p_v (log p_v + H)) / T.
-// Vectors are cut where the gradient's row is aligned.
+// Vectors are cut where the gradient's row is aligned, and stored past the caches, which then hold more of the logits:
+// 3072 x 128256 bf16 296 us (5.3 TB/s) instead of 311, 4096 x 32000 79 instead of 106.
 template <typename T>
 __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a) {
     constexpr int V = kVec16<T>;
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a)
             widen_raw<T>(load_word<typename Unaligned16<T>::type, true>(x + v), z);
 #pragma unroll
             for (int k = 0; k < V; ++k) z[k] = value(z[k], v + k);
-            store_word<true>(out + v, narrow_raw<T>(z));
+            __builtin_nontemporal_store(narrow_raw<T>(z), reinterpret_cast<u32x4*>(out + v));
         }
     }
 }

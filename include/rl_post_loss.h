@@ -581,7 +581,7 @@ int rlpl_grad_scale(void* const* grads, const int64_t* sizes, const int32_t* dty
  * A row whose mask byte is zero is not read: its outputs are 0, its indices -1, its gradients +0.  A target outside
  * [0, vocab) gives logp = NaN and no one-hot term.  A logit of -inf has probability 0; a row of them
  * alone, or with a NaN or +inf, gives NaN (and indices of -1 but for the row of -inf).  One pass over the logits, sums in
- * float32 in a fixed order.
+ * float32 in a fixed order.  The gradient's p are as exact as lse, which is held in float32: off by 2^-24 |lse|.
  *
  * logits      : `dtype`, row r's vocab elements side by side from group_stride (r / inner) + row_stride (r % inner)
  *               elements on: inner = rows and row_stride = vocab for a dense (rows, vocab), group_stride =
@@ -598,7 +598,7 @@ int rlpl_grad_scale(void* const* grads, const int64_t* sizes, const int32_t* dty
  *               one call in flight per workspace
  *
  * 1 <= rows < 2^31, 1 <= vocab <= 2^31 - 65536 (2^22 with top_k > 0), 0 <= top_k <= min(64, vocab), 1 <= inner <= rows,
- * strides >= 0; T finite and above 0.
+ * strides >= 0; T finite and above 4.3e-39.
  */
 size_t token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int64_t top_k);
 

@@ -50,6 +50,8 @@ bool token_strides_ok(int64_t rows, int64_t inner, int64_t group_stride, int64_t
     const __int128 last = __int128((rows - 1) / inner) * group_stride + __int128(inner - 1) * row_stride;
     return last < kMaxElements;
 }
+// T such that log2(e) / T is a float.
+bool token_temperature_ok(float t) { return std::isfinite(t) && t > 0.0f && std::isfinite(float(1.4426950408889634 / double(t))); }
 int token_vector(int dtype) { return 16 / int(dtype_bytes(dtype)); }
 int64_t token_vectors(int64_t vocab, int dtype) { return vocab / token_vector(dtype); }
 
@@ -120,7 +122,7 @@ int token_logprobs_fwd(const void* logits, const int64_t* targets, const void* m
     if (!logits || !targets || !logp_out || !lse_out || (top_k > 0 && (!top_logp_out || !top_index_out))) return RLPL_ERR_NULL;
     if (!token_shape_ok(rows, vocab, top_k) || !token_strides_ok(rows, inner, group_stride, row_stride)) return RLPL_ERR_SHAPE;
     if (!known_dtype(dtype)) return RLPL_ERR_DTYPE;
-    if (!std::isfinite(temperature) || !(temperature > 0.0f)) return RLPL_ERR_PARAM;
+    if (!token_temperature_ok(temperature)) return RLPL_ERR_PARAM;
     if (!is_aligned(logits, dtype_bytes(dtype)) || !is_aligned(targets, 8) || !is_aligned(logp_out, 4) ||
         !is_aligned(lse_out, 4) || !is_aligned(entropy_out, 4) || !is_aligned(top_logp_out, 4) || !is_aligned(top_index_out, 8))
         return RLPL_ERR_ALIGN;
@@ -156,7 +158,7 @@ int token_logprobs_bwd(const void* logits, const int64_t* targets, const void* m
     if (!logits || !targets || !lse || !grad_logits || (grad_entropy && !entropy)) return RLPL_ERR_NULL;
     if (!token_shape_ok(rows, vocab, 0) || !token_strides_ok(rows, inner, group_stride, row_stride)) return RLPL_ERR_SHAPE;
     if (!known_dtype(dtype)) return RLPL_ERR_DTYPE;
-    if (!std::isfinite(temperature) || !(temperature > 0.0f)) return RLPL_ERR_PARAM;
+    if (!token_temperature_ok(temperature)) return RLPL_ERR_PARAM;
     const size_t e = dtype_bytes(dtype);
     if (!is_aligned(logits, e) || !is_aligned(targets, 8) || !is_aligned(lse, 4) || !is_aligned(entropy, 4) ||
         !is_aligned(grad_logp, 4) || !is_aligned(grad_entropy, 4) || !is_aligned(grad_logits, e))

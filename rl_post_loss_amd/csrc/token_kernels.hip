@@ -61,18 +61,30 @@ __device__ __forceinline__ float wave_top(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+// Exponents count from c b, rounded, as c z - c b by one operation, the same for a row's sums and its results, so that the
+// rounding falls out of them.  Where c b is so large that its rounding is not small (a row of the type's lowest value; a tiny
+// temperature) they are (z - b) c.
+struct Base {
+    float b, bc;
+    bool far;
+    __device__ __forceinline__ Base(float top, float c) : b(base_of(top)), bc(c * b), far(!(fabsf(bc) < 0x1p20f)) {}
+    __device__ __forceinline__ float exponent(float z, float c) const { return far ? (z - b) * c : fmaf(z, c, -bc); }
+};
+
 // Sums that count from `top`.
 struct Sums {
     float top, s, t;
     static __device__ __forceinline__ Sums none() { return Sums{-__builtin_inff(), 0.0f, 0.0f}; }
     // Counts from a larger maximum.
     __device__ __forceinline__ void rise(float to, float c) {
-        const float d = hold(c * (base_of(top) - base_of(to)));
-        const float f = top == -__builtin_inff() ? 0.0f : exp2_hw(d);
+        const bool none = top == -__builtin_inff();            // nothing but NaN is in the sums
+        const float d = none ? 0.0f : hold(c * (base_of(top) - base_of(to)));
+        const float f = none ? 0.0f : exp2_hw(d);
         t = fmaf(d, s, t) * f;
         s *= f;
         top = to;
     }
+    // One more term, with its exponent.
     __device__ __forceinline__ void add(float d) {
         d = hold(d);
         const float e = exp2_hw(d);
@@ -115,16 +127,19 @@ struct Row {
 
 // The row's results from its joined sums.
 struct Finish {
-    float bc, l2;              // c b, log2 s
-    __device__ __forceinline__ Finish(const Sums& a, float c) : bc(c * base_of(a.top)), l2(__log2f(a.s)) {}
-    __device__ __forceinline__ float logp(float z, float c) const { return kLn2 * (fmaf(z, c, -bc) - l2); }
+    Base base;
+    float l2;                  // log2 s
+    __device__ __forceinline__ Finish(const Sums& a, float c) : base(a.top, c), l2(__log2f(a.s)) {}
+    __device__ __forceinline__ float logp(float z, float c) const { return kLn2 * (base.exponent(z, c) - l2); }
+    // b c may be too large where b / T = ln 2 b c is not.
+    __device__ __forceinline__ float lse(float c) const { return base.far ? base.b * (c * kLn2) + kLn2 * l2 : kLn2 * (base.bc + l2); }
 };
 
 template <typename T>
 __device__ __forceinline__ void write_row(const TokenFwdArgs& a, const Row<T>& r, int64_t row, const Sums& j, const Finish& f) {
     const int64_t y = a.targets[row];
     a.logp[row] = y >= 0 && y < r.n ? f.logp(widen(r.p[y]), a.scale) : __builtin_nanf("");
-    a.lse[row] = kLn2 * (f.bc + f.l2);
+    a.lse[row] = f.lse(a.scale);
     if (a.entropy) a.entropy[row] = kLn2 * (f.l2 - j.t / j.s);
 }
 __device__ __forceinline__ void write_masked(const TokenFwdArgs& a, int64_t row) {
@@ -247,11 +262,18 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
             if constexpr (TOP) tops[blocks][tid] = top;
             ++blocks;
             if (top > mine.top) mine.rise(top, c);
-            const float bc = c * base_of(mine.top);
+            const Base base(mine.top, c);
+            if (base.far) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int k = 0; k < V; ++k) mine.add(fmaf(z[u][k], c, -bc));
+                    for (int k = 0; k < V; ++k) mine.add((z[u][k] - base.b) * c);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) mine.add(fmaf(z[u][k], c, -base.bc));
+            }
         };
         int32_t i = first + tid;
         for (; i + (U - 1) * kTokenThreads < last; i += U * kTokenThreads) {
@@ -277,7 +299,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
         if (piece == 0 && tid < r.edges()) {                   // at most 2 (V - 1) elements outside the vectors
             const float z = widen(r.p[r.edge(tid)]);
             if (z > all.top) all.rise(z, c);
-            all.add(fmaf(z, c, -c * base_of(all.top)));
+            all.add(Base(all.top, c).exponent(z, c));
         }
         // lanes to wavefronts to the workgroup
         const float top = wave_top(all.top);

@@ -166,6 +166,50 @@ def test_nan_and_infinite_logits(rows):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows", [1, 1100])
+def test_masks_of_the_types_lowest_value(rows, dtype):
+    """Rows that are all of it give a uniform distribution; beside other logits it has probability 0."""
+    V, low = 5003, torch.finfo(DT[dtype]).min
+    z, y, _ = make(rows, V, dtype, seed=6)
+    z[0] = low
+    for T in (1.0, 0.6, 3.0):
+        logp, lse, H, top, index = rl.token_logprobs_fwd(z.to(DEV), y.to(DEV), temperature=T, top_k=5)
+        uniform = math.log(V)
+        assert abs(float(logp[0]) + uniform) <= 200 * E32 * uniform and abs(float(H[0]) - uniform) <= 200 * E32 * uniform
+        assert index[0].tolist() == [0, 1, 2, 3, 4] and ((top[0] + uniform).abs() <= 200 * E32 * uniform).all()
+        want = torch.tensor(low, dtype=torch.float64) / T + uniform
+        assert abs(float(lse[0]) - want.float().item()) <= 4 * E32 * abs(want) or float(lse[0]) == want.float().item()
+    w = z.clone()
+    w[0] = z[-1] if rows > 1 else torch.randn(V).to(DT[dtype])
+    w[0, ::3] = low
+    y[0] = 1
+    for T in (1.0, 0.6):
+        out = rl.token_logprobs_fwd(w.to(DEV), y.to(DEV), temperature=T, top_k=20)
+        forward_case(w[:1], y[:1], T, [t[:1] for t in out], 20)
+        one = torch.ones(rows, device=DEV)
+        dz = rl.token_logprobs_bwd(w.to(DEV), y.to(DEV), None, out[1], out[2], one, one, temperature=T)
+        backward_case(w[:1], y[:1], T, out[1][:1].cpu(), out[2][:1].cpu(), one[:1].cpu(), one[:1].cpu(), dz[:1])
+        assert (dz[0, ::3] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("T", [1e-3, 1e-30, 1e-38, 1e3, 1e38])
+def test_extreme_temperatures(T):
+    z, y, _ = make(3, 4000, "fp32", seed=8)
+    y[0] = z[0].argmax()
+    out = rl.token_logprobs_fwd(z.to(DEV), y.to(DEV), temperature=T, top_k=3)
+    x = z.double() / torch.tensor(T, dtype=torch.float32).double()
+    l = x - torch.logsumexp(x, -1, keepdim=True)
+    want = l.gather(-1, y[:, None])[:, 0]
+    L = (torch.logsumexp(x, -1) - x.amax(-1))
+    tol = (4000 / 256 * 1.2 + 150 + 4 * L) * E32 + 8 * E32 * (want.abs() + (x.amax(-1).abs() if T > 1e-10 else 0.0))
+    fits = want.abs() < 3e38
+    assert ((out[0].cpu().double() - want).abs() <= tol)[fits].all() and out[0].cpu()[~fits].isinf().all()
+    assert torch.equal(out[4].cpu(), torch.sort(z, dim=-1, descending=True, stable=True).indices[:, :3])
+
+
+@gpu
 def test_masked_rows_are_not_read_and_targets_outside():
     z, y, _ = make(1500, 777, "bf16")
     mask = torch.arange(1500) % 3 > 0
@@ -395,7 +439,7 @@ def test_refusals_of_the_c_entries():
             assert f(V=V) == 2
         assert f(inner=0) == 2 and f(inner=5) == 2 and f(gs=-1) == 2 and f(rs=-1) == 2
         assert f(rows=4, inner=1, gs=1 << 62) == 2 and f(rs=1 << 61) == 2 and f(rows=1 << 30, inner=1 << 30, rs=1 << 40) == 2
-        assert f(dt=3) == 4 and f(T=0.0) == 5 and f(T=math.nan) == 5 and f(T=math.inf) == 5 and f(T=-1.0) == 5
+        assert f(dt=3) == 4 and f(T=1e-40) == 5 and f(T=0.0) == 5 and f(T=math.nan) == 5 and f(T=math.inf) == 5 and f(T=-1.0) == 5
         assert f(z=odd) == 3 and f(y=ctypes.c_void_p(0x7F0000000004)) == 3 and f(lse=odd) == 3 and f(H=odd) == 3
     assert fwd(top=3) == 1 and fwd(top=3, tl=P) == 1 and fwd(top=65, tl=P, ti=P) == 2 and fwd(top=-1) == 2
     assert fwd(top=101, tl=P, ti=P) == 2 and fwd(ws=None) == 6 and fwd(wn=8) == 6 and fwd(ws=ctypes.c_void_p(0x7F0000000010)) == 3

@@ -58,7 +58,7 @@ int64_t token_vectors(int64_t vocab, int dtype) { return vocab / token_vector(dt
 // The pieces depend on the elements' size through their vectors: workspaces are sized for the most of them.
 size_t token_bytes(int64_t rows, int64_t vocab, int64_t top_k) {
     const int64_t pieces = token_fwd_pieces(rows, token_vectors(vocab, RLPL_F32), token_vector(RLPL_F32), int(top_k));
-    if (pieces == 1) return 256;
+    if (pieces == 1 || vocab <= kTokenShort) return 256;
     return up256(size_t(rows) * size_t(pieces) * sizeof(TokenPart)) +
            up256(size_t(rows) * size_t(pieces) * size_t(top_k) * sizeof(uint64_t));
 }
@@ -139,14 +139,15 @@ int token_logprobs_fwd(const void* logits, const int64_t* targets, const void* m
     a.entropy = entropy_out;
     a.top_logp = top_logp_out;
     a.top_index = top_index_out;
-    a.pieces = int32_t(token_fwd_pieces(rows, vectors, token_vector(dtype), int(top_k)));
+    a.pieces = vocab <= kTokenShort ? 1 : int32_t(token_fwd_pieces(rows, vectors, token_vector(dtype), int(top_k)));
     a.piece_vectors = div_up(vectors > 0 ? vectors : 1, a.pieces);
     a.top_k = int32_t(top_k);
     a.scale = float(1.4426950408889634 / double(temperature));
     a.part = static_cast<TokenPart*>(workspace);
     a.part_top = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) +
                                              up256(size_t(rows) * size_t(a.pieces) * sizeof(TokenPart)));
-    st = enqueue(pick_token_fwd(dtype, top_k > 0), a, dim3(capped(rows * a.pieces, kTokenMaxGrid)), kTokenThreads, stream);
+    const int64_t groups = vocab <= kTokenShort ? div_up(rows, kTokenThreads / 64) : rows * a.pieces;
+    st = enqueue(pick_token_fwd(dtype, top_k > 0, vocab), a, dim3(capped(groups, kTokenMaxGrid)), kTokenThreads, stream);
     if (st != RLPL_OK || a.pieces == 1) return st;
     return enqueue(pick_token_join(dtype), a, dim3(capped(rows, kTokenMaxGrid)), kTokenThreads, stream);
 }
@@ -175,10 +176,12 @@ int token_logprobs_bwd(const void* logits, const int64_t* targets, const void* m
     a.grad_entropy = grad_entropy;
     a.grad = grad_logits;
     // pieces of 8 vectors a lane
-    a.pieces = int32_t(div_up(vectors > 0 ? vectors : 1, 8 * kTokenThreads));
+    const int lanes = vocab <= kTokenShortBwd ? 64 : kTokenThreads;
+    a.pieces = int32_t(div_up(vectors > 0 ? vectors : 1, 8 * lanes));
     a.piece_vectors = div_up(vectors > 0 ? vectors : 1, a.pieces);
     a.inv_t = float(1.0 / double(temperature));
-    return enqueue(pick_token_bwd(dtype), a, dim3(capped(rows * a.pieces, kTokenMaxGrid)), kTokenThreads, stream);
+    return enqueue(pick_token_bwd(dtype, vocab), a, dim3(capped(div_up(rows * a.pieces, kTokenThreads / lanes), kTokenMaxGrid)),
+                   kTokenThreads, stream);
 }
 
 int rlpl_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t row_stride, int dtype, int block_rows, void* q,

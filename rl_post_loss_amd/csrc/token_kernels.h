@@ -13,6 +13,11 @@ constexpr int kTokenMaxTop = 64;           // alternatives a row can give: no mo
 constexpr int kTokenMaxPieces = 64;        // pieces of a row
 constexpr int kTokenMaxKeys = 2048;        // pieces times alternatives
 constexpr int kTokenBlocks = 16;           // blocks of 32 elements that a lane has of a piece with alternatives, at most
+// Rows of up to this many elements go to a wavefront each (20480 rows of bf16, a workgroup a row in brackets: 333 elements
+// 12.5 (35.7) us and with 20 alternatives 23.6 (101), 4001 elements 35.9 (54.6) and 69 (122); backward 333 elements 11.8
+// (26.1), 2048 27 (36), 4001 59 (52)).
+constexpr int64_t kTokenShort = 4096;
+constexpr int64_t kTokenShortBwd = 2048;
 constexpr int64_t kTokenMaxGrid = 1 << 20; // workgroups of a launch (they stride over the rest)
 
 // Where the rows lie: row r at group_stride (r / inner) + row_stride (r % inner) elements.
@@ -72,8 +77,8 @@ inline int64_t token_fwd_pieces(int64_t rows, int64_t vectors, int vector, int t
     return p < 1 ? 1 : p;
 }
 
-const void* pick_token_fwd(int dtype, bool top);
+const void* pick_token_fwd(int dtype, bool top, int64_t vocab);
 const void* pick_token_join(int dtype);
-const void* pick_token_bwd(int dtype);
+const void* pick_token_bwd(int dtype, int64_t vocab);
 
 }  // namespace rlpl

@@ -23,8 +23,8 @@
 // in steps if need be.
 //
 // The loop takes about ten vector operations an element (2^x counts four), a
-// little less time than its reading: 3072 x 128256 bf16 142 to 149 us (5.3 to 5.6
-// TB/s of 0.79 GB), with 5 alternatives 147, with 20 151, with 64 163 (225 with 20, while
+// little less time than its reading: 3000 x 128256 bf16 143 us (5.4 TB/s of
+// 0.77 GB), with 5 alternatives 144, with 20 146, with 64 159 (220 with 20, while
 // the elements of the lanes that reach the bound were read again, each vector a cache line
 // of its own).
 #include <hip/hip_runtime.h>
@@ -102,6 +102,7 @@ __device__ __forceinline__ float key_logit(uint64_t key) {
     const uint32_t o = uint32_t(key >> 32);
     return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
+constexpr uint32_t kKeyOfMinusInf = 0x007FFFFFu;               // a key's upper half
 __device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~uint32_t(key); }
 
 // A row: elements [0, head) and [head + V vectors, n) one by one, those between in 16-byte vectors of V.
@@ -142,13 +143,14 @@ __device__ __forceinline__ void write_row(const TokenFwdArgs& a, const Row<T>& r
     a.lse[row] = f.lse(a.scale);
     if (a.entropy) a.entropy[row] = kLn2 * (f.l2 - j.t / j.s);
 }
+template <int LANES>
 __device__ __forceinline__ void write_masked(const TokenFwdArgs& a, int64_t row) {
-    if (threadIdx.x == 0) {
+    if (threadIdx.x % LANES == 0) {
         a.logp[row] = 0.0f;
         a.lse[row] = 0.0f;
         if (a.entropy) a.entropy[row] = 0.0f;
     }
-    for (int i = threadIdx.x; i < a.top_k; i += kTokenThreads) {
+    for (int i = threadIdx.x % LANES; i < a.top_k; i += LANES) {
         a.top_logp[row * a.top_k + i] = 0.0f;
         a.top_index[row * a.top_k + i] = -1;
     }
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
         const int64_t row = a.pieces == 1 ? item : item / a.pieces;
         const int piece = a.pieces == 1 ? 0 : int(item % a.pieces);
         if (a.in.mask && !a.in.mask[row]) {
-            if (piece == 0) write_masked(a, row);
+            if (piece == 0) write_masked<kTokenThreads>(a, row);
             continue;
         }
         const Row<T> r(a.in, row);
@@ -423,6 +425,140 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
     }
 }
 
+constexpr int kShortFound = 256;           // candidates of a wavefront that there is room for
+
+// One wavefront a row of up to 64 E elements, which stay in its registers: one maximum for all lanes, no barrier, and the
+// alternatives' elements are found again in registers.  Their bound is the k-th largest of the lanes' largest; where equal
+// logits bring more than there is room for to it, the k-th largest key itself, bit by bit.  20480 rows of 1000 bf16 take
+// 16.5 us (7 to read them), with 20 alternatives 37: a wavefront's instructions, 33 passes of a comparison and its count among
+// them.
+template <typename T, int E, bool TOP>
+__global__ void __launch_bounds__(kTokenThreads, E > 32 && sizeof(T) == 2 ? 4 : 1) token_short(const TokenFwdArgs a) {
+    constexpr int V = kVec16<T>, U = E / V;
+    __shared__ uint64_t room[kTokenWaves][TOP ? kShortFound : 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int32_t n = int32_t(a.in.vocab), vectors = n / V;
+    const float c = a.scale;
+    for (int64_t row = int64_t(blockIdx.x) * kTokenWaves + wave; row < a.in.rows; row += int64_t(gridDim.x) * kTokenWaves) {
+        if (a.in.mask && !a.in.mask[row]) {
+            write_masked<64>(a, row);
+            continue;
+        }
+        const T* p = static_cast<const T*>(a.in.logits) + (row / a.in.inner) * a.in.group_stride + (row % a.in.inner) * a.in.row_stride;
+        const int64_t y = a.targets[row];
+        // vector u of a lane is the row's vector 64 u + lane; the elements past the last vector go to the first lanes
+        u32x4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            raw[u] = u32x4{0, 0, 0, 0};
+            if (64 * u + lane < vectors) raw[u] = load_word<typename Unaligned16<T>::type, true>(p + (64 * u + lane) * V);
+        }
+        const bool has_last = vectors * V + lane < n;
+        const float last = has_last ? widen(p[vectors * V + lane]) : -__builtin_inff();
+        const float zy = lane == 0 && y >= 0 && y < n ? widen(p[y]) : __builtin_nanf("");
+        float z[U][V], mine = last == last ? last : -__builtin_inff();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            widen_raw<T>(raw[u], z[u]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                if (64 * u + lane >= vectors) z[u][k] = -__builtin_inff();
+                mine = fmaxf(mine, z[u][k]);
+            }
+        }
+        Sums all{wave_top(mine), 0.0f, 0.0f};
+        const Base base(all.top, c);
+        all.add(base.exponent(last, c));
+        if (base.far) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < V; ++k) all.add((z[u][k] - base.b) * c);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int k = 0; k < V; ++k) all.add(fmaf(z[u][k], c, -base.bc));
+        }
+        all.s = wave_sum(all.s);
+        all.t = wave_sum(all.t);
+        const Finish f(all, c);
+        if (lane == 0) {
+            a.logp[row] = f.logp(zy, c);
+            a.lse[row] = f.lse(c);
+            if (a.entropy) a.entropy[row] = kLn2 * (f.l2 - all.t / all.s);
+        }
+        if constexpr (TOP) {
+            if (!(f.l2 < __builtin_inff())) {                  // a NaN or +inf among the logits
+                if (lane < a.top_k) write_top(a, row, lane, 0, f);
+                continue;
+            }
+            // Calls f(logit, index, whether it is one of the row's) for the lane's elements, one after the other.
+            const auto each = [&](auto&& f) {
+                int at = lane;             // anew, so that no pass keeps all its indexes for the next
+                asm volatile("" : "+v"(at));
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) f(z[u][k], (64 * u + at) * V + k, 64 * u + at < vectors);
+                f(last, vectors * V + at, vectors * V + at < n);
+            };
+            const auto how_many = [&](auto&& which) {
+                int m = 0;
+                each([&](float z, int index, bool live) { m += int(__popcll(__ballot(live && which(z, index)))); });
+                return m;
+            };
+            uint64_t* found = room[wave];
+            int count = 0;
+            const auto collect = [&](auto&& which) {
+                each([&](float z, int index, bool live) {
+                    const bool take = live && which(z, index);
+                    const uint64_t those = __ballot(take);
+                    if (!those) return;
+                    const int place = count + int(__builtin_amdgcn_mbcnt_hi(uint32_t(those >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(those), 0)));
+                    if (take && place < kShortFound) found[place] = key_of(z, uint32_t(index));
+                    count += int(__popcll(those));
+                });
+            };
+            float bound = all.top;
+            if (a.top_k > 1) {
+                int larger = 0;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) larger += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mine), i)) > mine ? 1 : 0;
+                bound = -wave_top(larger < a.top_k ? -mine : -__builtin_inff());
+            }
+            collect([&](float z, int) { return z >= bound; });
+            if (count > kShortFound) {     // uniform
+                // the k-th largest logit by the bits of its key, then the smallest index that leaves k of them
+                uint32_t key = 0;
+#pragma unroll 1
+                for (int b = 31; b >= 0; --b) {
+                    const uint32_t trial = key | 1u << b;
+                    const float least = key_logit(uint64_t(trial) << 32);      // NaN below -inf
+                    if (trial <= kKeyOfMinusInf || how_many([&](float z, int) { return z >= least; }) >= a.top_k) key = trial;
+                }
+                const float least = key_logit(uint64_t(key) << 32);
+                int behind = 0;
+#pragma unroll 1
+                for (int b = 12; b >= 0; --b) {
+                    const int trial = behind | ((1 << b) - 1);
+                    if (how_many([&](float z, int index) { return z > least || (z == least && index <= trial); }) < a.top_k) behind |= 1 << b;
+                }
+                count = 0;
+                collect([&](float z, int index) { return z > least || (z == least && index <= behind); });
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            for (int j = lane; j < count; j += 64) {
+                const int rank = rank_of(found[j], found, count);
+                if (rank < a.top_k) write_top(a, row, rank, found[j], f);
+            }
+            __builtin_amdgcn_wave_barrier();                   // the next row writes there
+        }
+    }
+}
+
 // A row's pieces joined: the sums in piece order, and the k largest of the pieces' k largest likewise.
 template <typename T>
 __global__ void __launch_bounds__(kTokenThreads) token_join(const TokenFwdArgs a) {
@@ -469,12 +605,12 @@ __global__ void __launch_bounds__(kTokenThreads) token_join(const TokenFwdArgs a
 // The gradient of sum(grad_logp logp + grad_entropy H): with p = exp(z / T - lse),
 //   dz_v = (grad_logp ((v == y) - p_v) - grad_entropy p_v (log p_v + H)) / T.
 // Vectors are cut where the gradient's row is aligned, and stored past the caches, which then hold more of the logits:
-// 3072 x 128256 bf16 296 us (5.3 TB/s) instead of 311, 4096 x 32000 79 instead of 106.
-template <typename T>
+// 3000 x 128256 bf16 287 us (5.4 TB/s) instead of 303, 4096 x 32000 79 instead of 106.
+template <typename T, int LANES>
 __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a) {
-    constexpr int V = kVec16<T>;
-    const int tid = threadIdx.x;
-    for (int64_t item = blockIdx.x; item < a.in.rows * a.pieces; item += gridDim.x) {
+    constexpr int V = kVec16<T>, ITEMS = kTokenThreads / LANES;
+    const int tid = threadIdx.x % LANES, which = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / LANES);
+    for (int64_t item = int64_t(blockIdx.x) * ITEMS + which; item < a.in.rows * a.pieces; item += int64_t(gridDim.x) * ITEMS) {
         const int64_t row = a.pieces == 1 ? item : item / a.pieces;
         const int piece = a.pieces == 1 ? 0 : int(item % a.pieces);
         const int32_t n = int32_t(a.in.vocab);
@@ -488,7 +624,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a)
         const int32_t edge = tid < head ? tid : tid + vectors * V;
         if (a.in.mask && !a.in.mask[row]) {
             if (piece == 0 && tid < edges) out[edge] = T(0.0f);
-            for (int32_t i = first + tid; i < last; i += kTokenThreads)
+            for (int32_t i = first + tid; i < last; i += LANES)
                 store_word<true>(out + head + int64_t(i) * V, u32x4{0, 0, 0, 0});
             continue;
         }
@@ -504,7 +640,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a)
         };
         if (piece == 0 && tid < edges) out[edge] = T(value(widen(x[edge]), edge));
 #pragma unroll 4
-        for (int32_t i = first + tid; i < last; i += kTokenThreads) {
+        for (int32_t i = first + tid; i < last; i += LANES) {
             const int32_t v = head + i * V;
             float z[V];
             widen_raw<T>(load_word<typename Unaligned16<T>::type, true>(x + v), z);
@@ -515,19 +651,26 @@ __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a)
     }
 }
 
-template <bool TOP>
-const void* fwd_of(int dtype) {
-    switch (dtype) {
-    case kF32: return reinterpret_cast<const void*>(&token_fwd<float, TOP>);
-    case kF16: return reinterpret_cast<const void*>(&token_fwd<_Float16, TOP>);
-    case kBF16: return reinterpret_cast<const void*>(&token_fwd<__bf16, TOP>);
-    }
-    return nullptr;
+template <typename T, bool TOP>
+const void* fwd_of(int64_t vocab) {
+    if (vocab <= 512) return reinterpret_cast<const void*>(&token_short<T, 8, TOP>);
+    if (vocab <= 2048) return reinterpret_cast<const void*>(&token_short<T, 32, TOP>);
+    if (vocab <= kTokenShort) return reinterpret_cast<const void*>(&token_short<T, 64, TOP>);
+    return reinterpret_cast<const void*>(&token_fwd<T, TOP>);
 }
+template <typename T>
+const void* fwd_of(bool top, int64_t vocab) { return top ? fwd_of<T, true>(vocab) : fwd_of<T, false>(vocab); }
 
 }  // namespace
 
-const void* pick_token_fwd(int dtype, bool top) { return top ? fwd_of<true>(dtype) : fwd_of<false>(dtype); }
+const void* pick_token_fwd(int dtype, bool top, int64_t vocab) {
+    switch (dtype) {
+    case kF32: return fwd_of<float>(top, vocab);
+    case kF16: return fwd_of<_Float16>(top, vocab);
+    case kBF16: return fwd_of<__bf16>(top, vocab);
+    }
+    return nullptr;
+}
 const void* pick_token_join(int dtype) {
     switch (dtype) {
     case kF32: return reinterpret_cast<const void*>(&token_join<float>);
@@ -536,11 +679,15 @@ const void* pick_token_join(int dtype) {
     }
     return nullptr;
 }
-const void* pick_token_bwd(int dtype) {
+template <typename T>
+const void* bwd_of(int64_t vocab) {
+    return vocab <= kTokenShortBwd ? reinterpret_cast<const void*>(&token_bwd<T, 64>) : reinterpret_cast<const void*>(&token_bwd<T, kTokenThreads>);
+}
+const void* pick_token_bwd(int dtype, int64_t vocab) {
     switch (dtype) {
-    case kF32: return reinterpret_cast<const void*>(&token_bwd<float>);
-    case kF16: return reinterpret_cast<const void*>(&token_bwd<_Float16>);
-    case kBF16: return reinterpret_cast<const void*>(&token_bwd<__bf16>);
+    case kF32: return bwd_of<float>(vocab);
+    case kF16: return bwd_of<_Float16>(vocab);
+    case kBF16: return bwd_of<__bf16>(vocab);
     }
     return nullptr;
 }

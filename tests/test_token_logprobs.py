@@ -141,6 +141,30 @@ def test_patterns_of_logits(V, dtype, copies):
 
 
 @gpu
+@pytest.mark.parametrize("V", [64, 511, 512, 513, 2047, 2048, 2049, 4096, 4097])
+def test_equal_logits_of_short_rows(V):
+    """More elements reach the bound than there is room for; of equal ones the first are the alternatives."""
+    z = torch.zeros(8, V, dtype=torch.bfloat16)
+    z[1] = -1.5
+    z[2, ::2] = -0.0                                           # equal to 0
+    z[3] = -math.inf
+    z[3, V // 2:V // 2 + 3] = 2.0
+    z[4, :V - 40] = -math.inf
+    z[5] = torch.arange(V) % 2
+    z[6] = torch.finfo(torch.bfloat16).min
+    z[6, -1] = 0.0
+    z[7] = torch.arange(V).flip(0) // 50
+    k = 64
+    order = torch.sort(z.float(), dim=-1, descending=True, stable=True).indices[:, :k]
+    for at in (0, 1):                                          # rows that start between two vectors likewise
+        y = torch.zeros(8, dtype=torch.int64)
+        buffer = torch.zeros(8, V + 5, dtype=torch.bfloat16, device=DEV)
+        buffer[:, at:at + V] = z.to(DEV)
+        index = rl.token_logprobs_fwd(buffer[:, at:at + V], y.to(DEV), top_k=k)[4]
+        assert torch.equal(index.cpu(), order), [i for i in range(8) if not torch.equal(index[i].cpu(), order[i])]
+
+
+@gpu
 @pytest.mark.parametrize("rows", [1, 1200])
 def test_nan_and_infinite_logits(rows):
     V = 5000

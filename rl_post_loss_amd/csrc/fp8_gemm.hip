@@ -13,14 +13,17 @@
 // A lane of a fragment takes 16-byte pieces q and q + 4 of a row's 128 bytes
 // (q = lane / 16) in both operands: which of K's elements meet is all that counts.
 //
-// Three shapes (score_abi.cpp chooses by a time model).  256 x 256, the loop of
+// Four shapes (score_abi.cpp chooses by a time model).  256 x 256, the loop of
 // the cross entropy's large tile: 1.03 ms for 2048 x 4096 x 128256 (2.1 PFLOP/s), 0.47
 // for 8192^3 (2.3; the library's product with one scale for each operand 0.98 and
 // 0.38 ms).  A step has 2048 cycles of matrix instructions (1.47 us alone, 1.7 to
-// 2.05 with its share of a tile's ends).  64 x 64 and 128 x 128, two stages, five and two
+// 2.05 with its share of a tile's ends).  64 x 64 and 128 x 128, five and two
 // workgroups a compute unit, for fewer results: 333 x 2048 x 5003 8 us, 2048 x 4096
-// x 4096 48 us (1.4 PFLOP/s).  Four stages instead of two changed nothing (128 x 4096
-// x 4096: 19 us with both; a step of a workgroup alone is bound by its instructions).
+// x 4096 46 us (1.5 PFLOP/s).  The projection's ring has a third stage at 128 x 128, where
+// it comes from memory: 128 x 4096 x 128256 136 us instead of 149 (4 TB/s).  64 x 64 with K
+// shared by four groups of wavefronts, for tiles too few to fill the chip: a step of a workgroup
+// alone is bound by its instructions, not by its copies (more stages change nothing), and four
+// groups take 1.1 us for four steps of 0.6.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -38,16 +41,17 @@ namespace rlpl {
 
 namespace {
 
-// Entries (M) by tokens (N), wavefronts along each, slots of the ring.
-template <int BM_, int BN_, int WAVES_M, int WAVES_N, int SLOTS_A, int SLOTS_B>
+// Entries (M) by tokens (N), wavefronts along each, slots of the ring; groups of wavefronts that have a share of K (and a
+// ring) each.
+template <int BM_, int BN_, int WAVES_M, int WAVES_N, int SLOTS_A, int SLOTS_B, int GROUPS = 1>
 struct Fp8Shape {
-    static constexpr int BM = BM_, BN = BN_, kWavesM = WAVES_M, kWavesN = WAVES_N;
-    static constexpr int kWaves = WAVES_M * WAVES_N, kThreads = 64 * kWaves;
+    static constexpr int BM = BM_, BN = BN_, kWavesM = WAVES_M, kWavesN = WAVES_N, kGroups = GROUPS;
+    static constexpr int kWaves = WAVES_M * WAVES_N, kThreads = 64 * kWaves * GROUPS;
     static constexpr int kWaveM = BM / WAVES_M, kWaveN = BN / WAVES_N;
     static constexpr int kRowTiles = kWaveM / 16, kColTiles = kWaveN / 16;
     static constexpr int kBytesA = BM * 128, kBytesB = BN * 128;
     static constexpr int kSlotsA = SLOTS_A, kSlotsB = SLOTS_B;
-    static constexpr int kLds = kSlotsA * kBytesA + kSlotsB * kBytesB;
+    static constexpr int kRing = kSlotsA * kBytesA + kSlotsB * kBytesB, kLds = kRing * GROUPS;
     static constexpr int kCopiesA = kBytesA / 1024 / kWaves, kCopiesB = kBytesB / 1024 / kWaves;   // of a wavefront and stage
     static_assert(kCopiesA * kWaves * 1024 == kBytesA && kCopiesB * kWaves * 1024 == kBytesB, "whole copies");
     static_assert(kCopiesA % 2 == 0 && kCopiesB % 2 == 0, "a wavefront's first copy is an even one");
@@ -57,10 +61,11 @@ struct Fp8Shape {
     }
 };
 using Large = Fp8Shape<256, 256, 2, 4, 3, 2>;
-using Middle = Fp8Shape<128, 128, 2, 2, 2, 2>;
+using Middle = Fp8Shape<128, 128, 2, 2, 3, 2>;
 using Small = Fp8Shape<64, 64, 2, 2, 2, 2>;
+using Deep = Fp8Shape<64, 64, 2, 2, 2, 2, 4>;
 static_assert(Large::launched_as(kFp8Shapes[kFp8Large]) && Middle::launched_as(kFp8Shapes[kFp8Middle]) &&
-              Small::launched_as(kFp8Shapes[kFp8Small]), "as launched");
+              Small::launched_as(kFp8Shapes[kFp8Small]) && Deep::launched_as(kFp8Shapes[kFp8Deep]), "as launched");
 
 // A fragment from the two pieces that a lane read of it.
 template <typename F>
@@ -110,14 +115,18 @@ __device__ __forceinline__ int staged_at(int row, int byte) {
 }
 
 template <typename T, typename S>
-__global__ void __launch_bounds__(S::kThreads, S::BM == 64 ? (sizeof(T) == 2 ? 5 : 4) : 2) fp8_tile(const Fp8LinearArgs g) {
-    extern __shared__ __attribute__((aligned(1024))) char ring[];
+__global__ void __launch_bounds__(S::kThreads, S::kGroups > 1 ? 4 : S::BM == 64 ? (sizeof(T) == 2 ? 5 : 4) : 2) fp8_tile(const Fp8LinearArgs g) {
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
     uint32_t tm, tn, split;
     tile_of(blockIdx.x, g.tiles_v, g.tiles_t, 1u, tm, tn, split);
     const int m0 = int(tm) * S::BM, n0 = int(tn) * S::BN;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = all_waves / S::kWaves, wave = all_waves % S::kWaves;
     const int wm = wave / S::kWavesN, wn = wave % S::kWavesN;
-    const int nst = g.blocks;
+    // the group's stages are first .. nst - 1, `share` of them but for the last group's
+    const int share = (g.blocks + S::kGroups - 1) / S::kGroups, first = group * share;
+    const int nst = first + share < g.blocks ? first + share : g.blocks;
+    char* const ring = lds + group * S::kRing;
     using F = Fragment<sizeof(T) == 4>;
     f32x4 acc[S::kRowTiles][S::kColTiles];
 #pragma unroll
@@ -178,24 +187,33 @@ __global__ void __launch_bounds__(S::kThreads, S::BM == 64 ? (sizeof(T) == 2 ? 5
             for (int j = 0; j < S::kColTiles; ++j)
                 next[j] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from_s, int(token(j) * uint32_t(g.blocks) * 4u), s * 4, 0));
         };
-        load_scales(0);
-        issue_a(0, 0);
-        issue_b(0, 0);
-        for (int s0 = 0; s0 < nst; s0 += 4) {
+        load_scales(first);
+        issue_a(first, 0);
+        issue_b(first, 0);
+        if constexpr (S::kSlotsA == 3) issue_a(first + 1, 1);
+        int slot = 0;                      // of the projection's ring
+        for (int s0 = first; s0 < first + share; s0 += 4) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int s = s0 + u;
-                if (s >= nst) break;
-                wait_copies<0>();
+                if (s >= first + share) break;             // every group meets as often
+                if (S::kSlotsA == 3 && s + 1 < nst) wait_copies<S::kCopiesA>();
+                else wait_copies<0>();
                 meet();
+                if (S::kGroups > 1 && s >= nst) continue;
                 if (u == 0) {
 #pragma unroll
                     for (int j = 0; j < S::kColTiles; ++j) now[j] = next[j];
                     load_scales(s0 + 4);
                 }
-                const uint32_t slot_a = uint32_t(u % 2 * S::kBytesA), slot_b = uint32_t(u % 2 * S::kBytesB);
-                issue_a(s + 1, (u + 1) % 2);
+                const uint32_t slot_a = uint32_t((S::kSlotsA == 3 ? slot : u % 2) * S::kBytesA), slot_b = uint32_t(u % 2 * S::kBytesB);
                 issue_b(s + 1, (u + 1) % 2);
+                if constexpr (S::kSlotsA == 3) {
+                    issue_a(s + 2, slot == 0 ? 2 : slot - 1);
+                    slot = slot == 2 ? 0 : slot + 1;
+                } else {
+                    issue_a(s + 1, (u + 1) % 2);
+                }
                 float scale[S::kColTiles];
 #pragma unroll
                 for (int j = 0; j < S::kColTiles; ++j) scale[j] = now[j][u] * sw[s];
@@ -270,6 +288,24 @@ __global__ void __launch_bounds__(S::kThreads, S::BM == 64 ? (sizeof(T) == 2 ? 5
         if (wm == 0) meet();
     }
     __syncthreads();                       // the ring is free
+    if constexpr (S::kGroups > 1) {        // the groups' shares, in their order
+        constexpr int kEach = S::kRowTiles * S::kColTiles;
+        static_assert((S::kGroups - 1) * kEach * S::kWaves * 1024 <= S::kLds, "the shares");
+        f32x4* part = reinterpret_cast<f32x4*>(lds) + threadIdx.x % (64 * S::kWaves);
+        if (group > 0) {
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                part[((group - 1) * kEach + i) * 64 * S::kWaves] = acc[i / S::kColTiles][i % S::kColTiles];
+        }
+        __syncthreads();
+        if (group == 0) {
+#pragma unroll
+            for (int o = 0; o < S::kGroups - 1; ++o)
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) acc[i / S::kColTiles][i % S::kColTiles] += part[(o * kEach + i) * 64 * S::kWaves];
+        }
+        __syncthreads();
+    }
 
     // Element e of accumulator (i, j) is entry m0 + wm kWaveM + 16 i + 4 (lane / 16) + e of token n0 + wn kWaveN + 16 j +
     // lane % 16.  The tile goes through LDS, so that a token's entries leave in whole rows.
@@ -279,6 +315,7 @@ __global__ void __launch_bounds__(S::kThreads, S::BM == 64 ? (sizeof(T) == 2 ? 5
     const T* bias = static_cast<const T*>(g.bias);
 #pragma unroll
     for (int i = 0; i < S::kRowTiles; ++i) {
+        if (group > 0) break;
         const int m = wm * S::kWaveM + 16 * i + 4 * (lane >> 4);
         float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (bias) {                        // entries past the end take the last one's: they are not stored
@@ -290,7 +327,7 @@ __global__ void __launch_bounds__(S::kThreads, S::BM == 64 ? (sizeof(T) == 2 ? 5
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = acc[i][j][e] + b[e];
-            store_row<4>(reinterpret_cast<T*>(ring + staged_at<kRow>(wn * S::kWaveN + 16 * j + (lane & 15), m * int(sizeof(T)))), v);
+            store_row<4>(reinterpret_cast<T*>(lds + staged_at<kRow>(wn * S::kWaveN + 16 * j + (lane & 15), m * int(sizeof(T)))), v);
         }
     }
     __syncthreads();
@@ -299,12 +336,12 @@ __global__ void __launch_bounds__(S::kThreads, S::BM == 64 ? (sizeof(T) == 2 ? 5
     for (int r = threadIdx.x / kLanes; r < kRows; r += S::kThreads / kLanes) {
         const int t = n0 + r;
         if (t >= g.n || v0 >= g.vocab) continue;
-        const u32x4 d = *reinterpret_cast<const u32x4*>(ring + staged_at<kRow>(r, 16 * c));
+        const u32x4 d = *reinterpret_cast<const u32x4*>(lds + staged_at<kRow>(r, 16 * c));
         T* to = out + int64_t(t) * g.vocab + v0;
         if (v0 + V <= g.vocab) {
             *reinterpret_cast<typename Unaligned16<T>::type*>(to) = d;
         } else {
-            const T* from = reinterpret_cast<const T*>(ring + staged_at<kRow>(r, 16 * c));
+            const T* from = reinterpret_cast<const T*>(lds + staged_at<kRow>(r, 16 * c));
             for (int k = 0; v0 + k < g.vocab; ++k) to[k] = from[k];
         }
     }
@@ -322,8 +359,12 @@ const void* tile_of_type(int out_dtype) {
 }  // namespace
 
 const void* pick_fp8_tile(int out_dtype, int kind) {
-    if (out_dtype == kF32) return kind == kFp8Small ? reinterpret_cast<const void*>(&fp8_tile<float, Small>) : nullptr;
+    if (out_dtype == kF32)
+        return kind == kFp8Small  ? reinterpret_cast<const void*>(&fp8_tile<float, Small>)
+               : kind == kFp8Deep ? reinterpret_cast<const void*>(&fp8_tile<float, Deep>)
+                                  : nullptr;
     switch (kind) {
+    case kFp8Deep: return tile_of_type<Deep>(out_dtype);
     case kFp8Small: return tile_of_type<Small>(out_dtype);
     case kFp8Middle: return tile_of_type<Middle>(out_dtype);
     case kFp8Large: return tile_of_type<Large>(out_dtype);

@@ -25,7 +25,7 @@ constexpr int64_t kMaxElements = int64_t(1) << 62;
 bool set_up(int dev) {
     if (!is_gfx950(dev)) return false;
     for (int dt : {RLPL_F32, RLPL_F16, RLPL_BF16})
-        for (int kind = kFp8Small; kind <= kFp8Large; ++kind) {
+        for (int kind = kFp8Small; kind <= kFp8Deep; ++kind) {
             const void* k = pick_fp8_tile(dt, kind);
             if (k && hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kFp8Shapes[kind].lds) != hipSuccess)
                 return false;
@@ -76,11 +76,11 @@ bool fp8_shape_ok(int64_t n, int64_t h, int64_t vocab) {
 // The time of a product's tiles in microseconds, to choose between their shapes: a tile of `steps` blocks of K takes
 // fixed + step * steps alone, and a chip full of them fill + pace * steps each on one of its 256 compute units (fitted to
 // 23 sizes between 1 x 1024 x 1000 and 8192^3: 333 x 2048 x 5003 takes 11 us with the small shape, 18 and 38 with the
-// others; 2048 x 4096 x 4096 68, 48 and 65; 2048 x 4096 x 128256 1969, 1533 and 1026).
+// others; 2048 x 4096 x 4096 66, 46 and 58; 128 x 4096 x 128256 182, 136 and 139; 2048 x 4096 x 128256 1969, 1533 and 1026).
 struct Fp8Pace {
     double fixed, step, fill, pace;
 };
-constexpr Fp8Pace kFp8Paces[] = {{2.0, 0.40, 0.5, 0.215}, {3.2, 0.825, 2.0, 0.6}, {8.8, 1.47, 9.0, 1.7}};
+constexpr Fp8Pace kFp8Paces[] = {{2.0, 0.40, 0.5, 0.215}, {3.2, 0.75, 2.0, 0.56}, {8.8, 1.47, 9.0, 1.7}};
 double fp8_time(int kind, int64_t n, int64_t blocks, int64_t vocab) {
     const Fp8TileShape& s = kFp8Shapes[kind];
     const Fp8Pace& p = kFp8Paces[kind];
@@ -89,6 +89,10 @@ double fp8_time(int kind, int64_t n, int64_t blocks, int64_t vocab) {
     return all > one ? all + 0.3 * one : one + 0.3 * all;
 }
 int fp8_kind(int64_t n, int64_t blocks, int64_t vocab, int out_dtype) {
+    // A small tile for each compute unit at most: four groups of wavefronts share K (33 x 8192 x 4096: 21 us instead of 41,
+    // 64 x 4096 x 16384 17 instead of 24, both with 256 tiles or fewer; 376 of them 26 instead of 24).
+    const Fp8TileShape& small = kFp8Shapes[kFp8Small];
+    if (div_up(vocab, small.vocab) * div_up(n, small.tokens) <= 256 && blocks >= 8) return kFp8Deep;
     if (out_dtype == RLPL_F32) return kFp8Small;
     int best = kFp8Small;
     for (int kind : {kFp8Middle, kFp8Large})

@@ -77,7 +77,7 @@ def product_case(x, xs, w, ws, bias, out, block_rows=128):
 
 SHAPES = [(1, 16, 1), (1, 128, 16), (1, 4096, 300), (2, 144, 65), (16, 256, 64), (17, 512, 129), (33, 272, 700), (64, 1024, 1000),
           (65, 384, 257), (100, 1040, 515), (128, 128, 256), (129, 2048, 384), (256, 512, 512), (257, 640, 513), (300, 4096, 1003),
-          (700, 256, 2051), (1, 65536, 40), (1000, 80, 90)]
+          (700, 256, 2051), (1, 65536, 40), (1000, 80, 90), (20, 1152, 70), (40, 2176, 130), (33, 2064, 64), (65, 8208, 129)]
 
 
 @gpu

@@ -630,8 +630,8 @@ int token_logprobs_bwd(const void* logits, const int64_t* targets, const void* m
  * workspace    : fp8_linear_workspace_bytes(n, hidden_size, vocab) bytes, 256-byte aligned, no initial contents needed;
  *                one call in flight per workspace
  *
- * 1 <= n <= 2^20, hidden_size a multiple of 16 in [16, 65536], 1 <= vocab < 2^22; for rlpl_fp8_quantize 1 <= rows < 2^31,
- * 1 <= cols <= 2^31 - 65536.
+ * 1 <= n <= 2^20, hidden_size a multiple of 16 in [16, 65536], 1 <= vocab < 2^22, fewer than 2^24 tiles of 64 rows by 64
+ * entries; for rlpl_fp8_quantize 1 <= rows < 2^31, 1 <= cols <= 2^31 - 65536.
  */
 int rlpl_fp8_quantize(const void* x, int64_t rows, int64_t cols, int64_t row_stride, int dtype, int block_rows, void* q,
                       float* scale, hipStream_t stream);

@@ -68,9 +68,11 @@ size_t token_bytes(int64_t rows, int64_t vocab, int64_t top_k) {
 constexpr int64_t kFp8MaxRows = int64_t(1) << 20;
 constexpr int64_t kFp8MaxHidden = 65536;
 constexpr int64_t kFp8MaxVocab = int64_t(1) << 22;
+constexpr int64_t kFp8MaxTiles = int64_t(1) << 24;          // of the small shape (x 256 lanes < 2^32)
 
 bool fp8_shape_ok(int64_t n, int64_t h, int64_t vocab) {
-    return n >= 1 && n <= kFp8MaxRows && h >= 16 && h <= kFp8MaxHidden && h % 16 == 0 && vocab >= 1 && vocab < kFp8MaxVocab;
+    return n >= 1 && n <= kFp8MaxRows && h >= 16 && h <= kFp8MaxHidden && h % 16 == 0 && vocab >= 1 && vocab < kFp8MaxVocab &&
+           div_up(n, kFp8Shapes[kFp8Small].tokens) * div_up(vocab, kFp8Shapes[kFp8Small].vocab) < kFp8MaxTiles;
 }
 
 // The time of a product's tiles in microseconds, to choose between their shapes: a tile of `steps` blocks of K takes

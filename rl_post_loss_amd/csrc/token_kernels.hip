@@ -105,6 +105,12 @@ __device__ __forceinline__ float key_logit(uint64_t key) {
 constexpr uint32_t kKeyOfMinusInf = 0x007FFFFFu;               // a key's upper half
 __device__ __forceinline__ uint32_t key_index(uint64_t key) { return ~uint32_t(key); }
 
+// Where row r starts, in elements; r and inner are below 2^31.
+__device__ __forceinline__ int64_t row_at(const TokenRows& in, int64_t row) {
+    const uint32_t r = uint32_t(row), inner = uint32_t(in.inner), group = r / inner;
+    return group * in.group_stride + int64_t(r - group * inner) * in.row_stride;
+}
+
 // A row: elements [0, head) and [head + V vectors, n) one by one, those between in 16-byte vectors of V.
 template <typename T>
 struct Row {
@@ -112,7 +118,7 @@ struct Row {
     const T* p;
     int32_t n, head, vectors;
     __device__ __forceinline__ Row(const TokenRows& in, int64_t row) {
-        p = static_cast<const T*>(in.logits) + (row / in.inner) * in.group_stride + (row % in.inner) * in.row_stride;
+        p = static_cast<const T*>(in.logits) + row_at(in, row);
         n = int32_t(in.vocab);
         head = int32_t((-reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
         if (head > n) head = n;
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(kTokenThreads, E > 32 && sizeof(T) == 2 ? 4 : 
             write_masked<64>(a, row);
             continue;
         }
-        const T* p = static_cast<const T*>(a.in.logits) + (row / a.in.inner) * a.in.group_stride + (row % a.in.inner) * a.in.row_stride;
+        const T* p = static_cast<const T*>(a.in.logits) + row_at(a.in, row);
         const int64_t y = a.targets[row];
         // vector u of a lane is the row's vector 64 u + lane; the elements past the last vector go to the first lanes
         u32x4 raw[U];
@@ -614,7 +620,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a)
         const int64_t row = a.pieces == 1 ? item : item / a.pieces;
         const int piece = a.pieces == 1 ? 0 : int(item % a.pieces);
         const int32_t n = int32_t(a.in.vocab);
-        const T* x = static_cast<const T*>(a.in.logits) + (row / a.in.inner) * a.in.group_stride + (row % a.in.inner) * a.in.row_stride;
+        const T* x = static_cast<const T*>(a.in.logits) + row_at(a.in, row);
         T* out = static_cast<T*>(a.grad) + row * a.in.vocab;
         int32_t head = int32_t((-reinterpret_cast<uintptr_t>(out) & 15) / sizeof(T));
         if (head > n) head = n;

@@ -542,7 +542,7 @@ def _grad_list(grads, in_place):
     try:
         devices, dtypes = set(map(torch.Tensor.get_device, kept)), set(map(_dtype_of, kept))
         plain = len(devices) == 1 and min(devices) >= 0 and dtypes <= DTYPE.keys() and all(map(torch.Tensor.is_contiguous, kept))
-    except TypeError:
+    except (TypeError, RuntimeError):                          # no tensor; a sparse one, which has no strides
         plain = False
     if not plain:
         _refuse_or_pack(kept, in_place)
@@ -555,8 +555,8 @@ def _grad_list(grads, in_place):
 def _refuse_or_pack(kept, in_place):
     """Raises for a gradient that cannot be taken, and replaces those that have gaps."""
     for i, g in enumerate(kept):
-        if not isinstance(g, torch.Tensor) or not g.is_cuda or g.dtype not in DTYPE:
-            raise TypeError(f"gradient {i} must be a float32, float16 or bfloat16 CUDA (HIP) tensor")
+        if not isinstance(g, torch.Tensor) or not g.is_cuda or g.dtype not in DTYPE or g.layout != torch.strided:
+            raise TypeError(f"gradient {i} must be a dense float32, float16 or bfloat16 CUDA (HIP) tensor")
         if g.device != kept[0].device:
             raise ValueError(f"gradient {i} must be on {kept[0].device}, as the first one")
         if not _without_gaps(g):
@@ -616,8 +616,9 @@ def scale_grads(grads: Sequence[Optional[torch.Tensor]], scale: torch.Tensor) ->
 
 def clip_grads(grads: Sequence[Optional[torch.Tensor]], max_norm, *, norm_type=2.0, eps=1e-6, workspace=None) -> torch.Tensor:
     """Scales the gradients in place by min(1, max_norm / (norm + eps)) and returns their norm before that, a 0-d float32
-    tensor.  Nothing is written where the norm is within max_norm.  Where ``adamw_step`` follows, ``grad_norm``'s scale
-    saves this second pass over the gradients."""
+    tensor.  Nothing is written where the norm is within max_norm; a NaN among the gradients makes all of them NaN, an
+    infinity makes it NaN and the others 0.  Where ``adamw_step`` follows, ``grad_norm``'s scale saves this second pass over
+    the gradients."""
     if max_norm is None:
         raise ValueError("max_norm must be a number")
     listed = _grad_list(grads, True)

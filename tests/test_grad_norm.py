@@ -213,7 +213,8 @@ def test_past_32_bits_of_elements():
 @gpu
 def test_refusals_of_tensors():
     g, s = torch.zeros(8, device=DEV), torch.ones((), device=DEV)
-    for bad, error in [([], ValueError), ([None], ValueError), ([g.cpu()], TypeError), ([g.int()], TypeError), ([3.0], TypeError)]:
+    for bad, error in [([], ValueError), ([None], ValueError), ([g.cpu()], TypeError), ([g.int()], TypeError), ([3.0], TypeError),
+                       ([g, torch.eye(3, device=DEV).to_sparse()], TypeError)]:
         with pytest.raises(error):
             rl.grad_norm(bad)
         with pytest.raises(error):

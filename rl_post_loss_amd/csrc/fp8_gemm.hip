@@ -23,7 +23,8 @@
 // it comes from memory: 128 x 4096 x 128256 136 us instead of 149 (4 TB/s).  64 x 64 with K
 // shared by four groups of wavefronts, for tiles too few to fill the chip: a step of a workgroup
 // alone is bound by its instructions, not by its copies (more stages change nothing), and four
-// groups take 1.1 us for four steps of 0.6.
+// groups take 1.1 us for four steps of 0.6.  float32 outputs: 8192^3 0.97 ms at 128 x 128
+// (1.13 PFLOP/s of 16-bit instructions; 1.26 ms at 64 x 64, whose wavefronts convert twice as much for each product).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -225,9 +226,20 @@ __global__ void __launch_bounds__(S::kThreads, S::kGroups > 1 ? 4 : S::BM == 64 
                 } else {
                     u32x4 v[16];
                     read_k(la + slot_a, ha + slot_a, lb + slot_b, hb + slot_b, v);
-                    const F a[4] = {whole<F>(v[0], v[4]), whole<F>(v[1], v[5]), whole<F>(v[2], v[6]), whole<F>(v[3], v[7])};
                     const F b[4] = {whole<F>(v[8], v[12]), whole<F>(v[9], v[13]), whole<F>(v[10], v[14]), whole<F>(v[11], v[15])};
-                    multiply<0>(a, b, scale, acc);
+                    if constexpr (sizeof(T) == 4) {        // a fragment is 16 registers: the first operand's one by one
+                        const auto row = [&](auto i) {
+                            const F a[1] = {whole<F>(v[i], v[4 + i])};
+                            multiply<i>(a, b, scale, acc);
+                        };
+                        row(std::integral_constant<int, 0>());
+                        row(std::integral_constant<int, 1>());
+                        row(std::integral_constant<int, 2>());
+                        row(std::integral_constant<int, 3>());
+                    } else {
+                        const F a[4] = {whole<F>(v[0], v[4]), whole<F>(v[1], v[5]), whole<F>(v[2], v[6]), whole<F>(v[3], v[7])};
+                        multiply<0>(a, b, scale, acc);
+                    }
                 }
             }
         }
@@ -360,9 +372,10 @@ const void* tile_of_type(int out_dtype) {
 
 const void* pick_fp8_tile(int out_dtype, int kind) {
     if (out_dtype == kF32)
-        return kind == kFp8Small  ? reinterpret_cast<const void*>(&fp8_tile<float, Small>)
-               : kind == kFp8Deep ? reinterpret_cast<const void*>(&fp8_tile<float, Deep>)
-                                  : nullptr;
+        return kind == kFp8Small    ? reinterpret_cast<const void*>(&fp8_tile<float, Small>)
+               : kind == kFp8Middle ? reinterpret_cast<const void*>(&fp8_tile<float, Middle>)
+               : kind == kFp8Deep   ? reinterpret_cast<const void*>(&fp8_tile<float, Deep>)
+                                    : nullptr;
     switch (kind) {
     case kFp8Deep: return tile_of_type<Deep>(out_dtype);
     case kFp8Small: return tile_of_type<Small>(out_dtype);

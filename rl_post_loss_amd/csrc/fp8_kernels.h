@@ -45,7 +45,7 @@ constexpr int kTurnRows = 64, kTurnCols = 4;   // of a workgroup
 struct Fp8TileShape {
     int vocab, tokens, threads, lds;
 };
-enum { kFp8Small = 0, kFp8Middle = 1, kFp8Large = 2, kFp8Deep = 3 };       // float32 outputs take the first or the last
+enum { kFp8Small = 0, kFp8Middle = 1, kFp8Large = 2, kFp8Deep = 3 };       // the large one has no float32 outputs
 constexpr Fp8TileShape kFp8Shapes[] = {{64, 64, 256, 32 * 1024}, {128, 128, 256, 80 * 1024}, {256, 256, 512, 160 * 1024},
                                        {64, 64, 1024, 128 * 1024}};
 const void* pick_fp8_tile(int out_dtype, int kind);

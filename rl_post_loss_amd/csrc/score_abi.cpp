@@ -83,9 +83,12 @@ struct Fp8Pace {
     double fixed, step, fill, pace;
 };
 constexpr Fp8Pace kFp8Paces[] = {{2.0, 0.40, 0.5, 0.215}, {3.2, 0.75, 2.0, 0.56}, {8.8, 1.47, 9.0, 1.7}};
-double fp8_time(int kind, int64_t n, int64_t blocks, int64_t vocab) {
+// float32 outputs take twice the matrix instructions, and conversions (1024 x 4096 x 4096 46 and 51 us with the small shape
+// and the middle one, 2048 x 4096 x 4096 86 and 69, 8192^3 1257 and 974).
+constexpr Fp8Pace kFp8WidePaces[] = {{3.0, 0.72, 1.0, 0.30}, {5.0, 1.15, 1.5, 0.95}};
+double fp8_time(int kind, int64_t n, int64_t blocks, int64_t vocab, bool wide) {
     const Fp8TileShape& s = kFp8Shapes[kind];
-    const Fp8Pace& p = kFp8Paces[kind];
+    const Fp8Pace& p = wide ? kFp8WidePaces[kind] : kFp8Paces[kind];
     const double tiles = double(div_up(vocab, s.vocab)) * double(div_up(n, s.tokens));
     const double one = p.fixed + p.step * double(blocks), all = tiles * (p.fill + p.pace * double(blocks)) / 256.0;
     return all > one ? all + 0.3 * one : one + 0.3 * all;
@@ -95,10 +98,10 @@ int fp8_kind(int64_t n, int64_t blocks, int64_t vocab, int out_dtype) {
     // 64 x 4096 x 16384 17 instead of 24, both with 256 tiles or fewer; 376 of them 26 instead of 24).
     const Fp8TileShape& small = kFp8Shapes[kFp8Small];
     if (div_up(vocab, small.vocab) * div_up(n, small.tokens) <= 256 && blocks >= 8) return kFp8Deep;
-    if (out_dtype == RLPL_F32) return kFp8Small;
+    const bool wide = out_dtype == RLPL_F32;
     int best = kFp8Small;
-    for (int kind : {kFp8Middle, kFp8Large})
-        if (fp8_time(kind, n, blocks, vocab) < fp8_time(best, n, blocks, vocab)) best = kind;
+    for (int kind = kFp8Middle; kind <= (wide ? kFp8Middle : kFp8Large); ++kind)
+        if (fp8_time(kind, n, blocks, vocab, wide) < fp8_time(best, n, blocks, vocab, wide)) best = kind;
     return best;
 }
 

@@ -18,7 +18,7 @@
 // for 8192^3 (2.3; the library's product with one scale for each operand 0.98 and
 // 0.38 ms).  A step has 2048 cycles of matrix instructions (1.47 us alone, 1.7 to
 // 2.05 with its share of a tile's ends).  64 x 64 and 128 x 128, five and two
-// workgroups a compute unit, for fewer results: 333 x 2048 x 5003 8 us, 2048 x 4096
+// workgroups a compute unit, for fewer results: 333 x 2048 x 5003 11 us, 2048 x 4096
 // x 4096 46 us (1.5 PFLOP/s).  The projection's ring has a third stage at 128 x 128, where
 // it comes from memory: 128 x 4096 x 128256 136 us instead of 149 (4 TB/s).  64 x 64 with K
 // shared by four groups of wavefronts, for tiles too few to fill the chip: a step of a workgroup

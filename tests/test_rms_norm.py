@@ -85,7 +85,8 @@ def forward_case(x, w, residual, eps, rstd, stream, y=None, q=None, scale=None):
 
 
 SHAPES = [(1, 1), (1, 4096), (3, 2), (5, 7), (4, 64), (9, 128), (7, 129), (33, 512), (9, 513), (130, 1024), (7, 2048),
-          (6, 2056), (257, 96), (3, 4100), (5, 8192), (2, 8199), (2, 16384), (3, 12345), (300, 130), (1500, 40), (40, 15)]
+          (6, 2056), (257, 96), (3, 4100), (5, 8192), (2, 8199), (2, 16384), (3, 12345), (300, 130), (1500, 40), (40, 15),
+          (25, 256), (90, 250), (7, 264), (2, 6144), (3, 6145), (4, 7000)]
 
 
 @gpu

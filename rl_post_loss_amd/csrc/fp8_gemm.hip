@@ -13,17 +13,18 @@
 // A lane of a fragment takes 16-byte pieces q and q + 4 of a row's 128 bytes
 // (q = lane / 16) in both operands: which of K's elements meet is all that counts.
 //
-// Four shapes (score_abi.cpp chooses by a time model).  256 x 256, the loop of
+// Five shapes (score_abi.cpp chooses by a time model), entries by tokens.  256 x 256, the loop of
 // the cross entropy's large tile: 1.03 ms for 2048 x 4096 x 128256 (2.1 PFLOP/s), 0.47
-// for 8192^3 (2.3; the library's product with one scale for each operand 0.98 and
-// 0.38 ms).  A step has 2048 cycles of matrix instructions (1.47 us alone, 1.7 to
+// for 8192^3 (2.3; the library's product with one scale for each operand 0.86 to 0.98 and
+// 0.36 to 0.38 ms).  A step has 2048 cycles of matrix instructions (1.47 us alone, 1.7 to
 // 2.05 with its share of a tile's ends).  64 x 64 and 128 x 128, five and two
 // workgroups a compute unit, for fewer results: 333 x 2048 x 5003 11 us, 2048 x 4096
 // x 4096 46 us (1.5 PFLOP/s).  The projection's ring has a third stage at 128 x 128, where
-// it comes from memory: 128 x 4096 x 128256 136 us instead of 149 (4 TB/s).  64 x 64 with K
-// shared by four groups of wavefronts, for tiles too few to fill the chip: a step of a workgroup
-// alone is bound by its instructions, not by its copies (more stages change nothing), and four
-// groups take 1.1 us for four steps of 0.6.  float32 outputs: 8192^3 0.97 ms at 128 x 128
+// it comes from memory: 128 x 4096 x 128256 136 us instead of 149 (4 TB/s).  128 x 64 with three stages
+// of both operands for up to 128 rows of a long projection (128 x 8192 x 30000 57 us; 67 by 64 x 64, 81 by
+// 128 x 128).  64 x 64 with K shared by four groups of wavefronts, for tiles too few to fill the chip: a
+// step of a workgroup alone is bound by its instructions, not by its copies (more stages change
+// nothing), and four groups take 1.1 us for four steps of 0.6.  float32 outputs: 8192^3 0.97 ms at 128 x 128
 // (1.13 PFLOP/s of 16-bit instructions; 1.26 ms at 64 x 64, whose wavefronts convert twice as much for each product).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -65,8 +66,10 @@ using Large = Fp8Shape<256, 256, 2, 4, 3, 2>;
 using Middle = Fp8Shape<128, 128, 2, 2, 3, 2>;
 using Small = Fp8Shape<64, 64, 2, 2, 2, 2>;
 using Deep = Fp8Shape<64, 64, 2, 2, 2, 2, 4>;
+using Narrow = Fp8Shape<128, 64, 2, 2, 3, 3>;
 static_assert(Large::launched_as(kFp8Shapes[kFp8Large]) && Middle::launched_as(kFp8Shapes[kFp8Middle]) &&
-              Small::launched_as(kFp8Shapes[kFp8Small]) && Deep::launched_as(kFp8Shapes[kFp8Deep]), "as launched");
+              Small::launched_as(kFp8Shapes[kFp8Small]) && Deep::launched_as(kFp8Shapes[kFp8Deep]) &&
+              Narrow::launched_as(kFp8Shapes[kFp8Narrow]), "as launched");
 
 // A fragment from the two pieces that a lane read of it.
 template <typename F>
@@ -194,13 +197,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kGroups > 1 ? 4 : S::BM == 64 
         issue_a(first, 0);
         issue_b(first, 0);
         if constexpr (S::kSlotsA == 3) issue_a(first + 1, 1);
-        int slot = 0;                      // of the projection's ring
+        if constexpr (S::kSlotsB == 3) issue_b(first + 1, 1);
+        int slot = 0;                      // of the rings of three
         for (int s0 = first; s0 < first + share; s0 += 4) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int s = s0 + u;
                 if (s >= first + share) break;             // every group meets as often
-                if (S::kSlotsA == 3 && s + 1 < nst) wait_copies<S::kCopiesA>();
+                if (S::kSlotsA == 3 && s + 1 < nst) wait_copies<S::kCopiesA + (S::kSlotsB == 3 ? S::kCopiesB : 0)>();
                 else wait_copies<0>();
                 meet();
                 if (S::kGroups > 1 && s >= nst) continue;
@@ -209,14 +213,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kGroups > 1 ? 4 : S::BM == 64 
                     for (int j = 0; j < S::kColTiles; ++j) now[j] = next[j];
                     load_scales(s0 + 4);
                 }
-                const uint32_t slot_a = uint32_t((S::kSlotsA == 3 ? slot : u % 2) * S::kBytesA), slot_b = uint32_t(u % 2 * S::kBytesB);
-                issue_b(s + 1, (u + 1) % 2);
-                if constexpr (S::kSlotsA == 3) {
-                    issue_a(s + 2, slot == 0 ? 2 : slot - 1);
-                    slot = slot == 2 ? 0 : slot + 1;
-                } else {
-                    issue_a(s + 1, (u + 1) % 2);
-                }
+                const uint32_t slot_a = uint32_t((S::kSlotsA == 3 ? slot : u % 2) * S::kBytesA);
+                const uint32_t slot_b = uint32_t((S::kSlotsB == 3 ? slot : u % 2) * S::kBytesB);
+                const int after = slot == 0 ? 2 : slot - 1;            // the slot that stage s - 1 left
+                if constexpr (S::kSlotsB == 3) issue_b(s + 2, after);
+                else issue_b(s + 1, (u + 1) % 2);
+                if constexpr (S::kSlotsA == 3) issue_a(s + 2, after);
+                else issue_a(s + 1, (u + 1) % 2);
+                slot = slot == 2 ? 0 : slot + 1;
                 float scale[S::kColTiles];
 #pragma unroll
                 for (int j = 0; j < S::kColTiles; ++j) scale[j] = now[j][u] * sw[s];
@@ -224,6 +228,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kGroups > 1 ? 4 : S::BM == 64 
                     u32x4 v[8];
                     read_stage(la + slot_a, ha + slot_a, lb + slot_b, hb + slot_b, v);
                     const F a[2] = {whole<F>(v[0], v[2]), whole<F>(v[1], v[3])}, b[2] = {whole<F>(v[4], v[6]), whole<F>(v[5], v[7])};
+                    multiply<0>(a, b, scale, acc);
+                } else if constexpr (S::kColTiles == 2) {
+                    u32x4 v[8], w[4];
+                    read_k(la + slot_a, ha + slot_a, v);
+                    read_k2(lb + slot_b, hb + slot_b, w);
+                    const F b[2] = {whole<F>(w[0], w[2]), whole<F>(w[1], w[3])};
+                    const F a[4] = {whole<F>(v[0], v[4]), whole<F>(v[1], v[5]), whole<F>(v[2], v[6]), whole<F>(v[3], v[7])};
                     multiply<0>(a, b, scale, acc);
                 } else {
                     u32x4 v[16];
@@ -377,9 +388,11 @@ const void* pick_fp8_tile(int out_dtype, int kind) {
         return kind == kFp8Small    ? reinterpret_cast<const void*>(&fp8_tile<float, Small>)
                : kind == kFp8Middle ? reinterpret_cast<const void*>(&fp8_tile<float, Middle>)
                : kind == kFp8Deep   ? reinterpret_cast<const void*>(&fp8_tile<float, Deep>)
+               : kind == kFp8Narrow ? reinterpret_cast<const void*>(&fp8_tile<float, Narrow>)
                                     : nullptr;
     switch (kind) {
     case kFp8Deep: return tile_of_type<Deep>(out_dtype);
+    case kFp8Narrow: return tile_of_type<Narrow>(out_dtype);
     case kFp8Small: return tile_of_type<Small>(out_dtype);
     case kFp8Middle: return tile_of_type<Middle>(out_dtype);
     case kFp8Large: return tile_of_type<Large>(out_dtype);

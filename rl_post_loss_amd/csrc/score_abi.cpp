@@ -25,7 +25,7 @@ constexpr int64_t kMaxElements = int64_t(1) << 62;
 bool set_up(int dev) {
     if (!is_gfx950(dev)) return false;
     for (int dt : {RLPL_F32, RLPL_F16, RLPL_BF16})
-        for (int kind = kFp8Small; kind <= kFp8Deep; ++kind) {
+        for (int kind = 0; kind < kFp8Kinds; ++kind) {
             const void* k = pick_fp8_tile(dt, kind);
             if (k && hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kFp8Shapes[kind].lds) != hipSuccess)
                 return false;
@@ -76,22 +76,32 @@ bool fp8_shape_ok(int64_t n, int64_t h, int64_t vocab) {
 }
 
 // The time of a product's tiles in microseconds, to choose between their shapes: a tile of `steps` blocks of K takes
-// fixed + step * steps alone, and a chip full of them fill + pace * steps each on one of its 256 compute units (fitted to
-// 23 sizes between 1 x 1024 x 1000 and 8192^3: 333 x 2048 x 5003 takes 11 us with the small shape, 18 and 38 with the
-// others; 2048 x 4096 x 4096 66, 46 and 58; 128 x 4096 x 128256 182, 136 and 139; 2048 x 4096 x 128256 1969, 1533 and 1026).
+// fixed + step * steps alone, and a chip full of them fill + pace * steps each on one of its 256 compute units; a
+// projection that the last cache does not hold arrives at `rate` GB a millisecond, once a row of tiles.  Fitted to 219 sizes drawn
+// from 17 to 4096 rows, H from 64 to 8192 and 1000 to 131072 entries, where the choice is 1 to 2 % behind the best shape's time:
+// 333 x 2048 x 5003 takes 11 us with the small shape, 18 and 38 with the middle and the large one; 2048 x 4096 x 4096 66, 46 and
+// 58; small, narrow and middle 64 x 4096 x 32000 24, 31 and 39, 64 x 4096 x 128256 126, 117 and 123, 128 x 4096 x 32000 37, 32
+// and 42; 128 x 4096 x 128256 182, 166, 136 and the large one 139; 2048 x 4096 x 128256 1969 with the small one, 1533 with the
+// middle and 1026 with the large one.
 struct Fp8Pace {
-    double fixed, step, fill, pace;
+    double fixed, step, fill, pace, rate;
 };
-constexpr Fp8Pace kFp8Paces[] = {{2.0, 0.40, 0.5, 0.215}, {3.2, 0.75, 2.0, 0.56}, {8.8, 1.47, 9.0, 1.7}};
+constexpr Fp8Pace kFp8Paces[] = {{2.8, 0.51, 0.30, 0.236, 6.0}, {1.0, 0.685, 0.79, 0.44, 6.4}, {3.7, 0.89, 1.37, 0.633, 4.5},
+                                 {9.2, 1.02, 7.5, 1.53, 3.6}};
 // float32 outputs take twice the matrix instructions, and conversions (1024 x 4096 x 4096 46 and 51 us with the small shape
 // and the middle one, 2048 x 4096 x 4096 86 and 69, 8192^3 1257 and 974).
-constexpr Fp8Pace kFp8WidePaces[] = {{3.0, 0.72, 1.0, 0.30}, {5.0, 1.15, 1.5, 0.95}};
+constexpr Fp8Pace kFp8WidePaces[] = {{0.0, 0.82, 0.65, 0.30, 5.4}, {0.7, 0.86, 1.44, 0.566, 5.4}, {2.9, 1.19, 2.57, 0.90, 3.6}};
+constexpr double kFp8Cached = 268435456.0;
 double fp8_time(int kind, int64_t n, int64_t blocks, int64_t vocab, bool wide) {
     const Fp8TileShape& s = kFp8Shapes[kind];
     const Fp8Pace& p = wide ? kFp8WidePaces[kind] : kFp8Paces[kind];
-    const double tiles = double(div_up(vocab, s.vocab)) * double(div_up(n, s.tokens));
-    const double one = p.fixed + p.step * double(blocks), all = tiles * (p.fill + p.pace * double(blocks)) / 256.0;
-    return all > one ? all + 0.3 * one : one + 0.3 * all;
+    const double rows = double(div_up(n, s.tokens)), tiles = double(div_up(vocab, s.vocab)) * rows;
+    // few workgroups a compute unit leave part of the last round idle
+    const double rounds = kind == kFp8Small ? tiles / 256.0 : 0.5 * (tiles / 256.0 + std::ceil(tiles / 256.0));
+    const double one = p.fixed + p.step * double(blocks), all = rounds * (p.fill + p.pace * double(blocks));
+    const double bytes = double(vocab) * double(blocks) * kFp8Group, stream = bytes > kFp8Cached ? bytes * rows / p.rate * 1e-6 : 0.0;
+    const double busy = all > one ? all + 0.3 * one : one + 0.3 * all;
+    return busy > stream ? busy : stream;
 }
 int fp8_kind(int64_t n, int64_t blocks, int64_t vocab, int out_dtype) {
     // A small tile for each compute unit at most: four groups of wavefronts share K (33 x 8192 x 4096: 21 us instead of 41,
@@ -100,7 +110,7 @@ int fp8_kind(int64_t n, int64_t blocks, int64_t vocab, int out_dtype) {
     if (div_up(vocab, small.vocab) * div_up(n, small.tokens) <= 256 && blocks >= 8) return kFp8Deep;
     const bool wide = out_dtype == RLPL_F32;
     int best = kFp8Small;
-    for (int kind = kFp8Middle; kind <= (wide ? kFp8Middle : kFp8Large); ++kind)
+    for (int kind = kFp8Narrow; kind <= (wide ? kFp8Middle : kFp8Large); ++kind)
         if (fp8_time(kind, n, blocks, vocab, wide) < fp8_time(best, n, blocks, vocab, wide)) best = kind;
     return best;
 }

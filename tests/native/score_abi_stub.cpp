@@ -156,7 +156,7 @@ static int fp8() {
     const int64_t ns[] = {INT64_MIN, 0, 1, 16, 17, 64, 65, 333, 2048, 4096, 65536, 1 << 20, (1 << 20) + 1, INT64_MAX};
     const int64_t hs[] = {INT64_MIN, 0, 8, 16, 24, 128, 2048, 4096, 8208, 65536, 65552, INT64_MAX};
     const int64_t vs[] = {INT64_MIN, 0, 1, 64, 512, 5003, 20000, 128256, 1 << 20, (1 << 22) - 1, 1 << 22, INT64_MAX};
-    long taken = 0, kinds[4] = {};
+    long taken = 0, kinds[kFp8Kinds] = {};
     for (int64_t n : ns)
         for (int64_t h : hs)
             for (int64_t v : vs) {
@@ -191,7 +191,7 @@ static int fp8() {
                         continue;
                     }
                     int kind = -1;
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < kFp8Kinds; ++i)
                         if (l.kernel == pick_fp8_tile(dt, i)) kind = i;
                     CHECK(kind >= 0);
                     ++kinds[kind];
@@ -208,7 +208,8 @@ static int fp8() {
                 }
             }
     g_look = nullptr;
-    CHECK(taken > 500 && kinds[0] > 10 && kinds[1] > 10 && kinds[2] > 10 && kinds[3] > 10);
+    CHECK(taken > 500);
+    for (long k : kinds) CHECK(k > 0);
     const int64_t dims[] = {INT64_MIN, -1, 0, 1, 100, 4096, (int64_t(1) << 31) - 65536, (int64_t(1) << 31) - 1, INT64_MAX};
     for (int64_t r : dims)
         for (int64_t c : dims)

@@ -93,9 +93,10 @@ def test_against_float64(n, H, V):
 
 
 @gpu
-@pytest.mark.parametrize("n,H,V", [(700, 2064, 40001), (1100, 144, 12001), (1500, 400, 30011), (257, 8192, 33000)])
+@pytest.mark.parametrize("n,H,V", [(700, 2064, 40001), (1100, 144, 12001), (1500, 400, 30011), (257, 8192, 33000),
+                                   (128, 2064, 50001), (65, 1040, 70003), (410, 1616, 7781)])
 def test_larger_tiles_by_some_of_their_results(n, H, V):
-    """Sizes that take the tiles of 256 and of 128, at rows and columns around the tiles' ends and some others."""
+    """Sizes that take the tiles of 256, of 128 and of 128 x 64, at rows and columns around the tiles' ends and some others."""
     x, xs, w, ws, b = make(n, H, V)
     rows = torch.tensor(sorted({r for r in (0, 1, 15, 16, 63, 64, 127, 128, 255, 256, 257, n // 2, n - 65, n - 2, n - 1) if r < n}))
     g = torch.Generator().manual_seed(0)

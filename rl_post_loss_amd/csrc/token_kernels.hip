@@ -432,12 +432,14 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
 }
 
 constexpr int kShortFound = 256;           // candidates of a wavefront that there is room for
+constexpr int kShortMany = 96;             // more of them cost more to rank than to thin out
 
 // One wavefront a row of up to 64 E elements, which stay in its registers: one maximum for all lanes, no barrier, and the
-// alternatives' elements are found again in registers.  Their bound is the k-th largest of the lanes' largest; where equal
-// logits bring more than there is room for to it, the k-th largest key itself, bit by bit.  20480 rows of 1000 bf16 take
-// 16.5 us (7 to read them), with 20 alternatives 37: a wavefront's instructions, 33 passes of a comparison and its count among
-// them.
+// alternatives' elements are found again in registers.  Their bound is the k-th largest of the lanes' largest, raised by
+// bisection where it leaves many; where equal logits still bring more than there is room for to it, the k-th largest key
+// itself, bit by bit.  20480 rows of 1000 bf16 take 16.5 us (7 to read them), with 20 alternatives 37, with 64 73: a wavefront's
+// instructions, 33 passes of a comparison and its count among them (with 64 and no bisection 325, a quarter of the rows bit by
+// bit).
 template <typename T, int E, bool TOP>
 __global__ void __launch_bounds__(kTokenThreads, E > 32 && sizeof(T) == 2 ? 4 : 1) token_short(const TokenFwdArgs a) {
     constexpr int V = kVec16<T>, U = E / V;
@@ -534,7 +536,35 @@ __global__ void __launch_bounds__(kTokenThreads, E > 32 && sizeof(T) == 2 ? 4 : 
                 bound = -wave_top(larger < a.top_k ? -mine : -__builtin_inff());
             }
             collect([&](float z, int) { return z >= bound; });
-            if (count > kShortFound) {     // uniform
+            if (count > kShortMany) {      // uniform: a tighter bound, nearer to the maximum
+                if (bound == -__builtin_inff()) {          // fewer lanes than alternatives: the smallest logit above -inf
+                    float low = __builtin_inff();
+                    each([&](float z, int, bool live) { low = live && z > -__builtin_inff() ? fminf(low, z) : low; });
+                    low = -wave_top(-low);
+                    const int m = how_many([&](float z, int) { return z >= low; });
+                    if (m >= a.top_k) {
+                        bound = low;
+                        count = m;
+                    }
+                }
+                float above = bound == -__builtin_inff() ? bound : all.top;
+#pragma unroll 1
+                for (int i = 0; i < 8 && count > kShortMany && bound < above; ++i) {
+                    const float middle = 0.5f * bound + 0.5f * above;
+                    const int m = how_many([&](float z, int) { return z >= middle; });
+                    if (m >= a.top_k) {
+                        bound = middle;
+                        count = m;
+                    } else {
+                        above = middle;
+                    }
+                }
+                if (count <= kShortFound) {
+                    count = 0;
+                    collect([&](float z, int) { return z >= bound; });
+                }
+            }
+            if (count > kShortFound) {
                 // the k-th largest logit by the bits of its key, then the smallest index that leaves k of them
                 uint32_t key = 0;
 #pragma unroll 1

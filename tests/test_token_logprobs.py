@@ -165,6 +165,23 @@ def test_equal_logits_of_short_rows(V):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [65, 130, 333, 500, 1000, 2048, 4001])
+def test_many_alternatives_of_short_rows(V, dtype):
+    """Few lanes with elements, many alternatives, and rows most of which is -inf."""
+    z = make(12, V, dtype)[0]
+    z[4:8, torch.rand(V, generator=torch.Generator().manual_seed(V)) < 0.6] = -math.inf
+    z[8:10] = (z[8:10] * 4).round() / 4                        # many equal ones
+    z[10] = torch.linspace(-1000, 0, V).exp().to(z.dtype)      # bisection finds no middle
+    z[11, V // 2:] += 500
+    y = torch.zeros(12, dtype=torch.int64)
+    for k in (20, 33, 48, 64):
+        order = torch.sort(z.float(), dim=-1, descending=True, stable=True).indices[:, :k]
+        index = rl.token_logprobs_fwd(z.to(DEV), y.to(DEV), top_k=k)[4].cpu()
+        assert torch.equal(index, order), [i for i in range(12) if not torch.equal(index[i], order[i])]
+
+
+@gpu
 @pytest.mark.parametrize("rows", [1, 1200])
 def test_nan_and_infinite_logits(rows):
     V = 5000

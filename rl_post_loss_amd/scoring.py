@@ -13,7 +13,7 @@ from __future__ import annotations
 import torch
 
 from . import DTYPE, MASK_DTYPE, _check, _ws_ptr, library
-from .training import GROUP, _dense, _on, _plain, _ptr, _scratch, _stream
+from .training import GROUP, _dense, _empty, _on, _plain, _ptr, _scratch, _stream
 
 __all__ = ["token_logprobs_fwd", "token_logprobs_bwd", "fp8_quantize", "fp8_linear"]
 
@@ -80,7 +80,8 @@ def token_logprobs_fwd(logits, targets, mask=None, *, temperature=1.0, top_k=0, 
     wp, wn = _ws_ptr(ws)
     logp = torch.empty_like(y, dtype=torch.float32)
     lse, entropy = torch.empty_like(logp), torch.empty_like(logp)
-    top_logp, top_index = (logp.new_empty((*lead, top_k)), y.new_empty((*lead, top_k))) if top_k else (None, None)
+    top_logp = _empty((*lead, top_k), torch.float32, dev) if top_k else None
+    top_index = _empty((*lead, top_k), torch.int64, dev) if top_k else None
     with _on(dev):
         _check("token_logprobs_fwd", lib.token_logprobs_fwd(
             z.data_ptr(), y.data_ptr(), _ptr(m), rows, V, inner, group, stride, DTYPE[z.dtype], float(temperature), top_k,
@@ -103,7 +104,7 @@ def token_logprobs_bwd(logits, targets, mask, lse, entropy, grad_logp=None, grad
         if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.shape != lead or t.device != dev:
             raise ValueError(f"{name} must be a float32 {tuple(lead)} tensor on the logits' device")
         held[name] = _dense(t)
-    grad = torch.empty(z.shape, dtype=z.dtype, device=dev)
+    grad = _empty(z.shape, z.dtype, dev)
     with _on(dev):
         _check("token_logprobs_bwd", library().token_logprobs_bwd(
             z.data_ptr(), y.data_ptr(), _ptr(m), *(_ptr(t) for t in held.values()), rows, z.shape[-1], inner, group, stride,
@@ -132,9 +133,9 @@ def fp8_quantize(x, *, block_rows=1):
     rows = x.numel() // C
     ld = x.stride(0) if x.dim() == 2 else C
     groups = (C + GROUP - 1) // GROUP
-    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    scale = torch.empty((*x.shape[:-1], groups) if block_rows == 1 else ((rows + GROUP - 1) // GROUP, groups),
-                        dtype=torch.float32, device=x.device)
+    q = _empty(x.shape, torch.float8_e4m3fn, x.device)
+    scale = _empty((*x.shape[:-1], groups) if block_rows == 1 else ((rows + GROUP - 1) // GROUP, groups), torch.float32,
+                   x.device)
     with _on(x.device):
         _check("rlpl_fp8_quantize", library().rlpl_fp8_quantize(x.data_ptr(), rows, C, ld, DTYPE[x.dtype], block_rows,
                                                                q.data_ptr(), scale.data_ptr(), _stream(x.device)))
@@ -175,7 +176,7 @@ def fp8_linear(x, x_scale, weight, weight_scale, bias=None, *, out_dtype=torch.b
     lib = library()
     ws = _scratch(lib.fp8_linear_workspace_bytes(n, H, V), workspace, dev, "fp8_linear_workspace_bytes")
     wp, wn = _ws_ptr(ws)
-    out = torch.empty((*lead, V), dtype=out_dtype, device=dev)
+    out = _empty((*lead, V), out_dtype, dev)
     with _on(dev):
         _check("fp8_linear", lib.fp8_linear(x.data_ptr(), xs.data_ptr(), w.data_ptr(), ws_.data_ptr(), _ptr(bias), n, H, V,
                                             DTYPE[out_dtype], out.data_ptr(), wp, wn, _stream(dev)))

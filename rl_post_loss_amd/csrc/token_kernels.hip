@@ -142,10 +142,13 @@ struct Finish {
     __device__ __forceinline__ float lse(float c) const { return base.far ? base.b * (c * kLn2) + kLn2 * l2 : kLn2 * (base.bc + l2); }
 };
 
+// The target's logit, NaN without one.
 template <typename T>
-__device__ __forceinline__ void write_row(const TokenFwdArgs& a, const Row<T>& r, int64_t row, const Sums& j, const Finish& f) {
-    const int64_t y = a.targets[row];
-    a.logp[row] = y >= 0 && y < r.n ? f.logp(widen(r.p[y]), a.scale) : __builtin_nanf("");
+__device__ __forceinline__ float target_logit(const T* p, int64_t y, int32_t n) {
+    return y >= 0 && y < n ? widen(p[y]) : __builtin_nanf("");
+}
+__device__ __forceinline__ void write_row(const TokenFwdArgs& a, int64_t row, float zy, const Sums& j, const Finish& f) {
+    a.logp[row] = f.logp(zy, a.scale);
     a.lse[row] = f.lse(a.scale);
     if (a.entropy) a.entropy[row] = kLn2 * (f.l2 - j.t / j.s);
 }
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
         }
         const Finish f(all, c);
         if (tid == 0) {
-            if (a.pieces == 1) write_row(a, r, row, all, f);
+            if (a.pieces == 1) write_row(a, row, target_logit(r.p, a.targets[row], r.n), all, f);
             else a.part[item] = TokenPart{all.top, all.s, all.t, 0.0f};
         }
         if constexpr (TOP) {
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kTokenThreads, E > 32 && sizeof(T) == 2 ? 4 : 
         }
         const bool has_last = vectors * V + lane < n;
         const float last = has_last ? widen(p[vectors * V + lane]) : -__builtin_inff();
-        const float zy = lane == 0 && y >= 0 && y < n ? widen(p[y]) : __builtin_nanf("");
+        const float zy = lane == 0 ? target_logit(p, y, n) : 0.0f;
         float z[U][V], mine = last == last ? last : -__builtin_inff();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -491,11 +494,7 @@ __global__ void __launch_bounds__(kTokenThreads, E > 32 && sizeof(T) == 2 ? 4 : 
         all.s = wave_sum(all.s);
         all.t = wave_sum(all.t);
         const Finish f(all, c);
-        if (lane == 0) {
-            a.logp[row] = f.logp(zy, c);
-            a.lse[row] = f.lse(c);
-            if (a.entropy) a.entropy[row] = kLn2 * (f.l2 - all.t / all.s);
-        }
+        if (lane == 0) write_row(a, row, zy, all, f);
         if constexpr (TOP) {
             if (!(f.l2 < __builtin_inff())) {                  // a NaN or +inf among the logits
                 if (lane < a.top_k) write_top(a, row, lane, 0, f);
@@ -604,37 +603,47 @@ __global__ void __launch_bounds__(kTokenThreads) token_join(const TokenFwdArgs a
     const int tid = threadIdx.x, lane = tid & 63;
     const float c = a.scale;
     static_assert(kTokenMaxPieces <= 64, "a lane a piece");
+    constexpr int kMine = kTokenMaxKeys / kTokenThreads;
     for (int64_t row = blockIdx.x; row < a.in.rows; row += gridDim.x) {
         if (a.in.mask && !a.in.mask[row]) continue;            // written by its first piece
+        const int64_t y = a.targets[row];
         const uint64_t* keys = a.part_top + row * a.pieces * a.top_k;
-        __syncthreads();                   // the last row's LDS may still be read
+        const int all_keys = a.pieces * a.top_k;
         Sums all = Sums::none();           // each wavefront joins the pieces, a lane a piece
         if (lane < a.pieces) {
             const TokenPart p = a.part[row * a.pieces + lane];
             all = Sums{p.top, p.sum, p.weighted};
         }
-        if (tid < 128 && a.top_k > 0) {    // the first few keys of each piece, k of them at least
+        uint64_t mine[kMine];              // all loads on their way at once
+#pragma unroll
+        for (int q = 0; q < kMine; ++q) mine[q] = q * kTokenThreads + tid < all_keys ? keys[q * kTokenThreads + tid] : 0;
+        uint64_t head = 0;                 // the first few keys of each piece, k of them at least
+        if (tid < 128 && a.top_k > 0) {
             const int few = min(a.top_k, 128 / a.pieces), p = tid / few;
-            heads[tid] = p < a.pieces ? keys[p * a.top_k + tid % few] : 0;
+            if (p < a.pieces) head = keys[p * a.top_k + tid % few];
         }
+        const Row<T> r(a.in, row);
+        const float zy = tid == 0 ? target_logit(r.p, y, r.n) : 0.0f;
+        __syncthreads();                   // the last row's LDS may still be read
+        if (tid < 128) heads[tid] = head;
         if (tid == 0) count = 0;
         all.rise(wave_top(all.top), c);
         all.s = wave_sum(all.s);
         all.t = wave_sum(all.t);
         const Finish f(all, c);
-        if (tid == 0) write_row(a, Row<T>(a.in, row), row, all, f);
-        if (a.top_k == 0) continue;
-        __syncthreads();
-        const uint64_t bound = bound_of<2>(heads, a.top_k);
-        for (int i = tid; i < a.pieces * a.top_k; i += kTokenThreads) {
-            const uint64_t key = keys[i];
-            if (key >= bound) found[atomicAdd(&count, 1)] = key;
+        if (a.top_k > 0) {
+            __syncthreads();
+            const uint64_t bound = bound_of<2>(heads, a.top_k);
+#pragma unroll
+            for (int q = 0; q < kMine; ++q)
+                if (q * kTokenThreads + tid < all_keys && mine[q] >= bound) found[atomicAdd(&count, 1)] = mine[q];
+            __syncthreads();
+            for (int j = tid; j < count; j += kTokenThreads) {
+                const int rank = rank_of(found[j], found, count);
+                if (rank < a.top_k) write_top(a, row, rank, found[j], f);
+            }
         }
-        __syncthreads();
-        for (int j = tid; j < count; j += kTokenThreads) {
-            const int rank = rank_of(found[j], found, count);
-            if (rank < a.top_k) write_top(a, row, rank, found[j], f);
-        }
+        if (tid == 0) write_row(a, row, zy, all, f);
     }
 }
 

@@ -61,10 +61,14 @@ struct TokenBwdArgs {
     float inv_t;               // 1 / temperature
 };
 
-// Pieces a row is cut into by the forward, so that few rows still fill the chip: 1024 workgroups in all, each with a
+// Pieces a row is cut into by the forward, so that few long rows still fill the chip: 1024 workgroups in all, each with a
 // vector for every lane at least; with alternatives pieces of 131,072 elements at most (32 of them take 2^22 elements).
+// Rows of up to 32 vectors a lane stay whole, since a second launch takes longer than what pieces save (8 rows of bf16
+// with 20 alternatives, whole and in pieces: 32000 elements 15.3 and 17.4 us, 65536 15.4 and 17.5, 128256 18.0 and 18.3; 300
+// rows of 65536 17.2 and 21.7).
 inline int64_t token_fwd_pieces(int64_t rows, int64_t vectors, int vector, int top_k) {
     const int64_t most = (vectors + kTokenThreads - 1) / kTokenThreads;
+    if (most <= 32) return 1;
     int64_t p = 1024 / rows;
     if (p > most) p = most;
     if (p > kTokenMaxPieces) p = kTokenMaxPieces;

@@ -126,10 +126,10 @@ def patterns(V):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("V", [70, 4099, 40000])
+@pytest.mark.parametrize("V", [70, 4099, 40000, 70001])
 @pytest.mark.parametrize("copies", [1, 1030])              # a row in pieces, and a workgroup a row
 def test_patterns_of_logits(V, dtype, copies):
-    if copies > 1 and V == 40000:
+    if copies > 1 and V >= 40000:
         copies = 80                                        # 13 patterns each
     rows = patterns(V)
     z = torch.stack(list(rows.values())).to(DT[dtype])
@@ -182,11 +182,10 @@ def test_many_alternatives_of_short_rows(V, dtype):
 
 
 @gpu
-@pytest.mark.parametrize("rows", [1, 1200])
-def test_nan_and_infinite_logits(rows):
-    V = 5000
+@pytest.mark.parametrize("rows,V", [(1, 5000), (1200, 5000), (1, 70001), (3, 70001), (2, 3000)])
+def test_nan_and_infinite_logits(rows, V):
     z, y, _ = make(rows, V, "fp32")
-    for where, bad in ((4321, math.nan), (0, math.inf), (17, math.nan)):
+    for where, bad in ((V - 679, math.nan), (0, math.inf), (17, math.nan)):
         w = z.clone()
         w[0, where] = bad
         logp, lse, entropy, top, index = rl.token_logprobs_fwd(w.to(DEV), y.to(DEV), top_k=4)
@@ -208,10 +207,10 @@ def test_nan_and_infinite_logits(rows):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
-@pytest.mark.parametrize("rows", [1, 1100])
-def test_masks_of_the_types_lowest_value(rows, dtype):
+@pytest.mark.parametrize("rows,V", [(1, 5003), (1100, 5003), (2, 70003), (2, 1001)])
+def test_masks_of_the_types_lowest_value(rows, V, dtype):
     """Rows that are all of it give a uniform distribution; beside other logits it has probability 0."""
-    V, low = 5003, torch.finfo(DT[dtype]).min
+    low = torch.finfo(DT[dtype]).min
     z, y, _ = make(rows, V, dtype, seed=6)
     z[0] = low
     for T in (1.0, 0.6, 3.0):
@@ -384,8 +383,9 @@ def test_autograd_single_outputs_slices_and_tracing():
 
 
 @gpu
-def test_equal_bits_another_stream_and_a_replayed_graph():
-    z, y, mask = make(5, 30011, "fp16", masked=0.2)
+@pytest.mark.parametrize("V", [3001, 30011, 80021])      # a wavefront a row, a workgroup, pieces
+def test_equal_bits_another_stream_and_a_replayed_graph(V):
+    z, y, mask = make(5, V, "fp16", masked=0.2)
     d, t, m = z.to(DEV), y.to(DEV), mask.to(DEV)
     ref = rl.token_logprobs_fwd(d, t, m, top_k=7)
     for _ in range(5):
@@ -402,7 +402,7 @@ def test_equal_bits_another_stream_and_a_replayed_graph():
         out = rl.token_logprobs_fwd(d, t, m, top_k=7)
         dz = rl.token_logprobs_bwd(d, t, m, out[1], out[2], one, one)
     for i in range(3):
-        d.copy_(torch.randn(5, 30011, device=DEV) * (i + 1))
+        d.copy_(torch.randn(5, V, device=DEV) * (i + 1))
         graph.replay()
         torch.cuda.synchronize()
         ref = rl.token_logprobs_fwd(d, t, m, top_k=7)
@@ -412,8 +412,8 @@ def test_equal_bits_another_stream_and_a_replayed_graph():
 
 @gpu
 def test_a_given_workspace():
-    z, y, _ = make(3, 20000, "bf16")
-    nbytes = rl.library().token_logprobs_workspace_bytes(3, 20000, 9)
+    z, y, _ = make(3, 140000, "bf16")
+    nbytes = rl.library().token_logprobs_workspace_bytes(3, 140000, 9)
     ws = torch.full((nbytes + 256,), 255, dtype=torch.uint8, device=DEV)
     forward_case(z, y, 1.0, rl.token_logprobs_fwd(z.to(DEV), y.to(DEV), top_k=9, workspace=ws), 9)
     with pytest.raises(rl.RlplError):

@@ -13,7 +13,7 @@
 // A lane of a fragment takes 16-byte pieces q and q + 4 of a row's 128 bytes
 // (q = lane / 16) in both operands: which of K's elements meet is all that counts.
 //
-// Five shapes (score_abi.cpp chooses by a time model), entries by tokens.  256 x 256, the loop of
+// Six shapes (score_abi.cpp chooses by a time model), entries by tokens.  256 x 256, the loop of
 // the cross entropy's large tile: 1.03 ms for 2048 x 4096 x 128256 (2.1 PFLOP/s), 0.47
 // for 8192^3 (2.3; the library's product with one scale for each operand 0.86 to 0.98 and
 // 0.36 to 0.38 ms).  A step has 2048 cycles of matrix instructions (1.47 us alone, 1.7 to
@@ -22,8 +22,8 @@
 // x 4096 46 us (1.5 PFLOP/s).  The projection's ring has a third stage at 128 x 128, where
 // it comes from memory: 128 x 4096 x 128256 136 us instead of 149 (4 TB/s).  128 x 64 with three stages
 // of both operands for up to 128 rows of a long projection (128 x 8192 x 30000 57 us; 67 by 64 x 64, 81 by
-// 128 x 128).  64 x 64 with K shared by four groups of wavefronts, for tiles too few to fill the chip: a
-// step of a workgroup alone is bound by its instructions, not by its copies (more stages change
+// 128 x 128).  64 x 64 with K shared by four or two groups of wavefronts, for tiles too few to fill the
+// chip: a step of a workgroup alone is bound by its instructions, not by its copies (more stages change
 // nothing), and four groups take 1.1 us for four steps of 0.6.  float32 outputs: 8192^3 0.97 ms at 128 x 128
 // (1.13 PFLOP/s of 16-bit instructions; 1.26 ms at 64 x 64, whose wavefronts convert twice as much for each product).
 #include <hip/hip_runtime.h>
@@ -66,10 +66,11 @@ using Large = Fp8Shape<256, 256, 2, 4, 3, 2>;
 using Middle = Fp8Shape<128, 128, 2, 2, 3, 2>;
 using Small = Fp8Shape<64, 64, 2, 2, 2, 2>;
 using Deep = Fp8Shape<64, 64, 2, 2, 2, 2, 4>;
+using Twice = Fp8Shape<64, 64, 2, 2, 2, 2, 2>;
 using Narrow = Fp8Shape<128, 64, 2, 2, 3, 3>;
 static_assert(Large::launched_as(kFp8Shapes[kFp8Large]) && Middle::launched_as(kFp8Shapes[kFp8Middle]) &&
               Small::launched_as(kFp8Shapes[kFp8Small]) && Deep::launched_as(kFp8Shapes[kFp8Deep]) &&
-              Narrow::launched_as(kFp8Shapes[kFp8Narrow]), "as launched");
+              Narrow::launched_as(kFp8Shapes[kFp8Narrow]) && Twice::launched_as(kFp8Shapes[kFp8Twice]), "as launched");
 
 // A fragment from the two pieces that a lane read of it.
 template <typename F>
@@ -388,10 +389,12 @@ const void* pick_fp8_tile(int out_dtype, int kind) {
         return kind == kFp8Small    ? reinterpret_cast<const void*>(&fp8_tile<float, Small>)
                : kind == kFp8Middle ? reinterpret_cast<const void*>(&fp8_tile<float, Middle>)
                : kind == kFp8Deep   ? reinterpret_cast<const void*>(&fp8_tile<float, Deep>)
+               : kind == kFp8Twice  ? reinterpret_cast<const void*>(&fp8_tile<float, Twice>)
                : kind == kFp8Narrow ? reinterpret_cast<const void*>(&fp8_tile<float, Narrow>)
                                     : nullptr;
     switch (kind) {
     case kFp8Deep: return tile_of_type<Deep>(out_dtype);
+    case kFp8Twice: return tile_of_type<Twice>(out_dtype);
     case kFp8Narrow: return tile_of_type<Narrow>(out_dtype);
     case kFp8Small: return tile_of_type<Small>(out_dtype);
     case kFp8Middle: return tile_of_type<Middle>(out_dtype);

@@ -45,9 +45,9 @@ constexpr int kTurnRows = 64, kTurnCols = 4;   // of a workgroup
 struct Fp8TileShape {
     int vocab, tokens, threads, lds;
 };
-enum { kFp8Small = 0, kFp8Narrow = 1, kFp8Middle = 2, kFp8Large = 3, kFp8Deep = 4, kFp8Kinds = 5 };   // no large float32 one
+enum { kFp8Small = 0, kFp8Narrow = 1, kFp8Middle = 2, kFp8Large = 3, kFp8Deep = 4, kFp8Twice = 5, kFp8Kinds = 6 };   // no large float32 one
 constexpr Fp8TileShape kFp8Shapes[] = {{64, 64, 256, 32 * 1024}, {128, 64, 256, 72 * 1024}, {128, 128, 256, 80 * 1024},
-                                       {256, 256, 512, 160 * 1024}, {64, 64, 1024, 128 * 1024}};
+                                       {256, 256, 512, 160 * 1024}, {64, 64, 1024, 128 * 1024}, {64, 64, 512, 64 * 1024}};
 const void* pick_fp8_tile(int out_dtype, int kind);
 
 // Up to 16 rows: a workgroup takes 64 vocabulary entries, or 32 or 16, its four wavefronts every fourth block of K each.

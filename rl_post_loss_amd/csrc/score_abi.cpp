@@ -104,10 +104,12 @@ double fp8_time(int kind, int64_t n, int64_t blocks, int64_t vocab, bool wide) {
     return busy > stream ? busy : stream;
 }
 int fp8_kind(int64_t n, int64_t blocks, int64_t vocab, int out_dtype) {
-    // A small tile for each compute unit at most: four groups of wavefronts share K (33 x 8192 x 4096: 21 us instead of 41,
-    // 64 x 4096 x 16384 17 instead of 24, both with 256 tiles or fewer; 376 of them 26 instead of 24).
+    // One small tile for each compute unit at most, or two: four groups of wavefronts share K, or two (33 x 8192 x 4096, 64
+    // tiles: 40, 27 and 21 us with one, two and four; 64 x 8192 x 8192, 128 tiles: 41, 29 and 24; 128 x 8192 x 12000, 376 tiles:
+    // 43, 35 and 46; 64 x 4096 x 32000, 500 tiles: 24.5, 22.7 and 29.7; 700 x 4096 x 3000, 517 tiles: 25, 31 and 37).
     const Fp8TileShape& small = kFp8Shapes[kFp8Small];
-    if (div_up(vocab, small.vocab) * div_up(n, small.tokens) <= 256 && blocks >= 8) return kFp8Deep;
+    const int64_t tiles = div_up(vocab, small.vocab) * div_up(n, small.tokens);
+    if (blocks >= 8 && tiles <= 512) return tiles <= 256 ? kFp8Deep : kFp8Twice;
     const bool wide = out_dtype == RLPL_F32;
     int best = kFp8Small;
     for (int kind = kFp8Narrow; kind <= (wide ? kFp8Middle : kFp8Large); ++kind)

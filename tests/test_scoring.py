@@ -71,6 +71,25 @@ def test_a_captured_scoring_pass():
         assert torch.equal(s["logits"], ref["logits"]) and all(torch.equal(a, b) for a, b in zip(s["out"], ref["out"]))
 
 
+def test_two_scoring_passes_at_once():
+    """Each on a stream of its own, with workspaces of their own: the bits of one after the other."""
+    passes = []
+    for rows, H, V, top_k in ((700, 1024, 20011, 5), (33, 2048, 70001, 64)):
+        head, inputs = Head(H, V, seed=V), batch((rows,), H, V, 7)
+        passes.append((head, inputs, top_k, head.score(*inputs, top_k), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for head, inputs, top_k, _, stream in passes:
+            with torch.cuda.stream(stream):
+                got.append([head.score(*inputs, top_k) for _ in range(2)])
+        torch.cuda.synchronize()
+        for results, (_, _, _, ref, _) in zip(got, passes):
+            for s in results:
+                assert torch.equal(s["logits"], ref["logits"]) and torch.equal(s["q"].view(torch.uint8), ref["q"].view(torch.uint8))
+                assert all(torch.equal(a, b) for a, b in zip(s["out"], ref["out"]))
+
+
 @pytest.mark.parametrize("max_norm", [1e-3, 1e6])
 def test_a_policy_step_with_an_entropy_bonus(max_norm):
     """Gradients of every stage through the autograd forms, clipped by the factor that the optimizer takes."""

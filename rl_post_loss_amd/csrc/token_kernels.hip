@@ -631,7 +631,9 @@ __global__ void __launch_bounds__(kTokenThreads) token_join(const TokenFwdArgs a
         all.s = wave_sum(all.s);
         all.t = wave_sum(all.t);
         const Finish f(all, c);
-        if (a.top_k > 0) {
+        if (!(f.l2 < __builtin_inff())) {  // a NaN or +inf among the logits: pieces of NaN alone may have left no keys
+            if (tid < a.top_k) write_top(a, row, tid, 0, f);
+        } else if (a.top_k > 0) {
             __syncthreads();
             const uint64_t bound = bound_of<2>(heads, a.top_k);
 #pragma unroll

@@ -137,7 +137,11 @@ struct Finish {
     Base base;
     float l2;                  // log2 s
     __device__ __forceinline__ Finish(const Sums& a, float c) : base(a.top, c), l2(__log2f(a.s)) {}
-    __device__ __forceinline__ float logp(float z, float c) const { return kLn2 * (base.exponent(z, c) - l2); }
+    // An exponent may be past float32 where ln 2 times it is not (a token that the lowest value of its type rules out).
+    __device__ __forceinline__ float logp(float z, float c) const {
+        const float l = kLn2 * (base.exponent(z, c) - l2);
+        return l == -__builtin_inff() ? 2.0f * ((0.5f * z - 0.5f * base.b) * (c * kLn2)) : l;
+    }
     // b c may be too large where b / T = ln 2 b c is not.
     __device__ __forceinline__ float lse(float c) const { return base.far ? base.b * (c * kLn2) + kLn2 * l2 : kLn2 * (base.bc + l2); }
 };

@@ -63,27 +63,37 @@ __device__ __forceinline__ float wave_top(float v) {
 
 // Exponents count from c b, rounded, as c z - c b by one operation, the same for a row's sums and its results, so that the
 // rounding falls out of them.  Where c b is so large that its rounding is not small (a row of the type's lowest value; a tiny
-// temperature) they are (z - b) c.
+// temperature) they are (z - b) c.  Either way c (z - from) - bc.
 struct Base {
-    float b, bc;
-    bool far;
-    __device__ __forceinline__ Base(float top, float c) : b(base_of(top)), bc(c * b), far(!(fabsf(bc) < 0x1p20f)) {}
-    __device__ __forceinline__ float exponent(float z, float c) const { return far ? (z - b) * c : fmaf(z, c, -bc); }
+    float b, from, bc;
+    __device__ __forceinline__ Base(float top, float c) : b(base_of(top)) {
+#pragma clang fp contract(off)
+        const float product = c * b;       // as it is rounded here, wherever it is used
+        const bool near = fabsf(product) < 0x1p20f;
+        from = near ? 0.0f : b;
+        bc = near ? product : 0.0f;
+    }
+    __device__ __forceinline__ bool far() const { return from != 0.0f; }
+    __device__ __forceinline__ float exponent(float z, float c) const { return fmaf(z - from, c, -bc); }
+    // What exponents that count from here grow by when they count from `to`.  With the rounded products' difference nothing of
+    // their rounding is left; c (b - b') gave log-probabilities off by 9e-6 and 1e-4 for logits around 300 and 3000.
+    __device__ __forceinline__ float less(const Base& to, float c) const { return fmaf(from - to.from, c, bc - to.bc); }
 };
 
 // Sums that count from `top`.
 struct Sums {
     float top, s, t;
     static __device__ __forceinline__ Sums none() { return Sums{-__builtin_inff(), 0.0f, 0.0f}; }
-    // Counts from a larger maximum.
-    __device__ __forceinline__ void rise(float to, float c) {
+    // Counts from a larger maximum, whose base is `there`; `here` is the present one's.
+    __device__ __forceinline__ void rise(float to, const Base& here, const Base& there, float c) {
         const bool none = top == -__builtin_inff();            // nothing but NaN is in the sums
-        const float d = none ? 0.0f : hold(c * (base_of(top) - base_of(to)));
+        const float d = none ? 0.0f : hold(here.less(there, c));
         const float f = none ? 0.0f : exp2_hw(d);
         t = fmaf(d, s, t) * f;
         s *= f;
         top = to;
     }
+    __device__ __forceinline__ void rise(float to, float c) { rise(to, Base(top, c), Base(to, c), c); }
     // One more term, with its exponent.
     __device__ __forceinline__ void add(float d) {
         d = hold(d);
@@ -143,7 +153,7 @@ struct Finish {
         return l == -__builtin_inff() ? 2.0f * ((0.5f * z - 0.5f * base.b) * (c * kLn2)) : l;
     }
     // b c may be too large where b / T = ln 2 b c is not.
-    __device__ __forceinline__ float lse(float c) const { return base.far ? base.b * (c * kLn2) + kLn2 * l2 : kLn2 * (base.bc + l2); }
+    __device__ __forceinline__ float lse(float c) const { return base.far() ? base.b * (c * kLn2) + kLn2 * l2 : kLn2 * (base.bc + l2); }
 };
 
 // The target's logit, NaN without one.
@@ -261,6 +271,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
         const int32_t first = int32_t(piece * a.piece_vectors) < r.vectors ? int32_t(piece * a.piece_vectors) : r.vectors;
         const int32_t last = piece == a.pieces - 1 || r.vectors - first < a.piece_vectors ? r.vectors : first + int32_t(a.piece_vectors);
         Sums mine = Sums::none();
+        Base base(mine.top, c);
         int blocks = 0;                    // the lane's, of U vectors each
         const auto block = [&](const u32x4 (&raw)[U], int live) {
             float z[U][V];
@@ -276,13 +287,16 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
             }
             if constexpr (TOP) tops[blocks][tid] = top;
             ++blocks;
-            if (top > mine.top) mine.rise(top, c);
-            const Base base(mine.top, c);
-            if (base.far) {
+            if (top > mine.top) {
+                const Base there(top, c);
+                mine.rise(top, base, there, c);
+                base = there;
+            }
+            if (base.far()) {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int k = 0; k < V; ++k) mine.add((z[u][k] - base.b) * c);
+                    for (int k = 0; k < V; ++k) mine.add((z[u][k] - base.from) * c);
             } else {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -484,11 +498,11 @@ __global__ void __launch_bounds__(kTokenThreads, E > 32 && sizeof(T) == 2 ? 4 : 
         Sums all{wave_top(mine), 0.0f, 0.0f};
         const Base base(all.top, c);
         all.add(base.exponent(last, c));
-        if (base.far) {
+        if (base.far()) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int k = 0; k < V; ++k) all.add((z[u][k] - base.b) * c);
+                for (int k = 0; k < V; ++k) all.add((z[u][k] - base.from) * c);
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u)

@@ -581,7 +581,9 @@ int rlpl_grad_scale(void* const* grads, const int64_t* sizes, const int32_t* dty
  * A row whose mask byte is zero is not read: its outputs are 0, its indices -1, its gradients +0.  A target outside
  * [0, vocab) gives logp = NaN and no one-hot term.  A logit of -inf has probability 0; a row of them
  * alone, or with a NaN or +inf, gives NaN (and indices of -1 but for the row of -inf).  One pass over the logits, sums in
- * float32 in a fixed order.  The gradient's p are as exact as lse, which is held in float32: off by 2^-24 |lse|.
+ * float32 in a fixed order.  The gradient's p are as exact as lse, which is held in float32: off by 2^-24 |lse|, up to
+ * |lse| = 8192.  Beyond (a row of the type's lowest value alone) p come from the row's sums formed anew, for which every
+ * workgroup of the row reads all of it.
  *
  * logits      : `dtype`, row r's vocab elements side by side from group_stride (r / inner) + row_stride (r % inner)
  *               elements on: inner = rows and row_stride = vocab for a dense (rows, vocab), group_stride =

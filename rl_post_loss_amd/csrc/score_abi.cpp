@@ -50,8 +50,9 @@ bool token_strides_ok(int64_t rows, int64_t inner, int64_t group_stride, int64_t
     const __int128 last = __int128((rows - 1) / inner) * group_stride + __int128(inner - 1) * row_stride;
     return last < kMaxElements;
 }
+float token_scale(float t) { return float(1.4426950408889634 / double(t)); }
 // T such that log2(e) / T is a float.
-bool token_temperature_ok(float t) { return std::isfinite(t) && t > 0.0f && std::isfinite(float(1.4426950408889634 / double(t))); }
+bool token_temperature_ok(float t) { return std::isfinite(t) && t > 0.0f && std::isfinite(token_scale(t)); }
 int token_vector(int dtype) { return 16 / int(dtype_bytes(dtype)); }
 int64_t token_vectors(int64_t vocab, int dtype) { return vocab / token_vector(dtype); }
 
@@ -163,7 +164,7 @@ int token_logprobs_fwd(const void* logits, const int64_t* targets, const void* m
     a.pieces = vocab <= kTokenShort ? 1 : int32_t(token_fwd_pieces(rows, vectors, token_vector(dtype), int(top_k)));
     a.piece_vectors = div_up(vectors > 0 ? vectors : 1, a.pieces);
     a.top_k = int32_t(top_k);
-    a.scale = float(1.4426950408889634 / double(temperature));
+    a.scale = token_scale(temperature);
     a.part = static_cast<TokenPart*>(workspace);
     a.part_top = reinterpret_cast<uint64_t*>(static_cast<char*>(workspace) +
                                              up256(size_t(rows) * size_t(a.pieces) * sizeof(TokenPart)));
@@ -201,6 +202,7 @@ int token_logprobs_bwd(const void* logits, const int64_t* targets, const void* m
     a.pieces = int32_t(div_up(vectors > 0 ? vectors : 1, 8 * lanes));
     a.piece_vectors = div_up(vectors > 0 ? vectors : 1, a.pieces);
     a.inv_t = float(1.0 / double(temperature));
+    a.scale = token_scale(temperature);
     return enqueue(pick_token_bwd(dtype, vocab), a, dim3(capped(div_up(rows * a.pieces, kTokenThreads / lanes), kTokenMaxGrid)),
                    kTokenThreads, stream);
 }

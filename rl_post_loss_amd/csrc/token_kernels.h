@@ -18,6 +18,8 @@ constexpr int kTokenBlocks = 16;           // blocks of 32 elements that a lane 
 // (26.1), 2048 27 (36), 4001 59 (52)).
 constexpr int64_t kTokenShort = 4096;
 constexpr int64_t kTokenShortBwd = 2048;
+// From this |lse| on, its rounding to float32 is half a step of a float16 gradient (2^-11), and the backward pass does without it.
+constexpr float kTokenFar = 8192.0f;
 constexpr int64_t kTokenMaxGrid = 1 << 20; // workgroups of a launch (they stride over the rest)
 
 // Where the rows lie: row r at group_stride (r / inner) + row_stride (r % inner) elements.
@@ -59,6 +61,7 @@ struct TokenBwdArgs {
     int64_t piece_vectors;
     int32_t pieces;
     float inv_t;               // 1 / temperature
+    float scale;               // log2(e) / temperature
 };
 
 // Pieces a row is cut into by the forward, so that few long rows still fill the chip: 1024 workgroups in all, each with a

@@ -101,7 +101,28 @@ struct Sums {
         s += e;
         t = fmaf(e, d, t);
     }
+    // A wavefront's lanes joined, in each of them.
+    __device__ __forceinline__ void join_lanes(float c) {
+        rise(wave_top(top), c);
+        s = wave_sum(s);
+        t = wave_sum(t);
+    }
 };
+
+// The workgroup's wavefronts' sums, in their order.
+__device__ __forceinline__ Sums join_waves(const Sums* joined, float c) {
+    Sums all = joined[0];
+#pragma unroll
+    for (int w = 1; w < kTokenWaves; ++w) {
+        Sums o = joined[w];
+        const float higher = fmaxf(all.top, o.top);
+        all.rise(higher, c);
+        o.rise(higher, c);
+        all.s += o.s;
+        all.t += o.t;
+    }
+    return all;
+}
 
 // A logit's place among others: larger keys are larger logits, of equal ones the one of the lower index.  Never 0.
 __device__ __forceinline__ uint64_t key_of(float z, uint32_t index) {
@@ -331,10 +352,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
             all.add(Base(all.top, c).exponent(z, c));
         }
         // lanes to wavefronts to the workgroup
-        const float top = wave_top(all.top);
-        all.rise(top, c);
-        all.s = wave_sum(all.s);
-        all.t = wave_sum(all.t);
+        all.join_lanes(c);
         __syncthreads();                   // the last row's LDS may still be read
         if ((tid & 63) == 0) joined[tid >> 6] = all;
         if (tid == 0) {
@@ -343,16 +361,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_fwd(const TokenFwdArgs a)
         }
         if constexpr (TOP) leave_heads(heads, blocks > 0 ? key_of(mine.top, uint32_t(tid)) : 0, last - first, a.top_k);
         __syncthreads();
-        all = joined[0];
-#pragma unroll
-        for (int w = 1; w < kTokenWaves; ++w) {
-            Sums o = joined[w];
-            const float higher = fmaxf(all.top, o.top);
-            all.rise(higher, c);
-            o.rise(higher, c);
-            all.s += o.s;
-            all.t += o.t;
-        }
+        all = join_waves(joined, c);
         const Finish f(all, c);
         if (tid == 0) {
             if (a.pieces == 1) write_row(a, row, target_logit(r.p, a.targets[row], r.n), all, f);
@@ -645,9 +654,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_join(const TokenFwdArgs a
         __syncthreads();                   // the last row's LDS may still be read
         if (tid < 128) heads[tid] = head;
         if (tid == 0) count = 0;
-        all.rise(wave_top(all.top), c);
-        all.s = wave_sum(all.s);
-        all.t = wave_sum(all.t);
+        all.join_lanes(c);
         const Finish f(all, c);
         if (!(f.l2 < __builtin_inff())) {  // a NaN or +inf among the logits: pieces of NaN alone may have left no keys
             if (tid < a.top_k) write_top(a, row, tid, 0, f);
@@ -667,13 +674,43 @@ __global__ void __launch_bounds__(kTokenThreads) token_join(const TokenFwdArgs a
     }
 }
 
+// A row's sums, in each of the LANES that have it.
+template <typename T, int LANES>
+__device__ __forceinline__ Sums sums_of_row(const T* x, int32_t n, int tid, float c, Sums* joined) {
+    constexpr int V = kVec16<T>;
+    const int32_t vectors = n / V;
+    Sums all = Sums::none();
+    const auto add = [&](float z) {
+        if (z > all.top) all.rise(z, c);
+        all.add(Base(all.top, c).exponent(z, c));
+    };
+#pragma unroll 1
+    for (int32_t i = tid; i < vectors; i += LANES) {
+        float z[V];
+        widen_raw<T>(load_word<typename Unaligned16<T>::type, true>(x + int64_t(i) * V), z);
+#pragma unroll
+        for (int k = 0; k < V; ++k) add(z[k]);
+    }
+    if (vectors * V + tid < n) add(widen(x[vectors * V + tid]));
+    all.join_lanes(c);
+    if constexpr (LANES > 64) {
+        __syncthreads();                   // the last row's LDS may still be read
+        if ((tid & 63) == 0) joined[tid >> 6] = all;
+        __syncthreads();
+        all = join_waves(joined, c);
+    }
+    return all;
+}
+
 // The gradient of sum(grad_logp logp + grad_entropy H): with p = exp(z / T - lse),
 //   dz_v = (grad_logp ((v == y) - p_v) - grad_entropy p_v (log p_v + H)) / T.
 // Vectors are cut where the gradient's row is aligned, and stored past the caches, which then hold more of the logits:
-// 3000 x 128256 bf16 287 us (5.4 TB/s) instead of 303, 4096 x 32000 79 instead of 106.
+// 3000 x 128256 bf16 287 us (5.4 TB/s) instead of 303, 4096 x 32000 79 instead of 106.  Rows whose lse is so large that float32
+// does not hold its fraction (a mask that leaves nothing but the type's lowest value) form their sums anew.
 template <typename T, int LANES>
 __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a) {
     constexpr int V = kVec16<T>, ITEMS = kTokenThreads / LANES;
+    __shared__ Sums joined[LANES > 64 ? kTokenWaves : 1];
     const int tid = threadIdx.x % LANES, which = __builtin_amdgcn_readfirstlane(int(threadIdx.x) / LANES);
     for (int64_t item = int64_t(blockIdx.x) * ITEMS + which; item < a.in.rows * a.pieces; item += int64_t(gridDim.x) * ITEMS) {
         const int64_t row = a.pieces == 1 ? item : item / a.pieces;
@@ -698,20 +735,29 @@ __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a)
         const float k0 = a.grad_entropy ? fmaf(h, a.entropy[row], g) : g;      // g + h H
         const int64_t target = a.targets[row];
         const int32_t y = target >= 0 && target < n ? int32_t(target) : -1;
-        const auto value = [&](float z, int32_t v) {
-            const float l = hold(fmaf(z, a.inv_t, -lse));
-            const float p = exp2_hw(l * kLog2e);
-            return a.inv_t * ((v == y ? g : 0.0f) - p * fmaf(h, l, k0));
-        };
-        if (piece == 0 && tid < edges) out[edge] = T(value(widen(x[edge]), edge));
+        // The row's gradient, from its elements' log-probabilities.
+        const auto write = [&](auto logp) {
+            const auto value = [&](float z, int32_t v) {
+                const float l = hold(logp(z));
+                const float p = exp2_hw(l * kLog2e);
+                return a.inv_t * ((v == y ? g : 0.0f) - p * fmaf(h, l, k0));
+            };
+            if (piece == 0 && tid < edges) out[edge] = T(value(widen(x[edge]), edge));
 #pragma unroll 4
-        for (int32_t i = first + tid; i < last; i += LANES) {
-            const int32_t v = head + i * V;
-            float z[V];
-            widen_raw<T>(load_word<typename Unaligned16<T>::type, true>(x + v), z);
+            for (int32_t i = first + tid; i < last; i += LANES) {
+                const int32_t v = head + i * V;
+                float z[V];
+                widen_raw<T>(load_word<typename Unaligned16<T>::type, true>(x + v), z);
 #pragma unroll
-            for (int k = 0; k < V; ++k) z[k] = value(z[k], v + k);
-            __builtin_nontemporal_store(narrow_raw<T>(z), reinterpret_cast<u32x4*>(out + v));
+                for (int k = 0; k < V; ++k) z[k] = value(z[k], v + k);
+                __builtin_nontemporal_store(narrow_raw<T>(z), reinterpret_cast<u32x4*>(out + v));
+            }
+        };
+        if (fabsf(lse) < kTokenFar || lse != lse) {
+            write([&](float z) { return fmaf(z, a.inv_t, -lse); });
+        } else {
+            const Finish f(sums_of_row<T, LANES>(x, n, tid, a.scale, joined), a.scale);
+            write([&](float z) { return kLn2 * (f.base.exponent(z, a.scale) - f.l2); });
         }
     }
 }

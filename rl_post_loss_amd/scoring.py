@@ -92,7 +92,8 @@ def token_logprobs_fwd(logits, targets, mask=None, *, temperature=1.0, top_k=0, 
 def token_logprobs_bwd(logits, targets, mask, lse, entropy, grad_logp=None, grad_entropy=None, *, temperature=1.0):
     """The gradient of sum(grad_logp * logp) + sum(grad_entropy * entropy) with respect to the logits: dense, of their
     shape and dtype.  logits, targets, mask and temperature as in the forward, lse and entropy (float32) what it gave;
-    entropy may be None without a grad_entropy; the two gradients are float32 of the leading shape, or None (zeros)."""
+    entropy may be None without a grad_entropy; the two gradients are float32 of the leading shape, or None (zeros).
+    Probabilities are as exact as lse (2^-24 |lse|), and formed anew where |lse| is 8192 or more."""
     z, y, m, (rows, inner, group, stride) = _token_operands(logits, targets, mask)
     lead, dev = z.shape[:-1], z.device
     held = {"lse": lse, "entropy": entropy, "grad_logp": grad_logp, "grad_entropy": grad_entropy}

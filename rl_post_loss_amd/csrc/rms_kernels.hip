@@ -14,7 +14,8 @@
 // With a residual, in 8 bits, 32768 x 4096 bf16 take 160 us (5.9 TB/s of 0.94 GB);
 // backward 16384 x 4096 96 us (5.6 TB/s of 0.54 GB with the stream's gradient) and 4.5 for the sum over
 // workgroups.  Rows whose elements start between two dwords (16-bit types, odd
-// lengths) take 1.2 to 1.4 times as long as those of even ones (30000 x 4001: forward 106 us, 4002: 89).
+// lengths) take 1.2 to 1.4 times as long as those of even ones (30000 x 4001: forward 105 us, 4002: 87; backward 218 and 162,
+// 296 and 233 with the stream's gradient; float32 rows of 4001, whose accesses start at dwords, backward 332, of 4000 322).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -72,7 +72,8 @@ def token_logprobs_fwd(logits, targets, mask=None, *, temperature=1.0, top_k=0, 
     rows take two strides at most (``logits[:, :-1]`` is not copied); targets int64 of the leading shape; mask bool, int8
     or uint8 of it, or None: rows of a zero are not read, and give 0 (indices -1).  logp, lse and entropy are float32 of
     the leading shape; top_logp (float32) and top_index (int64) have top_k <= 64 more columns (V up to 2^22 then), in falling
-    order, the lowest index first among equal logits.  A target outside [0, V) gives logp = NaN; logits of -inf have probability 0."""
+    order, the lowest index first among equal logits.  A target outside [0, V) gives logp = NaN; logits of -inf have probability 0.
+    A row with a NaN or +inf gives NaN and indices of -1, one of -inf alone an lse of -inf and NaN in the other floats."""
     z, y, m, (rows, inner, group, stride) = _token_operands(logits, targets, mask)
     V, lead, dev, lib = z.shape[-1], z.shape[:-1], z.device, library()
     top_k = int(top_k)
@@ -157,7 +158,12 @@ def fp8_linear(x, x_scale, weight, weight_scale, bias=None, *, out_dtype=torch.b
     """(x * x_scale) . (weight * weight_scale)^T + bias of 8-bit operands with a scale for each block of 128: the logits
     of an output projection.  x (*, H) and weight (V, H) float8_e4m3fn, H a multiple of 16; x_scale float32
     (*, ceil(H / 128)), weight_scale float32 (ceil(V / 128), ceil(H / 128)), as ``rms_norm_fp8`` and ``fp8_quantize`` give
-    them; bias (V,) of out_dtype, or None.  The result is (*, V) of out_dtype: bfloat16, float16 or float32."""
+    them; bias (V,) of out_dtype, or None.  The result is (*, V) of out_dtype: bfloat16, float16 or float32.
+
+    Sums are float32; for 16-bit outputs each aligned eight of K's products first loses what lies below 2^-13 of the largest of
+    them (1.5e-5 of ordinary results, more beside an outlier column); float32 outputs lose nothing.  x and weight are
+    read where they lie if they are dense and 16-byte aligned; otherwise each call copies them, a slice of a projection
+    as well: make such a weight dense once."""
     if not isinstance(x, torch.Tensor) or not isinstance(weight, torch.Tensor) or x.dim() < 1 or weight.dim() != 2 \
             or x.shape[-1] != weight.shape[1] or x.device != weight.device:
         raise ValueError("x (*, H) and weight (V, H) must be tensors that agree in H and device")

@@ -73,6 +73,13 @@ struct Base {
         from = near ? 0.0f : b;
         bc = near ? product : 0.0f;
     }
+    // Of a wavefront's one maximum, in scalar registers.
+    __device__ __forceinline__ Base uniform() const {
+        const auto one = [](float v) { return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v))); };
+        Base u = *this;
+        u.b = one(b), u.from = one(from), u.bc = one(bc);
+        return u;
+    }
     __device__ __forceinline__ bool far() const { return from != 0.0f; }
     __device__ __forceinline__ float exponent(float z, float c) const { return fmaf(z - from, c, -bc); }
     // What exponents that count from here grow by when they count from `to`.  With the rounded products' difference nothing of
@@ -167,7 +174,8 @@ struct Row {
 struct Finish {
     Base base;
     float l2;                  // log2 s
-    __device__ __forceinline__ Finish(const Sums& a, float c) : base(a.top, c), l2(__log2f(a.s)) {}
+    __device__ __forceinline__ Finish(const Base& base, float s) : base(base), l2(__log2f(s)) {}
+    __device__ __forceinline__ Finish(const Sums& a, float c) : Finish(Base(a.top, c), a.s) {}
     // An exponent may be past float32 where ln 2 times it is not (a token that the lowest value of its type rules out).
     __device__ __forceinline__ float logp(float z, float c) const {
         const float l = kLn2 * (base.exponent(z, c) - l2);
@@ -505,7 +513,7 @@ __global__ void __launch_bounds__(kTokenThreads, E > 32 && sizeof(T) == 2 ? 4 : 
             }
         }
         Sums all{wave_top(mine), 0.0f, 0.0f};
-        const Base base(all.top, c);
+        const Base base = Base(all.top, c).uniform();
         all.add(base.exponent(last, c));
         if (base.far()) {
 #pragma unroll
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(kTokenThreads, E > 32 && sizeof(T) == 2 ? 4 : 
         }
         all.s = wave_sum(all.s);
         all.t = wave_sum(all.t);
-        const Finish f(all, c);
+        const Finish f(base, all.s);
         if (lane == 0) write_row(a, row, zy, all, f);
         if constexpr (TOP) {
             if (!(f.l2 < __builtin_inff())) {                  // a NaN or +inf among the logits

@@ -20,6 +20,9 @@ constexpr int64_t kTokenShort = 4096;
 constexpr int64_t kTokenShortBwd = 2048;
 // From this |lse| on, its rounding to float32 is half a step of a float16 gradient (2^-11), and the backward pass does without it.
 constexpr float kTokenFar = 8192.0f;
+// Such a row is shared by this many workgroups at most, since each of them reads all of it (a row of 2^31 elements has 262,144
+// pieces otherwise).
+constexpr int kTokenFarPieces = 1024;
 constexpr int64_t kTokenMaxGrid = 1 << 20; // workgroups of a launch (they stride over the rest)
 
 // Where the rows lie: row r at group_stride (r / inner) + row_stride (r % inner) elements.

@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a)
         if (head > n) head = n;
         const int32_t vectors = (n - head) / V, edges = n - vectors * V;
         const int32_t first = int32_t(piece * a.piece_vectors) < vectors ? int32_t(piece * a.piece_vectors) : vectors;
-        const int32_t last = piece == a.pieces - 1 || vectors - first < a.piece_vectors ? vectors : first + int32_t(a.piece_vectors);
+        int32_t last = piece == a.pieces - 1 || vectors - first < a.piece_vectors ? vectors : first + int32_t(a.piece_vectors);
         const int32_t edge = tid < head ? tid : tid + vectors * V;
         if (a.in.mask && !a.in.mask[row]) {
             if (piece == 0 && tid < edges) out[edge] = T(0.0f);
@@ -743,29 +743,37 @@ __global__ void __launch_bounds__(kTokenThreads) token_bwd(const TokenBwdArgs a)
         const float k0 = a.grad_entropy ? fmaf(h, a.entropy[row], g) : g;      // g + h H
         const int64_t target = a.targets[row];
         const int32_t y = target >= 0 && target < n ? int32_t(target) : -1;
-        // The row's gradient, from its elements' log-probabilities.
-        const auto write = [&](auto logp) {
-            const auto value = [&](float z, int32_t v) {
-                const float l = hold(logp(z));
-                const float p = exp2_hw(l * kLog2e);
-                return a.inv_t * ((v == y ? g : 0.0f) - p * fmaf(h, l, k0));
-            };
-            if (piece == 0 && tid < edges) out[edge] = T(value(widen(x[edge]), edge));
-#pragma unroll 4
-            for (int32_t i = first + tid; i < last; i += LANES) {
-                const int32_t v = head + i * V;
-                float z[V];
-                widen_raw<T>(load_word<typename Unaligned16<T>::type, true>(x + v), z);
-#pragma unroll
-                for (int k = 0; k < V; ++k) z[k] = value(z[k], v + k);
-                __builtin_nontemporal_store(narrow_raw<T>(z), reinterpret_cast<u32x4*>(out + v));
-            }
+        // Of an element with log-probability l.
+        const auto value = [&](float l, int32_t v) {
+            l = hold(l);
+            const float p = exp2_hw(l * kLog2e);
+            return a.inv_t * ((v == y ? g : 0.0f) - p * fmaf(h, l, k0));
         };
-        if (fabsf(lse) < kTokenFar || lse != lse) {
-            write([&](float z) { return fmaf(z, a.inv_t, -lse); });
-        } else {
+        const auto write_edge = [&](auto logp) {
+            if (piece == 0 && tid < edges) out[edge] = T(value(logp(widen(x[edge])), edge));
+        };
+        const auto write_vector = [&](int32_t i, auto logp) {
+            const int32_t v = head + i * V;
+            float z[V];
+            widen_raw<T>(load_word<typename Unaligned16<T>::type, true>(x + v), z);
+#pragma unroll
+            for (int k = 0; k < V; ++k) z[k] = value(logp(z[k]), v + k);
+            __builtin_nontemporal_store(narrow_raw<T>(z), reinterpret_cast<u32x4*>(out + v));
+        };
+        const int run = (a.pieces + kTokenFarPieces - 1) / kTokenFarPieces;
+        if (__builtin_expect(!(fabsf(lse) >= kTokenFar), 1)) {
+            const auto logp = [&](float z) { return fmaf(z, a.inv_t, -lse); };
+            write_edge(logp);
+#pragma unroll 4
+            for (int32_t i = first + tid; i < last; i += LANES) write_vector(i, logp);
+        } else if (piece % run == 0) {                         // uniform in the lanes of a row
+            const int64_t many = run * a.piece_vectors;
+            last = vectors - first < many ? vectors : first + int32_t(many);
             const Finish f(sums_of_row<T, LANES>(x, n, tid, a.scale, joined), a.scale);
-            write([&](float z) { return kLn2 * (f.base.exponent(z, a.scale) - f.l2); });
+            const auto logp = [&](float z) { return kLn2 * (f.base.exponent(z, a.scale) - f.l2); };
+            write_edge(logp);
+#pragma unroll 1
+            for (int32_t i = first + tid; i < last; i += LANES) write_vector(i, logp);
         }
     }
 }

@@ -89,6 +89,20 @@ def test_through_autograd_beside_ordinary_rows_and_in_a_replayed_graph(V):
         assert torch.equal(dz, leaf.grad)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_a_row_so_long_that_its_pieces_are_longer(dtype):
+    """More than 1024 pieces of 8 vectors for each lane."""
+    V = (1 << 24) + 8195 * (1 if dtype == "fp32" else 3)
+    z = torch.randn(2, V, generator=torch.Generator().manual_seed(5)).to(DT[dtype])
+    z[0] = torch.finfo(DT[dtype]).min
+    y, one = torch.tensor([5, V - 1]), torch.ones(2)
+    d, t = z.to(DEV), y.to(DEV)
+    out = rl.token_logprobs_fwd(d, t)
+    dz = rl.token_logprobs_bwd(d, t, None, out[1], out[2], one.to(DEV), one.to(DEV))
+    for i in range(2):
+        gradient_case(z[i:i + 1], y[i:i + 1], 1.0, one[:1], one[:1], dz[i:i + 1])
+
+
 def test_a_tiny_temperature_whose_lse_is_infinite():
     z = torch.tensor([[1.0, 5.0, 2.0, 5.0]])
     y = torch.tensor([1])
